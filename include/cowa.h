@@ -67,9 +67,11 @@ typedef enum {
   COWA_ERR_WORKSPACE = 4,   /* workspace too small or misaligned */
   COWA_ERR_CUDA = 5,        /* CUDA runtime/driver error at launch */
   COWA_ERR_TIMEOUT = 6,     /* a device-side bounded wait ran out */
-  COWA_ERR_CHECK = 7        /* a device-side self-check of a COWA_DEBUG build failed (a planned
+  COWA_ERR_CHECK = 7,       /* a device-side self-check of a COWA_DEBUG build failed (a planned
                                tile or cache row outside the call's tensors); the access was
                                skipped.  Release builds never report it. */
+  COWA_ERR_PAGE = 8         /* the page table entry of a page that holds visible keys lies outside
+                               the pool; those keys were left out */
 } cowa_status;
 
 /* Window parameters of one attention layer.
@@ -305,10 +307,119 @@ cowa_status cowa_decode_noalloc(const cowa_pattern* pat, int B, int H_q, int H_k
  * Copies 4 bytes to the host and allocates nothing. */
 cowa_status cowa_decode_noalloc_status(void* stream);
 
+/* ---- rotary positions -----------------------------------------------------------------------
+ * This and the paged cache below have no counterpart on the CoWA pages: they are what a program
+ * needs directly before and after the attention calls of this library.
+ *
+ * Rotates pairs (a, b) of each head's elements by an angle that depends on the token's position:
+ *   angle(t, i) = pos[axis(i)][t] * inv_freq[i],   i = 0 .. rotary_dim/2 - 1
+ *   (a, b) -> scale * (a cos - b sin, b cos + a sin)
+ * Pair i is elements (i, i + rotary_dim/2), or (2i, 2i+1) if interleaved; elements from rotary_dim on
+ * pass through.  With more than one axis (time, height and width of images and video) the pairs are
+ * dealt out in order: the first section[0] pairs turn with axis 0, the next section[1] with axis 1 ...
+ *   inv_freq    device fp32 [rotary_dim / 2], 4-byte aligned
+ *   rotary_dim  even, 2 .. d
+ *   n_axes      1 .. 4; section[0 .. n_axes) must add up to rotary_dim / 2 (ignored for one axis)
+ *   scale       factor of cos and sin, finite (0 means 1) */
+typedef struct {
+  const float* inv_freq;
+  int32_t rotary_dim;
+  int32_t n_axes;
+  int32_t section[4];
+  int32_t interleaved;
+  float scale;
+} cowa_rotary;
+
+/* Inputs  q [B, N, H_q, d], k [B, N, H_kv, d] (bf16, any cowa_tensor strides); H_q or H_kv may be 0,
+ *         its tensors are then ignored.  positions: device int32, the position of token (b, t) on axis
+ *         a at positions[a * stride_axis + b * stride_b + t] (strides >= 0; any int32 value), or NULL
+ *         for position t on every axis.
+ * Outputs q_out, k_out of the same shapes; each may be its input (in place), but must not overlap the
+ *         inputs in any other way.
+ * Angles are formed in 64 bits and the rotation in 32; the result is rounded once.  cowa_rope_bwd is
+ * the transpose (dq, dk of the rotated q, k in; of the unrotated ones out).  No workspace. */
+cowa_status cowa_rope(const cowa_rotary* rot, int B, int N, int H_q, int H_kv, int d, cowa_tensor q, cowa_tensor k,
+                      cowa_tensor q_out, cowa_tensor k_out, const int32_t* positions, int64_t stride_axis,
+                      int64_t stride_b, void* stream);
+cowa_status cowa_rope_bwd(const cowa_rotary* rot, int B, int N, int H_q, int H_kv, int d, cowa_tensor dq,
+                          cowa_tensor dk, cowa_tensor dq_out, cowa_tensor dk_out, const int32_t* positions,
+                          int64_t stride_axis, int64_t stride_b, void* stream);
+
+/* ---- paged K/V cache ------------------------------------------------------------------------
+ * Keys and values live in a pool of n_pages pages of page_size positions.  Position s of sequence b is
+ * slot s % page_size of page table(b, g, s / page_size).  Either all KV heads of a sequence share its
+ * pages (per_head = 0: the pool is a cowa_tensor over [n_pages, page_size, H_kv, d], its stride_b being
+ * the page stride), or every head has pages of its own (per_head = 1: a pool over [n_pages, page_size,
+ * 1, d], stride_h unused but validated).  With pages of its own a head needs only those that hold its
+ * sink, its interval and its band (cowa_pages_needed): the others' entries may be -1 and their pages
+ * go to other sequences, which is the memory that the position-defined pattern saves in decoding.
+ *   table       device int32, entry (b, g, i) at table[b * stride_b + g * stride_h + i] (strides >= 0;
+ *               stride_h is used with per_head only and must then be > 0)
+ *   max_pages   entries per (b, g); the capacity max_pages * page_size must not exceed 2^30
+ *   page_size   a multiple of 8
+ *   n_pages     pages in the pool
+ * Entries that no call reaches may hold anything.  The pools must not be larger than 2^40 bytes. */
+typedef struct {
+  const int32_t* table;
+  int64_t stride_b, stride_h;
+  int32_t max_pages, page_size, n_pages;
+  int32_t per_head;
+} cowa_page_table;
+
+/* Which pages a head of its own must keep: out[g * n + i] (host memory, H_kv * n bytes) is 1 if page i
+ * holds a position that local KV head g sees from position pos or a later one, or a position past pos,
+ * else 0.  n, page_size >= 1 with n * page_size <= INT_MAX, pos >= 0. */
+cowa_status cowa_pages_needed(const cowa_pattern* pat, int H_kv, int page_size, int n, int pos, uint8_t* out);
+
+/* Writes the tokens of a step into the cache, rotating queries and keys on the way (one launch).
+ * Row i of q [total, H_q, d], k and v [total, H_kv, d] (cowa_tensor strides, stride_b unused but
+ * validated; slices of one packed projection are fine) is the token at position pos[i] of sequence
+ * seq[i] (NULL: sequence i, total <= n_seq):
+ *   q_out row i = rotated q (H_q may be 0: q and q_out are then ignored; q_out may be q)
+ *   the page slots of its position = rotated k, and v
+ * rot NULL: nothing is rotated.  rope_pos: the position of row i on axis a at
+ * rope_pos[a * rope_stride + i], or NULL for pos[i] on every axis.
+ * Rows with pos[i] < 0 or seq[i] outside [0, n_seq) (padding) are left out, q_out included.  Keys and
+ * values whose table entry lies outside [0, n_pages), or whose position lies past the capacity, are
+ * dropped.  No two rows of a call may have the same page slot (which of them it would then hold, or
+ * parts of both, is undefined).  pos, seq, rope_pos: device int32.  No workspace. */
+cowa_status cowa_paged_append(const cowa_rotary* rot, int total, int n_seq, int H_q, int H_kv, int d, cowa_tensor q,
+                              cowa_tensor k, cowa_tensor v, cowa_tensor q_out, const int32_t* pos,
+                              const int32_t* seq, const int32_t* rope_pos, int64_t rope_stride, cowa_tensor k_pages,
+                              cowa_tensor v_pages, cowa_page_table table, void* stream);
+/* The same into pages of E4M3 codes (uint8 pools, byte strides, d = 128): the code of the float32 value x
+ * (a key: rotated in 64 bits and rounded to float32) is that of cowa_quantize_e4m3, a float32 multiply
+ * by the float32 reciprocal of the scale, then round to nearest even, saturating. */
+cowa_status cowa_paged_append_fp8(const cowa_rotary* rot, int total, int n_seq, int H_q, int H_kv, int d,
+                                  cowa_tensor q, cowa_tensor k, cowa_tensor v, cowa_tensor q_out, const int32_t* pos,
+                                  const int32_t* seq, const int32_t* rope_pos, int64_t rope_stride,
+                                  cowa_tensor k_pages, cowa_tensor v_pages, float k_scale, float v_scale,
+                                  cowa_page_table table, void* stream);
+
+/* Decode over the pages: the result of cowa_decode over a contiguous cache with the same keys.
+ * pos[b] < 0 marks a slot without a sequence: its o is 0 and its lse -inf.  Positions past the
+ * capacity are clamped to the last one.  A page with a visible key whose entry lies outside
+ * [0, n_pages) is left out of the softmax and reported as COWA_ERR_PAGE by cowa_workspace_status (a row
+ * with no key left: o 0, lse -inf).  Rows of the pages that are not visible are never used, whatever
+ * they hold.  The workspace's first 256 bytes must be zero before its first call.
+ * Other arguments, ownership and errors as for cowa_decode. */
+size_t cowa_decode_paged_workspace_size(const cowa_pattern* pat, int B, int H_q, int H_kv, int d, int max_pages,
+                                        int page_size);
+cowa_status cowa_decode_paged(const cowa_pattern* pat, int B, int H_q, int H_kv, int d, const void* q_t,
+                              cowa_tensor k_pages, cowa_tensor v_pages, cowa_page_table table, const int32_t* pos,
+                              void* o, float* lse_or_null, void* ws, size_t ws_bytes, void* stream);
+/* Over pages of E4M3 codes (d = 128; scales as for cowa_decode_fp8). */
+size_t cowa_decode_paged_fp8_workspace_size(const cowa_pattern* pat, int B, int H_q, int H_kv, int d, int max_pages,
+                                            int page_size);
+cowa_status cowa_decode_paged_fp8(const cowa_pattern* pat, int B, int H_q, int H_kv, int d, const void* q_t,
+                                  cowa_tensor k_pages, cowa_tensor v_pages, float k_scale, float v_scale,
+                                  cowa_page_table table, const int32_t* pos, void* o, float* lse_or_null, void* ws,
+                                  size_t ws_bytes, void* stream);
+
 /* ---- status --------------------------------------------------------------------------------
  * Synchronizes `stream`, reads and clears the device status word in `ws` (the workspace of an
- * earlier call), and returns COWA_OK, COWA_ERR_TIMEOUT, or (debug builds) COWA_ERR_CHECK
- * (COWA_ERR_CUDA if the stream failed).  A debug build records the first failed self-check in
+ * earlier call), and returns COWA_OK, COWA_ERR_TIMEOUT, COWA_ERR_PAGE (paged calls), or (debug
+ * builds) COWA_ERR_CHECK (COWA_ERR_CUDA if the stream failed).  A debug build records the first failed self-check in
  * the two 32-bit words after the status word (a check code: 0x1nn forward, 0x2nn dK/dV, 0x3nn
  * dQ, 0x4nn decode; and the offending tile index or cache row); they are cleared with it. */
 cowa_status cowa_workspace_status(void* ws, void* stream);

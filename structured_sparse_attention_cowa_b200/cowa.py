@@ -15,12 +15,14 @@ acceptable (a workspace the binding allocates itself is not checked).
 Function names follow the C ABI (include/cowa.h): cowa_fwd, cowa_fwd_chunk,
 cowa_fwd_varlen, cowa_bwd, cowa_bwd_varlen, cowa_decode, cowa_decode_compact (with compact_cache /
 compact_append), the E4M3-cache decodes (cowa_decode_fp8, cowa_decode_fp8_compact, with
-quantize_e4m3, compact_cache_fp8, compact_append_fp8), cowa_decode_noalloc, plus the planner
-introspection helpers.
+quantize_e4m3, compact_cache_fp8, compact_append_fp8), cowa_decode_noalloc, the rotary positions
+(cowa_rope, cowa_rope_bwd), the paged cache (paged_append, cowa_decode_paged, their E4M3 forms
+paged_append_fp8, cowa_decode_paged_fp8, and pages_needed), plus the planner introspection helpers.
 """
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import dataclasses
 import os
@@ -34,7 +36,8 @@ LIB_PATH = os.path.join(_HERE, "libcowa_debug.so" if os.environ.get("COWA_DEBUG"
 
 COWA_OK = 0
 _STATUS = {0: "COWA_OK", 1: "COWA_ERR_INVALID_ARG", 2: "COWA_ERR_UNSUPPORTED", 3: "COWA_ERR_ALIGNMENT",
-           4: "COWA_ERR_WORKSPACE", 5: "COWA_ERR_CUDA", 6: "COWA_ERR_TIMEOUT", 7: "COWA_ERR_CHECK"}
+           4: "COWA_ERR_WORKSPACE", 5: "COWA_ERR_CUDA", 6: "COWA_ERR_TIMEOUT", 7: "COWA_ERR_CHECK",
+           8: "COWA_ERR_PAGE"}
 
 BWD_PREPROCESS, BWD_DKDV, BWD_DQ = 1, 2, 4
 
@@ -54,6 +57,17 @@ class c_pattern(ctypes.Structure):
 class c_tensor(ctypes.Structure):
     _fields_ = [("ptr", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_t", ctypes.c_int64),
                 ("stride_h", ctypes.c_int64)]
+
+
+class c_rotary(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rotary_dim", ctypes.c_int32), ("n_axes", ctypes.c_int32),
+                ("section", ctypes.c_int32 * 4), ("interleaved", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class c_page_table(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_h", ctypes.c_int64),
+                ("max_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+                ("per_head", ctypes.c_int32)]
 
 
 @dataclasses.dataclass(frozen=True)
@@ -139,6 +153,25 @@ def lib() -> ctypes.CDLL:
     L.cowa_decode_fp8_compact_workspace_size.restype = sz
     L.cowa_decode_fp8_compact.argtypes = [P, i, i, i, i, vp, vp, vp, f, f, vp, vp, vp, vp, sz, vp]
     L.cowa_decode_fp8_compact.restype = i
+    R, PT, i64 = ctypes.POINTER(c_rotary), c_page_table, ctypes.c_int64
+    L.cowa_rope.argtypes = [R, i, i, i, i, i, T, T, T, T, vp, i64, i64, vp]
+    L.cowa_rope.restype = i
+    L.cowa_rope_bwd.argtypes = L.cowa_rope.argtypes
+    L.cowa_rope_bwd.restype = i
+    L.cowa_pages_needed.argtypes = [P, i, i, i, i, vp]
+    L.cowa_pages_needed.restype = i
+    L.cowa_paged_append.argtypes = [R, i, i, i, i, i, T, T, T, T, vp, vp, vp, i64, T, T, PT, vp]
+    L.cowa_paged_append.restype = i
+    L.cowa_paged_append_fp8.argtypes = [R, i, i, i, i, i, T, T, T, T, vp, vp, vp, i64, T, T, f, f, PT, vp]
+    L.cowa_paged_append_fp8.restype = i
+    L.cowa_decode_paged_workspace_size.argtypes = [P, i, i, i, i, i, i]
+    L.cowa_decode_paged_workspace_size.restype = sz
+    L.cowa_decode_paged.argtypes = [P, i, i, i, i, vp, T, T, PT, vp, vp, vp, vp, sz, vp]
+    L.cowa_decode_paged.restype = i
+    L.cowa_decode_paged_fp8_workspace_size.argtypes = [P, i, i, i, i, i, i]
+    L.cowa_decode_paged_fp8_workspace_size.restype = sz
+    L.cowa_decode_paged_fp8.argtypes = [P, i, i, i, i, vp, T, T, f, f, PT, vp, vp, vp, vp, sz, vp]
+    L.cowa_decode_paged_fp8.restype = i
     L.cowa_workspace_status.argtypes = [vp, vp]
     L.cowa_workspace_status.restype = i
     L.cowa_status_string.argtypes = [i]
@@ -575,6 +608,271 @@ def cowa_decode_fp8_compact(q_t, kc, vc, pos, pattern: Pattern, k_scale: float, 
                                                                 lse.data_ptr(), workspace.data_ptr(),
                                                                 workspace.numel(), _stream(stream)))
     return out, lse
+
+
+# ---------------------------------------------------------------------------- rotary positions, paged cache
+def _launch_on(x, stream):
+    """Context in which x's device is current and allocations and launches go to `stream` (the
+    device's current stream if None): what a call allocates then belongs to the stream that uses it."""
+    import torch
+
+    if stream is not None:
+        if stream.device != x.device:
+            raise ValueError("stream and tensors are on different devices")
+        return torch.cuda.stream(stream)
+    if torch.cuda.current_device() != x.device.index:
+        return torch.cuda.device(x.device)
+    return contextlib.nullcontext()
+
+
+def _same_device(x, **others):
+    for name, y in others.items():
+        if y is not None and y.device != x.device:
+            raise ValueError(f"{name} is on {y.device}, not on {x.device}")
+
+
+def _int32(name, x, shape):
+    import torch
+
+    if x.dtype != torch.int32 or not x.is_cuda:
+        raise TypeError(f"{name} must be a CUDA int32 tensor")
+    if tuple(x.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(x.shape)}, expected {tuple(shape)}")
+    if x.shape[-1] > 1 and x.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous along its last dimension")
+
+
+_NO_TENSOR = c_tensor(None, 0, 0, 0)
+
+
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, device="cuda"):
+    """inv_freq[i] = base^(-2 i / rotary_dim), i < rotary_dim / 2, float32 on `device`."""
+    import torch
+
+    return (float(base) ** (-torch.arange(0, rotary_dim, 2, dtype=torch.float64) / rotary_dim)).float().to(device)
+
+
+class Rope:
+    """Rotary positions of a layer (cowa_rotary in include/cowa.h): inv_freq, a CUDA float32 tensor of
+    rotary_dim / 2 frequencies; `sections`, how many pairs turn with each position axis (1 to 4 axes,
+    adding up to rotary_dim / 2; default one axis); `interleaved`, pairs (2i, 2i+1) instead of
+    (i, i + rotary_dim/2); `scale`, a factor of cos and sin."""
+
+    def __init__(self, inv_freq, sections=(), interleaved: bool = False, scale: float = 1.0):
+        import torch
+
+        if not (inv_freq.is_cuda and inv_freq.dtype == torch.float32 and inv_freq.dim() == 1
+                and inv_freq.is_contiguous() and inv_freq.numel() > 0):
+            raise TypeError("inv_freq must be a contiguous 1-D CUDA float32 tensor")
+        sections = tuple(int(s) for s in sections) or (inv_freq.numel(),)
+        if len(sections) > 4 or min(sections) < 0 or sum(sections) != inv_freq.numel():
+            raise ValueError("sections: 1 to 4 counts of pairs that add up to the number of frequencies")
+        self.inv_freq, self.sections, self.n_axes = inv_freq, sections, len(sections)
+        self._c = c_rotary(inv_freq.data_ptr(), 2 * inv_freq.numel(), len(sections),
+                           (ctypes.c_int32 * 4)(*sections), int(bool(interleaved)), float(scale))
+
+    def c(self) -> c_rotary:
+        return self._c
+
+
+def _rope(fn, q, k, rope, positions, q_out, k_out, stream):
+    import torch
+
+    if q is None and k is None:
+        raise ValueError("q or k is needed")
+    x = q if q is not None else k
+    B, N, _, d = x.shape
+    for n_, x_, o_ in (("q", q, q_out), ("k", k, k_out)):
+        if x_ is None:
+            continue
+        _bf16_cuda(n_, x_)
+        if x_.dim() != 4 or x_.shape[0] != B or x_.shape[1] != N or x_.shape[3] != d:
+            raise ValueError("q and k are [B, N, H, d] with the same B, N and d")
+        if o_ is not None:
+            _bf16_cuda(n_ + "_out", o_)
+            if o_.shape != x_.shape:
+                raise ValueError(f"{n_}_out must have the shape of {n_}")
+    _same_device(x, k=k, positions=positions, q_out=q_out, k_out=k_out, inv_freq=rope.inv_freq)
+    sa = sb = 0
+    if positions is not None:
+        if positions.dim() == 2 and rope.n_axes == 1:
+            positions = positions.unsqueeze(0)
+        _int32("positions", positions, (rope.n_axes, B, N))
+        sa, sb = positions.stride(0), positions.stride(1)
+    with _launch_on(x, stream):
+        if q is not None and q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if k is not None and k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        t = lambda y: _NO_TENSOR if y is None else _t4(y)
+        _check(fn, getattr(lib(), fn)(ctypes.byref(rope.c()), B, N, 0 if q is None else q.shape[2],
+                                      0 if k is None else k.shape[2], d, t(q), t(k), t(q_out) if q is not None else t(None),
+                                      t(k_out) if k is not None else t(None),
+                                      positions.data_ptr() if positions is not None else None, sa, sb, _stream(None)))
+    return q_out, k_out
+
+
+def cowa_rope(q, k, rope: Rope, positions=None, q_out=None, k_out=None, stream=None):
+    """Rotated (q, k), both [B, N, H, d] bf16 (either may be None): positions CUDA int32 [n_axes, B, N]
+    ([B, N] for one axis; default: t).  q_out, k_out may be q, k."""
+    return _rope("cowa_rope", q, k, rope, positions, q_out, k_out, stream)
+
+
+def cowa_rope_bwd(dq, dk, rope: Rope, positions=None, dq_out=None, dk_out=None, stream=None):
+    """Gradients of q and k from those of the rotated q and k (the transpose of cowa_rope)."""
+    return _rope("cowa_rope_bwd", dq, dk, rope, positions, dq_out, dk_out, stream)
+
+
+def pages_needed(pattern: Pattern, h_kv: int, page_size: int, n_pages: int, pos: int) -> np.ndarray:
+    """bool [h_kv, n_pages]: the pages that hold a key each KV head sees from position pos on, or a
+    position past pos; a head with pages of its own may give the others back."""
+    out = np.zeros((h_kv, n_pages), dtype=np.uint8)
+    _check("cowa_pages_needed", lib().cowa_pages_needed(ctypes.byref(pattern.c()), h_kv, page_size, n_pages, pos,
+                                                        out.ctypes.data_as(ctypes.c_void_p)))
+    return out.astype(bool)
+
+
+def _pages(k_pages, v_pages, page_table, layout, h_kv, d, n_seq=None):
+    """(k, v as cowa_tensor, cowa_page_table) of pools [n_pages, page_size, H, d] ("bthd") or
+    [n_pages, H, page_size, d] ("bhtd"), H = h_kv or, with a table [n_seq, h_kv, max_pages], 1."""
+    import torch
+
+    if layout not in ("bthd", "bhtd"):
+        raise ValueError("layout must be 'bhtd' or 'bthd'")
+    if page_table.dtype != torch.int32 or not page_table.is_cuda:
+        raise TypeError("page_table must be a CUDA int32 tensor")
+    per_head = page_table.dim() == 3
+    ax_t, ax_h = (1, 2) if layout == "bthd" else (2, 1)
+    if page_table.dim() not in (2, 3) or (per_head and page_table.shape[1] != h_kv):
+        raise ValueError("page_table is [n_seq, max_pages] or [n_seq, H_kv, max_pages]")
+    if n_seq is not None and page_table.shape[0] != n_seq:
+        raise ValueError(f"page_table has {page_table.shape[0]} sequences, expected {n_seq}")
+    if page_table.shape[-1] > 1 and page_table.stride(-1) != 1:
+        raise ValueError("page_table must be contiguous along its last dimension")
+    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.shape[3] != d or \
+            k_pages.shape[ax_h] != (1 if per_head else h_kv):
+        raise ValueError("k_pages and v_pages must be pools of this layout, with one head per page if the table is per head")
+    tab = c_page_table(page_table.data_ptr(), page_table.stride(0), page_table.stride(1) if per_head else 0,
+                       page_table.shape[-1], k_pages.shape[ax_t], k_pages.shape[0], int(per_head))
+    return _cache_tensor(k_pages, layout), _cache_tensor(v_pages, layout), tab
+
+
+def _paged_append(fn, q, k, v, pos, k_pages, v_pages, page_table, rope, seq, rope_pos, q_out, layout, scales, stream):
+    import torch
+
+    total, Hkv, d = k.shape
+    for n_, x_ in (("q", q), ("k", k), ("v", v), ("q_out", q_out)):
+        if x_ is not None:
+            _bf16_cuda(n_, x_)
+    if v.shape != k.shape or (q is not None and (q.dim() != 3 or q.shape[0] != total or q.shape[2] != d)):
+        raise ValueError("q is [total, H_q, d], k and v are [total, H_kv, d]")
+    if q is not None and q_out is not None and q_out.shape != q.shape:
+        raise ValueError("q_out must have the shape of q")
+    _int32("pos", pos, (total,))
+    if seq is not None:
+        _int32("seq", seq, (total,))
+    if rope_pos is not None:
+        if rope is None:
+            raise ValueError("rope_pos without rope")
+        if rope_pos.dim() == 1 and rope.n_axes == 1:
+            rope_pos = rope_pos.unsqueeze(0)
+        _int32("rope_pos", rope_pos, (rope.n_axes, total))
+    _same_device(k, q=q, v=v, pos=pos, seq=seq, rope_pos=rope_pos, q_out=q_out, k_pages=k_pages, v_pages=v_pages,
+                 page_table=page_table, inv_freq=None if rope is None else rope.inv_freq)
+    kp, vp, tab = _pages(k_pages, v_pages, page_table, layout, Hkv, d)
+    with _launch_on(k, stream):
+        if q is not None and q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        t = lambda y: _NO_TENSOR if y is None else _t4(y.unsqueeze(0))
+        ptr = lambda y: None if y is None else y.data_ptr()
+        _check(fn, getattr(lib(), fn)(None if rope is None else ctypes.byref(rope.c()), total, page_table.shape[0],
+                                      0 if q is None else q.shape[1], Hkv, d, t(q), t(k), t(v),
+                                      t(q_out) if q is not None else t(None), pos.data_ptr(), ptr(seq), ptr(rope_pos),
+                                      0 if rope_pos is None else rope_pos.stride(0), kp, vp, *scales, tab, _stream(None)))
+    return q_out if q is not None else None
+
+
+def paged_append(q, k, v, pos, k_pages, v_pages, page_table, rope: Rope = None, seq=None, rope_pos=None, q_out=None,
+                 layout: str = "bthd", stream=None):
+    """Writes the tokens of a step into a paged cache in place and returns the rotated queries.
+
+    Row i of q [total, H_q, d] (may be None), k and v [total, H_kv, d] is the token at position pos[i]
+    of sequence seq[i] (default i); rope None rotates nothing; rope_pos [n_axes, total] defaults to pos.
+    k_pages, v_pages: [n_pages, page_size, H_kv, d] (layout "bthd") or [n_pages, H_kv, page_size, d]
+    ("bhtd") with page_table [n_seq, max_pages], or one head per page (H_kv replaced by 1) with
+    page_table [n_seq, H_kv, max_pages].  Rows with pos < 0 are left out (q_out too); keys and values
+    without a page are dropped."""
+    for n_, x_ in (("k_pages", k_pages), ("v_pages", v_pages)):
+        _bf16_cuda(n_, x_)
+    return _paged_append("cowa_paged_append", q, k, v, pos, k_pages, v_pages, page_table, rope, seq, rope_pos, q_out,
+                         layout, (), stream)
+
+
+def paged_append_fp8(q, k, v, pos, k_pages, v_pages, page_table, k_scale: float, v_scale: float, rope: Rope = None,
+                     seq=None, rope_pos=None, q_out=None, layout: str = "bthd", stream=None):
+    """paged_append into pages of E4M3 codes (uint8, d = 128), quantised as by quantize_e4m3."""
+    _u8_cuda("k_pages", k_pages)
+    _u8_cuda("v_pages", v_pages)
+    return _paged_append("cowa_paged_append_fp8", q, k, v, pos, k_pages, v_pages, page_table, rope, seq, rope_pos,
+                         q_out, layout, (float(k_scale), float(v_scale)), stream)
+
+
+def _decode_paged(fn, q_t, k_pages, v_pages, page_table, pos, pattern, scales, layout, out, lse, workspace, stream,
+                  want_lse):
+    import torch
+
+    _bf16_cuda("q_t", q_t)
+    B, Hq, d = q_t.shape
+    if not q_t.is_contiguous():
+        raise ValueError("q_t must be contiguous [B, H_q, d]")
+    if layout not in ("bthd", "bhtd") or k_pages.dim() != 4 or page_table.dim() not in (2, 3):
+        raise ValueError("k_pages is 4-D in layout 'bthd' or 'bhtd', page_table [B, max_pages] or [B, H_kv, max_pages]")
+    Hkv = page_table.shape[1] if page_table.dim() == 3 else k_pages.shape[2 if layout == "bthd" else 1]
+    kp, vp, tab = _pages(k_pages, v_pages, page_table, layout, Hkv, d, B)
+    _int32("pos", pos, (B,))
+    if out is not None:
+        _bf16_cuda("out", out)
+        if out.shape != q_t.shape or not out.is_contiguous():
+            raise ValueError("out must be contiguous [B, H_q, d]")
+    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (B, Hq) or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous float32 [B, H_q] tensor")
+    _same_device(q_t, k_pages=k_pages, v_pages=v_pages, page_table=page_table, pos=pos, out=out, lse=lse,
+                 workspace=workspace)
+    pat = pattern.c()
+    L = lib()
+    with _launch_on(q_t, stream):
+        if out is None:
+            out = torch.empty((B, Hq, d), dtype=torch.bfloat16, device=q_t.device)
+        if lse is None and want_lse:
+            lse = torch.empty((B, Hq), dtype=torch.float32, device=q_t.device)
+        if workspace is None:
+            workspace = _workspace(getattr(L, fn + "_workspace_size")(ctypes.byref(pat), B, Hq, Hkv, d, tab.max_pages,
+                                                                      tab.page_size), q_t.device)
+        _check(fn, getattr(L, fn)(ctypes.byref(pat), B, Hq, Hkv, d, q_t.data_ptr(), kp, vp, *scales, tab,
+                                  pos.data_ptr(), out.data_ptr(), lse.data_ptr() if lse is not None else None,
+                                  workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(None)))
+    return out, lse
+
+
+def cowa_decode_paged(q_t, k_pages, v_pages, page_table, pos, pattern: Pattern, layout: str = "bthd", out=None,
+                      lse=None, workspace=None, stream=None, want_lse: bool = True):
+    """o [B, H_q, d] bf16 (and lse [B, H_q] fp32) for one new token per sequence at pos[b] over a paged
+    cache (pools and page_table as for paged_append).  pos[b] < 0: no sequence, o = 0 and lse = -inf."""
+    for n_, x_ in (("k_pages", k_pages), ("v_pages", v_pages)):
+        _bf16_cuda(n_, x_)
+    return _decode_paged("cowa_decode_paged", q_t, k_pages, v_pages, page_table, pos, pattern, (), layout, out, lse,
+                         workspace, stream, want_lse)
+
+
+def cowa_decode_paged_fp8(q_t, k_pages, v_pages, page_table, pos, pattern: Pattern, k_scale: float, v_scale: float,
+                          layout: str = "bthd", out=None, lse=None, workspace=None, stream=None,
+                          want_lse: bool = True):
+    """cowa_decode_paged over pages of E4M3 codes (uint8, d = 128): keys k_scale * e4m3(code), values
+    v_scale * e4m3(code)."""
+    _u8_cuda("k_pages", k_pages)
+    _u8_cuda("v_pages", v_pages)
+    return _decode_paged("cowa_decode_paged_fp8", q_t, k_pages, v_pages, page_table, pos, pattern,
+                         (float(k_scale), float(v_scale)), layout, out, lse, workspace, stream, want_lse)
 
 
 def decode_noalloc_status(stream=None) -> int:

@@ -143,6 +143,7 @@ const char* cowa_status_string(cowa_status s) {
     case COWA_ERR_CUDA: return "CUDA error";
     case COWA_ERR_TIMEOUT: return "a device-side bounded wait ran out";
     case COWA_ERR_CHECK: return "a device-side self-check of the debug build failed";
+    case COWA_ERR_PAGE: return "a visible page's table entry lies outside the pool";
   }
   return "unknown status";
 }
@@ -150,14 +151,16 @@ const char* cowa_status_string(cowa_status s) {
 cowa_status cowa_workspace_status(void* ws, void* stream) {
   if (!ws) return COWA_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  uint32_t word = 0;
-  if (cudaMemcpyAsync(&word, ws, sizeof(word), cudaMemcpyDeviceToHost, s) != cudaSuccess) return COWA_ERR_CUDA;
+  uint32_t word[4] = {0, 0, 0, 0};
+  if (cudaMemcpyAsync(word, ws, sizeof(word), cudaMemcpyDeviceToHost, s) != cudaSuccess) return COWA_ERR_CUDA;
   if (cudaStreamSynchronize(s) != cudaSuccess) return COWA_ERR_CUDA;
-  if (word != 0) {
-    // clear the status word and the self-check record (words 1 and 2) for the next call
-    if (cudaMemsetAsync(ws, 0, 3 * sizeof(word), s) != cudaSuccess) return COWA_ERR_CUDA;
+  if (word[0] != 0 || word[3] != 0) {
+    // clear the status word, the self-check record (words 1 and 2) and the bad-page flag (word 3)
+    // for the next call
+    if (cudaMemsetAsync(ws, 0, sizeof(word), s) != cudaSuccess) return COWA_ERR_CUDA;
     if (cudaStreamSynchronize(s) != cudaSuccess) return COWA_ERR_CUDA;
-    return (word & 2u) ? COWA_ERR_CHECK : COWA_ERR_TIMEOUT;
+    if (word[0] == 0) return COWA_ERR_PAGE;
+    return (word[0] & 2u) ? COWA_ERR_CHECK : COWA_ERR_TIMEOUT;
   }
   return COWA_OK;
 }
@@ -649,6 +652,241 @@ cowa_status cowa_bwd_varlen(const cowa_pattern* pat, int n_seq, int total, int H
   if (launch_seq_table(cu_seqlens, n_seq, total, a.seq_tab, st) != cudaSuccess) return COWA_ERR_CUDA;
   return launch_bwd(a, COWA_BWD_PREPROCESS | COWA_BWD_DKDV | COWA_BWD_DQ, st) == cudaSuccess ? COWA_OK
                                                                                             : COWA_ERR_CUDA;
+}
+
+// ------------------------------------------------------------------------------ rotary positions
+namespace {
+// Rotation part of the arguments; a null rot rotates nothing.
+cowa_status check_rotary(const cowa_rotary* rot, int d, bool transpose, RopeArgs* a) {
+  a->scale = 1.f;
+  if (!rot) return COWA_OK;
+  const int r = rot->rotary_dim;
+  if (!rot->inv_freq || r < 2 || r > d || r % 2 != 0 || rot->n_axes < 1 || rot->n_axes > 4 || !isfinite(rot->scale))
+    return COWA_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(rot->inv_freq) & 3u) return COWA_ERR_ALIGNMENT;
+  a->inv_freq = rot->inv_freq;
+  a->half = r / 2;
+  int end[3] = {r / 2, r / 2, r / 2}, sum = 0;
+  if (rot->n_axes > 1) {
+    for (int x = 0; x < rot->n_axes; ++x) {
+      if (rot->section[x] < 0 || rot->section[x] > r / 2 - sum) return COWA_ERR_INVALID_ARG;
+      sum += rot->section[x];
+      if (x + 1 < rot->n_axes) end[x] = sum;
+    }
+    if (sum != r / 2) return COWA_ERR_INVALID_ARG;
+  }
+  a->end0 = end[0]; a->end1 = end[1]; a->end2 = end[2];
+  a->interleaved = rot->interleaved != 0;
+  a->scale = rot->scale == 0.f ? 1.f : rot->scale;
+  a->sin_scale = transpose ? -a->scale : a->scale;
+  return COWA_OK;
+}
+
+const __nv_bfloat16* in_ptr(const cowa_tensor& t) { return static_cast<const __nv_bfloat16*>(t.ptr); }
+__nv_bfloat16* out_ptr(const cowa_tensor& t) { return static_cast<__nv_bfloat16*>(t.ptr); }
+
+cowa_status rope(const cowa_rotary* rot, bool transpose, int B, int N, int Hq, int Hkv, int d, const cowa_tensor& q,
+                 const cowa_tensor& k, const cowa_tensor& qo, const cowa_tensor& ko, const int32_t* positions,
+                 int64_t stride_axis, int64_t stride_b, void* stream) {
+  if (!rot || B < 1 || N < 1 || Hq < 0 || Hkv < 0 || Hq + (int64_t)Hkv < 1 || Hq + (int64_t)Hkv > 0x3fffffff)
+    return COWA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return COWA_ERR_UNSUPPORTED;
+  RopeArgs a;
+  memset(&a, 0, sizeof(a));
+  COWA_TRY(check_rotary(rot, d, transpose, &a));
+  if (Hq > 0) {
+    COWA_TRY(check_tensor(q));
+    COWA_TRY(check_tensor(qo));
+  }
+  if (Hkv > 0) {
+    COWA_TRY(check_tensor(k));
+    COWA_TRY(check_tensor(ko));
+  }
+  if (positions && (stride_axis < 0 || stride_b < 0)) return COWA_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(positions) & 3u) return COWA_ERR_ALIGNMENT;
+  a.pos = positions; a.pos_sa = stride_axis; a.pos_sb = stride_b;
+  a.M = (long long)B * N; a.N = N; a.d = d; a.Hq = Hq; a.Hk = Hkv;
+  a.q = in_ptr(q); a.q_sb = q.stride_b; a.q_st = q.stride_t; a.q_sh = q.stride_h;
+  a.k = in_ptr(k); a.k_sb = k.stride_b; a.k_st = k.stride_t; a.k_sh = k.stride_h;
+  a.qo = out_ptr(qo); a.qo_sb = qo.stride_b; a.qo_st = qo.stride_t; a.qo_sh = qo.stride_h;
+  a.ko = out_ptr(ko); a.ko_sb = ko.stride_b; a.ko_st = ko.stride_t; a.ko_sh = ko.stride_h;
+  return launch_rope(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? COWA_OK : COWA_ERR_CUDA;
+}
+}  // namespace
+
+cowa_status cowa_rope(const cowa_rotary* rot, int B, int N, int H_q, int H_kv, int d, cowa_tensor q, cowa_tensor k,
+                      cowa_tensor q_out, cowa_tensor k_out, const int32_t* positions, int64_t stride_axis,
+                      int64_t stride_b, void* stream) {
+  return rope(rot, false, B, N, H_q, H_kv, d, q, k, q_out, k_out, positions, stride_axis, stride_b, stream);
+}
+
+cowa_status cowa_rope_bwd(const cowa_rotary* rot, int B, int N, int H_q, int H_kv, int d, cowa_tensor dq,
+                          cowa_tensor dk, cowa_tensor dq_out, cowa_tensor dk_out, const int32_t* positions,
+                          int64_t stride_axis, int64_t stride_b, void* stream) {
+  return rope(rot, true, B, N, H_q, H_kv, d, dq, dk, dq_out, dk_out, positions, stride_axis, stride_b, stream);
+}
+
+// ------------------------------------------------------------------------------ paged cache
+namespace {
+cowa_status check_page_table(const cowa_page_table& t, int n_seq, PageTab* out) {
+  if (!t.table || t.stride_b < 0 || t.max_pages < 1 || t.n_pages < 1 || t.page_size < 8 || t.page_size % 8 != 0 ||
+      (int64_t)t.max_pages * t.page_size > (1 << 30) || (t.per_head && t.stride_h <= 0))
+    return COWA_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(t.table) & 3u) return COWA_ERR_ALIGNMENT;
+  out->ptr = t.table; out->sb = t.stride_b; out->sh = t.per_head ? t.stride_h : 0;
+  out->max_pages = t.max_pages; out->page_size = t.page_size; out->n_pages = t.n_pages; out->n_seq = n_seq;
+  return COWA_OK;
+}
+
+// rows of a TMA box: the largest power of two up to `most` that divides the page size (>= 8)
+int page_box_rows(int page_size, int most) {
+  int r = most;
+  while (page_size % r != 0) r /= 2;
+  return r;
+}
+
+cowa_status paged_append(const cowa_rotary* rot, int total, int n_seq, int Hq, int Hkv, int d, const cowa_tensor& q,
+                         const cowa_tensor& k, const cowa_tensor& v, const cowa_tensor& qo, const int32_t* pos,
+                         const int32_t* seq, const int32_t* rope_pos, int64_t rope_stride, const cowa_tensor& kp,
+                         const cowa_tensor& vp, bool e4m3, float k_scale, float v_scale, const cowa_page_table& table,
+                         void* stream) {
+  if (total < 1 || n_seq < 1 || Hq < 0 || Hq > 0x1fffffff || Hkv < 1 || !pos || (!seq && total > n_seq))
+    return COWA_ERR_INVALID_ARG;
+  if ((d != 64 && d != 128) || (e4m3 && d != 128) || Hkv > 1024) return COWA_ERR_UNSUPPORTED;
+  if (e4m3 && (!(k_scale > 0.f) || !(v_scale > 0.f) || !isfinite(k_scale) || !isfinite(v_scale)))
+    return COWA_ERR_INVALID_ARG;
+  RopeArgs a;
+  memset(&a, 0, sizeof(a));
+  COWA_TRY(check_rotary(rot, d, false, &a));
+  if (Hq > 0) {
+    COWA_TRY(check_tensor(q));
+    COWA_TRY(check_tensor(qo));
+  }
+  COWA_TRY(check_tensor(k));
+  COWA_TRY(check_tensor(v));
+  COWA_TRY(e4m3 ? check_tensor8(kp) : check_tensor(kp));
+  COWA_TRY(e4m3 ? check_tensor8(vp) : check_tensor(vp));
+  COWA_TRY(check_page_table(table, n_seq, &a.tab));
+  if (rope_pos && rope_stride < 0) return COWA_ERR_INVALID_ARG;
+  for (const int32_t* x : {pos, seq, rope_pos})
+    if (reinterpret_cast<uintptr_t>(x) & 3u) return COWA_ERR_ALIGNMENT;
+  a.pos = rope_pos; a.pos_sa = rope_stride;
+  a.cache_pos = pos; a.seq = seq;
+  a.M = total; a.N = total; a.d = d; a.Hq = Hq; a.Hk = Hkv;
+  a.q = in_ptr(q); a.q_st = q.stride_t; a.q_sh = q.stride_h;
+  a.k = in_ptr(k); a.k_st = k.stride_t; a.k_sh = k.stride_h;
+  a.v = in_ptr(v); a.v_st = v.stride_t; a.v_sh = v.stride_h;
+  a.qo = out_ptr(qo); a.qo_st = qo.stride_t; a.qo_sh = qo.stride_h;
+  a.kp = kp.ptr; a.kp_sp = kp.stride_b; a.kp_st = kp.stride_t; a.kp_sh = kp.stride_h;
+  a.vp = vp.ptr; a.vp_sp = vp.stride_b; a.vp_st = vp.stride_t; a.vp_sh = vp.stride_h;
+  if (e4m3) { a.inv_k = 1.0f / k_scale; a.inv_v = 1.0f / v_scale; }
+  return launch_paged_append(a, e4m3, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? COWA_OK : COWA_ERR_CUDA;
+}
+
+size_t paged_workspace(const cowa_pattern* pat, int B, int Hq, int Hkv, int d, bool e4m3, int max_pages,
+                       int page_size) {
+  Pat p;
+  if (check_pattern(pat, Hkv, &p) != COWA_OK || check_heads(B, 1, Hq, Hkv, d) != COWA_OK || (e4m3 && d != 128) ||
+      max_pages < 1 || page_size < 8 || page_size % 8 != 0 || (int64_t)max_pages * page_size > (1 << 30))
+    return 0;
+  return kWsHeader + paged_decode_bytes(paged_decode_grid(p, B, Hq, Hkv, d, e4m3, max_pages, page_size), Hq / Hkv, d);
+}
+
+cowa_status decode_paged(const cowa_pattern* pat, int B, int Hq, int Hkv, int d, const void* q_t, const cowa_tensor& kp,
+                         const cowa_tensor& vp, bool e4m3, float k_scale, float v_scale, const cowa_page_table& table,
+                         const int32_t* pos, void* o, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  Pat p;
+  COWA_TRY(check_pattern(pat, Hkv, &p));
+  COWA_TRY(check_heads(B, 1, Hq, Hkv, d));
+  if ((int64_t)B * Hkv > 0x3fffffff) return COWA_ERR_INVALID_ARG;
+  if (e4m3 && d != 128) return COWA_ERR_UNSUPPORTED;
+  if (!q_t || !pos || !o) return COWA_ERR_INVALID_ARG;
+  if (e4m3 && (!(k_scale > 0.f) || !(v_scale > 0.f) || !isfinite(k_scale) || !isfinite(v_scale)))
+    return COWA_ERR_INVALID_ARG;
+  COWA_TRY(e4m3 ? check_tensor8(kp) : check_tensor(kp));
+  COWA_TRY(e4m3 ? check_tensor8(vp) : check_tensor(vp));
+  PagedDecodeArgs a;
+  memset(&a, 0, sizeof(a));
+  COWA_TRY(check_page_table(table, B, &a.tab));
+  if (!aligned16(q_t) || !aligned16(o) || (reinterpret_cast<uintptr_t>(pos) & 3u) ||
+      (reinterpret_cast<uintptr_t>(lse) & 3u))
+    return COWA_ERR_ALIGNMENT;
+  COWA_TRY(check_ws(ws, ws_bytes, paged_workspace(pat, B, Hq, Hkv, d, e4m3, table.max_pages, table.page_size)));
+  a.pat = p; a.B = B; a.Hkv = Hkv; a.grp = Hq / Hkv;
+  a.q_t = q_t; a.pos = pos; a.o = o; a.lse = lse;
+  a.status = reinterpret_cast<uint32_t*>(ws);
+  a.grid = paged_decode_grid(p, B, Hq, Hkv, d, e4m3, table.max_pages, table.page_size);
+  a.rec = reinterpret_cast<int4*>(reinterpret_cast<char*>(ws) + kWsHeader);
+  a.part = reinterpret_cast<float*>(reinterpret_cast<char*>(a.rec) + align_up((size_t)a.grid * sizeof(int4), 256));
+  a.scale_log2 = scale_of(pat, d) * 1.4426950408889634f * (e4m3 ? k_scale : 1.f);
+  a.v_scale = v_scale;
+  a.box_rows = page_box_rows(table.page_size, 64);
+  const int h = table.per_head ? 1 : Hkv;
+  auto map = e4m3 ? make_tmap_u8 : make_tmap_bf16;
+  if (!map(&a.tm_k, kp.ptr, d, table.page_size, h, table.n_pages, kp.stride_t, kp.stride_h, kp.stride_b, a.box_rows) ||
+      !map(&a.tm_v, vp.ptr, d, table.page_size, h, table.n_pages, vp.stride_t, vp.stride_h, vp.stride_b, a.box_rows))
+    return COWA_ERR_CUDA;
+  return launch_paged_decode(a, d, e4m3, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? COWA_OK
+                                                                                                : COWA_ERR_CUDA;
+}
+}  // namespace
+
+cowa_status cowa_pages_needed(const cowa_pattern* pat, int Hkv, int page_size, int n, int pos, uint8_t* out) {
+  Pat p;
+  if (Hkv < 1) return COWA_ERR_INVALID_ARG;
+  COWA_TRY(check_pattern(pat, Hkv, &p));
+  if (page_size < 1 || n < 1 || pos < 0 || !out || (int64_t)n * page_size > 0x7fffffffLL) return COWA_ERR_INVALID_ARG;
+  for (int g = 0; g < Hkv; ++g) {
+    const Range iv = interval_of(p, g);
+    for (int i = 0; i < n; ++i) {
+      const int64_t lo = (int64_t)i * page_size, hi = lo + page_size;
+      const bool band = hi - 1 > (int64_t)pos - p.L;  // the band only moves on from here
+      out[(size_t)g * n + i] = lo < p.S || band || (iv.lo < hi && iv.hi > lo && iv.lo < iv.hi);
+    }
+  }
+  return COWA_OK;
+}
+
+cowa_status cowa_paged_append(const cowa_rotary* rot, int total, int n_seq, int H_q, int H_kv, int d, cowa_tensor q,
+                              cowa_tensor k, cowa_tensor v, cowa_tensor q_out, const int32_t* pos,
+                              const int32_t* seq, const int32_t* rope_pos, int64_t rope_stride, cowa_tensor k_pages,
+                              cowa_tensor v_pages, cowa_page_table table, void* stream) {
+  return paged_append(rot, total, n_seq, H_q, H_kv, d, q, k, v, q_out, pos, seq, rope_pos, rope_stride, k_pages,
+                      v_pages, false, 1.f, 1.f, table, stream);
+}
+
+cowa_status cowa_paged_append_fp8(const cowa_rotary* rot, int total, int n_seq, int H_q, int H_kv, int d,
+                                  cowa_tensor q, cowa_tensor k, cowa_tensor v, cowa_tensor q_out, const int32_t* pos,
+                                  const int32_t* seq, const int32_t* rope_pos, int64_t rope_stride,
+                                  cowa_tensor k_pages, cowa_tensor v_pages, float k_scale, float v_scale,
+                                  cowa_page_table table, void* stream) {
+  return paged_append(rot, total, n_seq, H_q, H_kv, d, q, k, v, q_out, pos, seq, rope_pos, rope_stride, k_pages,
+                      v_pages, true, k_scale, v_scale, table, stream);
+}
+
+size_t cowa_decode_paged_workspace_size(const cowa_pattern* pat, int B, int H_q, int H_kv, int d, int max_pages,
+                                        int page_size) {
+  return paged_workspace(pat, B, H_q, H_kv, d, false, max_pages, page_size);
+}
+
+cowa_status cowa_decode_paged(const cowa_pattern* pat, int B, int H_q, int H_kv, int d, const void* q_t,
+                              cowa_tensor k_pages, cowa_tensor v_pages, cowa_page_table table, const int32_t* pos,
+                              void* o, float* lse_or_null, void* ws, size_t ws_bytes, void* stream) {
+  return decode_paged(pat, B, H_q, H_kv, d, q_t, k_pages, v_pages, false, 1.f, 1.f, table, pos, o, lse_or_null, ws,
+                      ws_bytes, stream);
+}
+
+size_t cowa_decode_paged_fp8_workspace_size(const cowa_pattern* pat, int B, int H_q, int H_kv, int d, int max_pages,
+                                            int page_size) {
+  return paged_workspace(pat, B, H_q, H_kv, d, true, max_pages, page_size);
+}
+
+cowa_status cowa_decode_paged_fp8(const cowa_pattern* pat, int B, int H_q, int H_kv, int d, const void* q_t,
+                                  cowa_tensor k_pages, cowa_tensor v_pages, float k_scale, float v_scale,
+                                  cowa_page_table table, const int32_t* pos, void* o, float* lse_or_null, void* ws,
+                                  size_t ws_bytes, void* stream) {
+  return decode_paged(pat, B, H_q, H_kv, d, q_t, k_pages, v_pages, true, k_scale, v_scale, table, pos, o, lse_or_null,
+                      ws, ws_bytes, stream);
 }
 
 // ------------------------------------------------------------------------------ introspection

@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -64,6 +65,61 @@ cudaError_t launch_compact_append(const Pat& p, int B, int Hkv, int d, const voi
 cudaError_t launch_compact_build(const Pat& p, int B, int N, int Hkv, int d, const void* k, int64_t ksb, int64_t kst,
                                  int64_t ksh, const void* v, int64_t vsb, int64_t vst, int64_t vsh, void* kc, void* vc,
                                  cudaStream_t s);
+
+// ---- paged cache ----
+// Entry (b, g, i): the page that holds positions [i * page_size, (i + 1) * page_size) of sequence b
+// (and KV head g); per head tables have sh > 0 and pages of one head, shared ones sh = 0.
+struct PageTab {
+  const int32_t* ptr;
+  int64_t sb, sh;
+  int max_pages, page_size, n_pages, n_seq;
+};
+struct PagedDecodeArgs {
+  Pat pat;
+  int B, Hkv, grp;   // grp: query heads per KV head
+  PageTab tab;
+  const void* q_t;
+  const int32_t* pos;
+  void* o;
+  float* lse;        // may be null
+  uint32_t* status;  // word 3: a visible page's entry was outside the pool
+  int4* rec;         // [grid]: {b, g, last CTA} of the pair that begins in CTA c and does not end there; x = -1: none
+  float* part;       // [2 grid][grp][d + 2] fp32 partials: m, l, o
+  float scale_log2, v_scale;
+  int grid;
+  int box_rows;      // rows per TMA box: the largest power of two up to 64 that divides the page size
+  CUtensorMap tm_k, tm_v;
+};
+int paged_decode_grid(const Pat& p, int B, int Hq, int Hkv, int d, bool kv8, int max_pages, int page_size);
+size_t paged_decode_bytes(int grid, int grp, int d);
+cudaError_t launch_paged_decode(const PagedDecodeArgs& a, int d, bool kv8, cudaStream_t s);
+
+// ---- rotary positions, and the write of tokens into a paged cache ----
+struct RopeArgs {
+  const float* inv_freq;           // [half]
+  int half;                        // pairs; 2 * half elements of a head are rotated
+  int end0, end1, end2;            // first pair of axes 1, 2, 3
+  int interleaved;
+  float scale, sin_scale;          // factors of cos and sin (the backward pass negates the second)
+  const int32_t* pos;              // position of token t of batch b on an axis; null: t (append: cache_pos)
+  int64_t pos_sa, pos_sb;
+  long long M;                     // tokens
+  int N;                           // per batch element
+  int d, Hq, Hk;
+  const __nv_bfloat16 *q, *k, *v;
+  int64_t q_sb, q_st, q_sh, k_sb, k_st, k_sh, v_st, v_sh;
+  __nv_bfloat16 *qo, *ko;
+  int64_t qo_sb, qo_st, qo_sh, ko_sb, ko_st, ko_sh;
+  // append
+  const int32_t* cache_pos;
+  const int32_t* seq;              // null: token i belongs to sequence i
+  PageTab tab;
+  void *kp, *vp;
+  int64_t kp_sp, kp_st, kp_sh, vp_sp, vp_st, vp_sh;
+  float inv_k, inv_v;              // E4M3: reciprocals of the scales
+};
+cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s);
+cudaError_t launch_paged_append(const RopeArgs& a, bool e4m3, cudaStream_t s);
 
 // ---- forward ----
 struct FwdArgs {

@@ -1,0 +1,595 @@
+// cowa_paged.cu -- decode over a paged K/V cache: one new query token per sequence attends to the
+// keys its KV head can see ("CoWindow Attention: Full Causal Coverage Is a Collective Property",
+// Abstract: the same position-defined pattern in training and decoding), the rows of position s
+// being found in page table[b (, g)][s / page_size] at slot s % page_size.
+//
+//   o = sum_s p_s v_s / sum_s p_s,   p_s = 2^(scale log2(e) q.k_s - m),   s over the visible set
+//
+// HBM-bound: each visible K and V row is read once.  What the kernel is built around:
+//   * The work is the list of 64-position tiles of all (sequence, KV head) pairs, in that order.
+//     Lengths are known on the device only, and differ from 1 to the whole cache, so every CTA adds up
+//     the tile counts itself (integer arithmetic on pos) and takes an equal, contiguous share of the
+//     list.  A pair that lies inside one CTA's share is finished there; one that several CTAs share
+//     leaves fp32 partials (at most two per CTA), which a second kernel joins in order.
+//   * A producer warp looks up the pages (one lane per box of 8 to 64 rows, one tile ahead of the
+//     copies) and streams K and V tiles into a shared-memory ring with TMA; boxes that hold no
+//     visible key are not fetched.
+//   * 4 compute warps each take 16 tokens of a tile.  Tokens are the 16 rows of the warp MMAs
+//     (m16n8k16) and the query heads of the group (at most 8) their 8 columns, so no MMA row is
+//     wasted: S^T = K Q^T and O^T += V^T P^T, the scores turned into the P^T operand with two 8x8
+//     transposes.  Each thread owns two heads, so the running maxima are compared without shuffles;
+//     only a growth past 2^8 makes the warp reduce and rescale.
+//   * Masked tokens are selected away in the scores and cleared in V, so what stands in unseen rows
+//     (infinities, NaN) does not matter.
+#include <cuda_bf16.h>
+#include <math.h>
+
+#include "cowa_internal.h"
+#include "sm100_ptx.cuh"
+
+namespace cowa {
+namespace {
+
+constexpr int kWarps = 4;                      // compute warps
+constexpr int kThreads = (kWarps + 1) * 32;    // + the producer
+constexpr int kTok = 64;                       // positions per tile
+constexpr int kBoxBytes = kTok * 128;          // 64 rows x 128 bytes
+constexpr float kRescale = 8.0f;               // lazy-rescale threshold, log2 units
+// E4M3: P is rounded to f16, whose smallest normal number is 2^-14; relative to a running maximum
+// lifted by 2^6 (P at most 2^14) it covers P down to 2^-20 of the largest at full precision.
+template <bool KV8>
+constexpr float kLift = KV8 ? 6.0f : 0.0f;
+
+template <int D, bool KV8>
+struct Geo {
+  static_assert(!KV8 || D == 128, "E4M3 rows are whole 128-byte rows");
+  static constexpr int kBarBytes = 256;  // 3 words per stage, then a few of the block's own
+  static constexpr int kUnits = KV8 ? 1 : D / 64;  // 128-byte columns of a row
+  static constexpr int kTileBytes = kUnits * kBoxBytes;
+  static constexpr int kStages = KV8 ? 4 : (D == 128 ? 3 : 5);
+  static constexpr int kCtas = KV8 ? 3 : 2;        // per SM, what the ring leaves room for
+  static constexpr int kOffBar = kStages * 2 * kTileBytes;
+  static_assert(3 * kStages <= 16, "the block's own words start at word 16");
+  static constexpr int kOffRed = kOffBar + kBarBytes;
+  static int smem(int grp) { return kOffRed + kWarps * grp * (D + 2) * 4; }
+  // of an SM's 228 KB a block takes its shared memory and 1 KB more
+  static int ctas(int grp) { return imin(kCtas, (228 * 1024) / (smem(grp) + 1024)); }
+};
+
+// the (sequence, KV head) pair `item`: its visible ranges at pos[b] and their 64-position tiles
+struct Pair {
+  int b, g, n;
+  int lo0, hi0, lo1, hi1, lo2, hi2;  // visible ranges, sorted and disjoint (empty: hi <= lo)
+  int n0, n1;                        // tiles of the first two
+  __device__ __forceinline__ void tile(int i, int& base, int& lo, int& hi) const {
+    int first = lo0 / kTok;
+    lo = lo0; hi = hi0;
+    if (i >= n0) {
+      i -= n0;
+      lo = lo1; hi = hi1;
+      if (i >= n1) { i -= n1; lo = lo2; hi = hi2; }
+      first = lo / kTok;
+    }
+    base = (first + i) * kTok;
+    lo = imax(lo, base);
+    hi = imin(hi, base + kTok);
+  }
+};
+
+__device__ __forceinline__ int tiles_of(int lo, int hi) { return hi > lo ? (hi + kTok - 1) / kTok - lo / kTok : 0; }
+
+__device__ __forceinline__ Pair pair_of(const PagedDecodeArgs& a, int item) {
+  Pair s;
+  s.b = item / a.Hkv;
+  s.g = item - s.b * a.Hkv;
+  int t = a.pos[s.b];
+  const int cap = a.tab.max_pages * a.tab.page_size;
+  if (t >= cap) t = cap - 1;
+  Range r[3] = {{0, 0}, {0, 0}, {0, 0}};
+  if (t >= 0) {
+    const int n = row_ranges(a.pat, interval_of(a.pat, s.g), t, r);
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      if (i >= n) r[i] = Range{0, 0};
+  }
+  s.lo0 = r[0].lo; s.hi0 = r[0].hi; s.lo1 = r[1].lo; s.hi1 = r[1].hi; s.lo2 = r[2].lo; s.hi2 = r[2].hi;
+  s.n0 = tiles_of(s.lo0, s.hi0);
+  s.n1 = tiles_of(s.lo1, s.hi1);
+  s.n = s.n0 + s.n1 + tiles_of(s.lo2, s.hi2);
+  return s;
+}
+
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}" : "=r"(r) : "r"(two));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w) {
+  return pack_f16(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ void mma_f16(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
+  return r;
+}
+// transpose of an 8x8 matrix of 16-bit elements held as an MMA fragment
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+// address of 16-byte unit u of row r of a tile whose 128-byte columns are swizzled
+__device__ __forceinline__ uint32_t unit_addr(uint32_t tile, int r, int u) {
+  return tile + (u >> 3) * kBoxBytes + r * 128 + (((u & 7) ^ (r & 7)) << 4);
+}
+
+// Running state of a warp: per thread two heads (2 tq, 2 tq + 1) and D/16 fragments of O^T, whose rows
+// are the head dimension: bf16, row r of fragment j is d = 16 j + r; E4M3, rows gr and gr + 8 of
+// fragment j are d = 16 gr + 2 j and 16 gr + 2 j + 1 (see below).
+template <int D>
+struct State {
+  float acc[D / 16][4];
+  float m0, m1, l0, l1;
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+    m0 = m1 = -INFINITY;
+    l0 = l1 = 0.f;
+  }
+  // the running maxima grow to cover x0, x1 (this thread's largest scores of its two heads)
+  __device__ __forceinline__ void cover(float x0, float x1) {
+    if (!__any_sync(0xffffffffu, x0 > m0 + kRescale || x1 > m1 + kRescale)) return;
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+      x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, o));
+      x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, o));
+    }
+    float f0 = 1.f, f1 = 1.f;
+    if (x0 > m0 + kRescale) { f0 = m0 == -INFINITY ? 0.f : ptx::ex2(m0 - x0); m0 = x0; }
+    if (x1 > m1 + kRescale) { f1 = m1 == -INFINITY ? 0.f : ptx::ex2(m1 - x1); m1 = x1; }
+    l0 *= f0;
+    l1 *= f1;
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j) {
+      acc[j][0] *= f0; acc[j][1] *= f1; acc[j][2] *= f0; acc[j][3] *= f1;
+    }
+  }
+};
+
+// First tile of CTA c's share of W tiles cut into G shares (none of a cut into more shares than tiles
+// is empty: G is then W).
+__device__ __forceinline__ long long share(long long W, int G, int c) { return c >= G ? W : W * c / G; }
+
+template <int D, bool KV8>
+__global__ void __launch_bounds__(kThreads, Geo<D, KV8>::kCtas)
+    paged_split_kernel(const __grid_constant__ PagedDecodeArgs a) {
+  using G_ = Geo<D, KV8>;
+  constexpr int KS = D / 16;
+  constexpr int kStages = G_::kStages;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + G_::kOffBar);
+  uint64_t* empty_bar = full_bar + kStages;
+  volatile uint64_t* seen = empty_bar + kStages;  // per stage: the tile's visible positions
+  long long* warp_sum = reinterpret_cast<long long*>(full_bar + 16);  // [5]
+  volatile int& abort_flag = *reinterpret_cast<volatile int*>(full_bar + 24);
+  int& first_item = *reinterpret_cast<int*>(full_bar + 25);
+  int& first_off = *reinterpret_cast<int*>(full_bar + 26);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int c = blockIdx.x;
+  const int n_items = a.B * a.Hkv;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      ptx::mbar_init(&full_bar[s], 1);
+      ptx::mbar_init(&empty_bar[s], kWarps);
+    }
+    abort_flag = 0;
+    ptx::fence_mbar_init();
+  }
+  // the joining kernel may be set up while this one runs (it waits for this one's results)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // ---- this CTA's share: tiles [w0, w1) of the list
+  const int per = (n_items + kThreads - 1) / kThreads;
+  const int i0 = imin(n_items, (int)threadIdx.x * per), i1 = imin(n_items, i0 + per);
+  long long mine = 0;
+  for (int i = i0; i < i1; ++i) mine += pair_of(a, i).n;
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) warp_sum[warp] = incl;
+  __syncthreads();
+  long long before = incl - mine, W = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += warp_sum[w];
+    W += warp_sum[w];
+  }
+  const int G = W < (long long)gridDim.x ? (int)W : (int)gridDim.x;
+  const long long w0 = share(W, G, c), w1 = share(W, G, c + 1);
+  if (w0 < w1 && before <= w0 && w0 < before + mine) {
+    long long p = before;
+    for (int i = i0; i < i1; ++i) {
+      const int n = pair_of(a, i).n;
+      if (w0 < p + n) { first_item = i; first_off = (int)(w0 - p); break; }
+      p += n;
+    }
+  }
+  __syncthreads();
+  const bool pool_ok = (ptx::smem_u32(smem) & 1023u) == 0;  // the swizzle pattern assumes it
+
+  if (warp == kWarps) {
+    // ------------------------------------------------------------------ producer
+    if (w0 < w1 && pool_ok) {
+      if (lane == 0) {
+        ptx::tma_prefetch_desc(&a.tm_k);
+        ptx::tma_prefetch_desc(&a.tm_v);
+      }
+      const int nbox = kTok / a.box_rows;
+      const int ntile = (int)(w1 - w0);
+      int item = first_item, off = first_off;
+      Pair s = pair_of(a, item);
+      // box `lane` of the tile at hand: its first position, its page (-1: nothing to fetch)
+      int base, lo, hi, page, slot;
+      bool want;
+      auto look = [&]() {
+        while (off >= s.n) { s = pair_of(a, ++item); off = 0; }
+        s.tile(off, base, lo, hi);
+        const int p = base + lane * a.box_rows;
+        want = lane < nbox && p < hi && p + a.box_rows > lo;
+        page = -1;
+        slot = 0;
+        if (want) {
+          const int i = p / a.tab.page_size;
+          slot = p - i * a.tab.page_size;
+          page = a.tab.ptr[s.b * a.tab.sb + s.g * a.tab.sh + i];
+        }
+      };
+      look();
+      int issued = 0;
+      for (int st = 0; st < ntile; ++st) {
+        const int sl = st % kStages;
+        const bool good = want && page >= 0 && page < a.tab.n_pages;
+        const uint32_t fetch = __ballot_sync(0xffffffffu, good);
+        const uint32_t bad = __ballot_sync(0xffffffffu, want && !good);
+        const int my_page = page, my_slot = slot, g = a.tab.sh ? 0 : s.g;
+        uint64_t vis = (hi - base >= kTok ? ~0ull : (1ull << (hi - base)) - 1) & ~((1ull << (lo - base)) - 1);
+        if (bad) {  // entries outside the pool: reported, their keys left out
+          const uint64_t rows = a.box_rows == kTok ? ~0ull : (1ull << a.box_rows) - 1;
+          for (int x = 0; x < nbox; ++x)
+            if ((bad >> x) & 1) vis &= ~(rows << (x * a.box_rows));
+          if (lane == 0) a.status[3] = 1u;
+        }
+        ++off;
+        if (st + 1 < ntile) look();  // the next tile's pages, while this one waits for its slot
+        if (st >= kStages && !ptx::mbar_wait_warp(&empty_bar[sl], ((st / kStages) & 1) ^ 1, &abort_flag, a.status)) break;
+        uint8_t* ks = smem + sl * 2 * G_::kTileBytes;
+        uint8_t* vs = ks + G_::kTileBytes;
+        if (lane == 0) {
+          seen[sl] = vis;
+          ptx::mbar_arrive_expect_tx(&full_bar[sl], 2 * G_::kUnits * __popc(fetch) * a.box_rows * 128);
+        }
+        __syncwarp();
+        if (good) {
+          const int at = lane * a.box_rows * 128;
+#pragma unroll
+          for (int u = 0; u < G_::kUnits; ++u) {
+            ptx::tma_load_4d(ks + u * kBoxBytes + at, &a.tm_k, &full_bar[sl], u * (KV8 ? 128 : 64), my_slot, g, my_page);
+            ptx::tma_load_4d(vs + u * kBoxBytes + at, &a.tm_v, &full_bar[sl], u * (KV8 ? 128 : 64), my_slot, g, my_page);
+          }
+        }
+        issued = st + 1;
+      }
+      // never leave the CTA with copies in flight
+      for (int st = (issued > kStages ? issued - kStages : 0); st < issued; ++st)
+        ptx::mbar_wait(&full_bar[st % kStages], (st / kStages) & 1, nullptr, a.status);
+    }
+    return;
+  }
+
+  // -------------------------------------------------------------------- compute warps
+  const int gr = lane >> 2, tq = lane & 3;
+  const int grp = a.grp;
+  float* red = reinterpret_cast<float*>(smem + G_::kOffRed);  // [warp][head][D + 2]
+  const uint32_t ring = ptx::smem_u32(smem);
+  const int row0 = warp * 16;
+  bool ok = pool_ok;
+  if (!pool_ok && threadIdx.x == 0) atomicOr(a.status, (uint32_t)ptx::kStatusCheck);
+
+  // pairs that see nothing (a slot without a sequence): zeros and -inf, by one CTA each
+  for (int i = c; i < n_items; i += gridDim.x) {
+    const Pair s = pair_of(a, i);
+    if (s.n) continue;
+    const size_t h0 = (size_t)s.b * a.Hkv * grp + (size_t)s.g * grp;
+    for (int x = threadIdx.x; x < grp * D; x += kWarps * 32)
+      reinterpret_cast<__nv_bfloat16*>(a.o)[h0 * D + x] = __float2bfloat16_rn(0.f);
+    if (a.lse && (int)threadIdx.x < grp) a.lse[h0 + threadIdx.x] = -INFINITY;
+  }
+
+  int4 rec = make_int4(-1, 0, 0, 0);
+  int st = 0;
+  int item = first_item, off = first_off;
+  for (long long w = w0; w < w1;) {
+    const Pair s = pair_of(a, item);
+    const int take = (int)(w1 - w < s.n - off ? w1 - w : s.n - off);
+    if (take > 0) {
+      // Q^T fragments: columns are the heads of the group (those past it are zero)
+      uint32_t qf[KS][2];
+      const uint32_t* q = reinterpret_cast<const uint32_t*>(
+          reinterpret_cast<const __nv_bfloat16*>(a.q_t) + ((size_t)s.b * a.Hkv * grp + (size_t)s.g * grp + imin(gr, grp - 1)) * D);
+#pragma unroll
+      for (int kk = 0; kk < KS; ++kk) {
+        // E4M3: the head dimension is visited in another order, so that a thread's bytes of a key row are
+        // contiguous: chunk kk of thread tq is d = 32 tq + 4 kk .. + 3
+        const uint32_t x = KV8 ? q[16 * tq + 2 * kk] : q[8 * kk + tq];
+        const uint32_t y = KV8 ? q[16 * tq + 2 * kk + 1] : q[8 * kk + 4 + tq];
+        qf[kk][0] = gr < grp ? (KV8 ? bf16x2_to_f16x2(x) : x) : 0u;
+        qf[kk][1] = gr < grp ? (KV8 ? bf16x2_to_f16x2(y) : y) : 0u;
+      }
+      State<D> z;
+      z.clear();
+      for (int i = 0; ok && i < take; ++i, ++st) {
+        const int sl = st % kStages;
+        if (!ptx::mbar_wait_warp(&full_bar[sl], (st / kStages) & 1, &abort_flag, a.status)) { ok = false; break; }
+        const uint32_t bits = (uint32_t)(seen[sl] >> row0) & 0xffffu;  // this warp's 16 tokens
+        const uint32_t kt = ring + sl * 2 * G_::kTileBytes, vt = kt + G_::kTileBytes;
+        if (bits == 0) {
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&empty_bar[sl]);
+          continue;
+        }
+        // ---- scores S^T[token][head]
+        float sc[2][4] = {};
+        uint4 vr[4];  // E4M3: bytes [16 gr, 16 gr + 16) of value rows 2 tq, 2 tq + 1, 2 tq + 8, 2 tq + 9
+        if constexpr (KV8) {
+          uint32_t kw[2][8];  // bytes [32 tq, 32 tq + 32) of key rows gr and gr + 8
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int r = row0 + 8 * h + gr;
+            const uint4 x0 = lds128(kt + r * 128 + (((2 * tq) ^ (r & 7)) << 4));
+            const uint4 x1 = lds128(kt + r * 128 + (((2 * tq + 1) ^ (r & 7)) << 4));
+            kw[h][0] = x0.x; kw[h][1] = x0.y; kw[h][2] = x0.z; kw[h][3] = x0.w;
+            kw[h][4] = x1.x; kw[h][5] = x1.y; kw[h][6] = x1.z; kw[h][7] = x1.w;
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = 2 * tq + (e & 1) + 8 * (e >> 1), r = row0 + j;
+            vr[e] = lds128(vt + r * 128 + ((gr ^ (r & 7)) << 4));
+            if (bits != 0xffffu && !((bits >> j) & 1)) vr[e] = make_uint4(0, 0, 0, 0);
+          }
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&empty_bar[sl]);  // the stage's bytes are in registers
+#pragma unroll
+          for (int kk = 0; kk < KS; ++kk) {
+            const uint32_t f[4] = {e4m3x2_to_f16x2(kw[0][kk] & 0xffffu), e4m3x2_to_f16x2(kw[1][kk] & 0xffffu),
+                                   e4m3x2_to_f16x2(kw[0][kk] >> 16), e4m3x2_to_f16x2(kw[1][kk] >> 16)};
+            mma_f16(sc[kk & 1], f, qf[kk][0], qf[kk][1]);
+          }
+        } else {
+#pragma unroll
+          for (int kk = 0; kk < KS; ++kk) {
+            uint32_t f[4];
+            ptx::ldsm_x4(unit_addr(kt, row0 + (lane & 15), 2 * kk + (lane >> 4)), f);
+            ptx::mma_16816(sc[kk & 1], f, qf[kk][0], qf[kk][1]);
+          }
+        }
+        // ---- online softmax; tokens gr and gr + 8, heads 2 tq and 2 tq + 1
+        float x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = (sc[0][e] + sc[1][e]) * a.scale_log2;
+        if (bits != 0xffffu) {
+          if (!((bits >> gr) & 1)) x[0] = x[1] = -INFINITY;
+          if (!((bits >> (gr + 8)) & 1)) x[2] = x[3] = -INFINITY;
+        }
+        z.cover(fmaxf(x[0], x[2]), fmaxf(x[1], x[3]));
+        const float r0 = z.m0 == -INFINITY ? 0.f : z.m0 - kLift<KV8>, r1 = z.m1 == -INFINITY ? 0.f : z.m1 - kLift<KV8>;
+        const float p0 = ptx::ex2(x[0] - r0), p1 = ptx::ex2(x[1] - r1);
+        const float p2 = ptx::ex2(x[2] - r0), p3 = ptx::ex2(x[3] - r1);
+        z.l0 += p0 + p2;
+        z.l1 += p1 + p3;
+        // P^T as the second operand: rows are tokens, so transpose the 8x8 halves
+        const uint32_t b0 = transpose8(KV8 ? pack_f16(p0, p1) : ptx::pack_bf16(p0, p1));
+        const uint32_t b1 = transpose8(KV8 ? pack_f16(p2, p3) : ptx::pack_bf16(p2, p3));
+        // ---- O^T[d][head] += V^T[d][token] P^T[token][head]
+        if constexpr (KV8) {
+          // fragment j's rows gr and gr + 8 are d = 16 gr + 2 j and + 1: the bytes 2 j and 2 j + 1 of this
+          // thread's value bytes, of the token pairs (2 tq, 2 tq + 1) and (2 tq + 8, 2 tq + 9)
+          const uint32_t va[4] = {vr[0].x, vr[0].y, vr[0].z, vr[0].w}, vb[4] = {vr[1].x, vr[1].y, vr[1].z, vr[1].w};
+          const uint32_t vc[4] = {vr[2].x, vr[2].y, vr[2].z, vr[2].w}, vd[4] = {vr[3].x, vr[3].y, vr[3].z, vr[3].w};
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint32_t sel = (j & 1) ? 0x7362u : 0x5140u;
+            const uint32_t lo2 = prmt(va[j >> 1], vb[j >> 1], sel), hi2 = prmt(vc[j >> 1], vd[j >> 1], sel);
+            const uint32_t f[4] = {e4m3x2_to_f16x2(lo2 & 0xffffu), e4m3x2_to_f16x2(lo2 >> 16),
+                                   e4m3x2_to_f16x2(hi2 & 0xffffu), e4m3x2_to_f16x2(hi2 >> 16)};
+            mma_f16(z.acc[j], f, b0, b1);
+          }
+        } else {
+          // masked tokens' V elements become zero in the fragments (0 times an infinity is not 0)
+          uint32_t k0 = ~0u, k1 = ~0u;
+          if (bits != 0xffffu) {
+            k0 = (((bits >> (2 * tq)) & 1) ? 0xffffu : 0u) | (((bits >> (2 * tq + 1)) & 1) ? 0xffff0000u : 0u);
+            k1 = (((bits >> (2 * tq + 8)) & 1) ? 0xffffu : 0u) | (((bits >> (2 * tq + 9)) & 1) ? 0xffff0000u : 0u);
+          }
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j) {
+            uint32_t f[4];
+            ptx::ldsm_x4_trans(unit_addr(vt, row0 + (lane & 7) + 8 * (lane >> 4), 2 * j + ((lane >> 3) & 1)), f);
+            f[0] &= k0; f[1] &= k0; f[2] &= k1; f[3] &= k1;
+            ptx::mma_16816(z.acc[j], f, b0, b1);
+          }
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&empty_bar[sl]);
+        }
+      }
+      // ---- join the warps
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) {
+        z.l0 += __shfl_xor_sync(0xffffffffu, z.l0, o);
+        z.l1 += __shfl_xor_sync(0xffffffffu, z.l1, o);
+      }
+      asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");  // the last join has been read
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int hd = 2 * tq + h;
+        if (hd < grp) {
+          float* r = red + (warp * grp + hd) * (D + 2);
+          if (gr == 0) { r[0] = (h ? z.m1 : z.m0) - kLift<KV8>; r[1] = h ? z.l1 : z.l0; }
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j) {
+            const int d0 = KV8 ? 16 * gr + 2 * j : 16 * j + gr, d1 = KV8 ? d0 + 1 : d0 + 8;
+            r[2 + d0] = z.acc[j][h];
+            r[2 + d1] = z.acc[j][2 + h];
+          }
+        }
+      }
+      asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
+      const bool begins = off == 0, ends = off + take == s.n;
+      if (ok && !abort_flag) {
+        const size_t h0 = (size_t)s.b * a.Hkv * grp + (size_t)s.g * grp;
+        float* part = a.part + ((size_t)2 * c + (begins ? 1 : 0)) * grp * (D + 2);
+        for (int x = threadIdx.x; x < grp * D; x += kWarps * 32) {
+          const int hd = x / D, d = x - hd * D;
+          float m = -INFINITY;
+#pragma unroll
+          for (int v = 0; v < kWarps; ++v) m = fmaxf(m, red[(v * grp + hd) * (D + 2)]);
+          float o = 0.f, l = 0.f;
+#pragma unroll
+          for (int v = 0; v < kWarps; ++v) {
+            const float* r = red + (v * grp + hd) * (D + 2);
+            const float f = r[0] == -INFINITY ? 0.f : ptx::ex2(r[0] - m);
+            o += f * r[2 + d];
+            l += f * r[1];
+          }
+          if (KV8) o *= a.v_scale;
+          if (begins && ends) {  // the pair is finished here
+            reinterpret_cast<__nv_bfloat16*>(a.o)[(h0 + hd) * D + d] = __float2bfloat16_rn(m == -INFINITY ? 0.f : o / l);
+            if (a.lse && d == 0) a.lse[h0 + hd] = m == -INFINITY ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
+          } else {
+            part[hd * (D + 2) + 2 + d] = o;
+            if (d == 0) { part[hd * (D + 2)] = m; part[hd * (D + 2) + 1] = l; }
+          }
+        }
+      }
+      if (begins && !ends) {  // the pair's other tiles: CTAs c + 1 .. last
+        const long long end = w + s.n;
+        int last = c + 1;
+        while (share(W, G, last + 1) < end) ++last;
+        rec = make_int4(s.b, s.g, last, 0);
+      }
+      w += take;
+    }
+    ++item;
+    off = 0;
+  }
+  if (threadIdx.x == 0) a.rec[c] = rec;
+}
+
+// Joins the pieces of the pair that begins in CTA c and goes on in later ones; one block per
+// (c, head of the group).  Each warp takes every fourth piece; the pieces' order is fixed.
+template <int D>
+__global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ PagedDecodeArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c = blockIdx.x, hd = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int4 rec = a.rec[c];
+  if (rec.x < 0) return;
+  constexpr int E = D / 32;
+  __shared__ float sm[4], sl[4], so[4][D];
+  const int n = rec.z - c + 1;
+  const size_t slot = (size_t)a.grp * (D + 2);
+  // piece 0 is CTA c's last segment, piece i CTA c + i's first
+  auto piece = [&](int i) { return a.part + (i == 0 ? 2 * (size_t)c + 1 : 2 * ((size_t)c + i)) * slot + hd * (D + 2); };
+  float m = -INFINITY;
+  for (int i = warp * 32 + lane; i < n; i += 128) m = fmaxf(m, piece(i)[0]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (lane == 0) sm[warp] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
+  float acc[E] = {}, l = 0.f;
+#pragma unroll 4
+  for (int i = warp; i < n; i += 4) {
+    const float* p = piece(i);
+    const float f = p[0] == -INFINITY ? 0.f : ptx::ex2(p[0] - m);
+    l += f * p[1];
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] += f * p[2 + lane + 32 * e];
+  }
+  if (lane == 0) sl[warp] = l;
+#pragma unroll
+  for (int e = 0; e < E; ++e) so[warp][lane + 32 * e] = acc[e];
+  __syncthreads();
+  if (threadIdx.x >= D) return;
+  const int d = threadIdx.x;
+  l = sl[0] + sl[1] + sl[2] + sl[3];
+  const float o = so[0][d] + so[1][d] + so[2][d] + so[3][d];
+  const size_t h = (size_t)rec.x * a.Hkv * a.grp + (size_t)rec.y * a.grp + hd;
+  reinterpret_cast<__nv_bfloat16*>(a.o)[h * D + d] = __float2bfloat16_rn(m == -INFINITY ? 0.f : o / l);
+  if (a.lse && d == 0) a.lse[h] = m == -INFINITY ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
+}
+
+template <int D, bool KV8>
+cudaError_t launch_paged_t(const PagedDecodeArgs& a, cudaStream_t s) {
+  const int bytes = Geo<D, KV8>::smem(a.grp);
+  cudaError_t e = cudaFuncSetAttribute(paged_split_kernel<D, KV8>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  paged_split_kernel<D, KV8><<<a.grid, kThreads, bytes, s>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.grid, a.grp);
+  cfg.blockDim = dim3(128);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_join_kernel<D>, a);
+}
+
+}  // namespace
+
+// CTAs of a paged decode: as many as the GPU holds at once, and no more than there can be tiles.
+int paged_decode_grid(const Pat& p, int B, int Hq, int Hkv, int d, bool kv8, int max_pages, int page_size) {
+  const int grp = Hq / Hkv;
+  const int most = 148 * (kv8 ? Geo<128, true>::ctas(grp) : (d == 128 ? Geo<128, false>::ctas(grp) : Geo<64, false>::ctas(grp)));
+  const int64_t cap = (int64_t)max_pages * page_size, R = (int64_t)p.T - p.S;
+  const int64_t wide = R > 0 ? (R + p.H - 1) / p.H : 0;
+  auto tiles = [&](int64_t n) { return n > 0 ? ((n < cap ? n : cap) + kTok - 1) / kTok + 1 : 0; };
+  const int64_t n = (tiles(p.S) + tiles(wide) + tiles(p.L)) * B * Hkv;
+  return (int)(n < most ? n : most);
+}
+
+size_t paged_decode_bytes(int grid, int grp, int d) {
+  return align_up((size_t)grid * sizeof(int4), 256) + align_up((size_t)2 * grid * grp * (d + 2) * sizeof(float), 256);
+}
+
+cudaError_t launch_paged_decode(const PagedDecodeArgs& a, int d, bool kv8, cudaStream_t s) {
+  if (kv8) return d == 128 ? launch_paged_t<128, true>(a, s) : cudaErrorInvalidValue;
+  if (d == 64) return launch_paged_t<64, false>(a, s);
+  if (d == 128) return launch_paged_t<128, false>(a, s);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace cowa

@@ -1,0 +1,314 @@
+// cowa_rope.cu -- rotary positions with one to four axes, and the write of a step's tokens into a
+// paged cache (the queries and keys rotated on the way).
+//
+// A rotation turns pairs (a, b) of a head's elements by an angle that depends on the token:
+//   angle(t, i) = pos[axis(i)][t] * inv_freq[i],   i = 0 .. r/2 - 1
+//   (a, b) -> scale * (a cos - b sin, b cos + a sin)
+// Pair i is (i, i + r/2) or, interleaved, (2i, 2i + 1); elements r .. d-1 pass through.  Its
+// transpose, which the backward pass needs, is the rotation by the negated angle.
+//
+// Angles are formed in 64 bits (int32 position times fp32 frequency) and reduced to a fraction of a
+// turn there: at position 100000 an fp32 product is off by 0.004 radians.  Sine and cosine of the
+// reduced angle, and the rotation itself, are in 32 bits; the result is rounded once.  (Keys that
+// become E4M3 codes are rotated in 64 bits, see below.)
+//
+// Bound: every element is read and written once, so HBM.  A block owns a few tokens and all their
+// heads: the angles of a token are computed once, into shared memory, and used by all its heads; the
+// rows are then moved with 16-byte loads and stores, each thread fetching its next row before it
+// turns the one it has.
+#include <cuda_bf16.h>
+
+#include "cowa_internal.h"
+
+namespace cowa {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxTok = 8;  // tokens per block, at most
+
+// How a row is cut into units of work:
+//   kSplit  8 pairs (i, i + r/2): two 16-byte pieces     (r/2 a multiple of 8)
+//   kInter  4 pairs (2i, 2i + 1): one 16-byte piece      (r a multiple of 8; also no rotation at all)
+//   kAny    one 16-byte piece, its partners wherever they are, through shared memory
+enum { kSplit, kInter, kAny };
+// What becomes of the rows: rotated copies; bf16 pages; pages of E4M3 codes
+enum { kTurn, kPagesBf16, kPagesE4m3 };
+
+// bytes of a block's fp32 cos and sin tables, and of all its shared memory
+__host__ __device__ inline size_t table_bytes(int entries) { return ((size_t)entries * 8 + 15) / 16 * 16; }
+inline size_t smem_bytes(int mode, int tok, int half, int Hk) {
+  return table_bytes(tok * half) + (mode == kPagesE4m3 ? (size_t)tok * half * 16 : 0) + (mode == kTurn ? 0 : (size_t)tok * Hk * 16);
+}
+
+struct Row {
+  uint4 lo, hi;
+};
+
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ void widen8(const uint4& v, float* x) {
+  x[0] = bf_lo(v.x); x[1] = bf_hi(v.x); x[2] = bf_lo(v.y); x[3] = bf_hi(v.y);
+  x[4] = bf_lo(v.z); x[5] = bf_hi(v.z); x[6] = bf_lo(v.w); x[7] = bf_hi(v.w);
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint4 narrow8(const float* x) {
+  return make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
+}
+// E4M3 codes of x * inv: a float32 product, then round to nearest even, saturating (as the quantiser)
+__device__ __forceinline__ uint2 codes8(const float* x, float inv) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint16_t c;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(x[2 * i + 1] * inv), "f"(x[2 * i] * inv));
+    w[i] = c;
+  }
+  return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+}
+
+template <int MODE, int CUT>
+__global__ void __launch_bounds__(kThreads) turn_kernel(const __grid_constant__ RopeArgs a, int tok_per_block) {
+  // cos and sin of the block's tokens.  Vector cuts: [token][piece][unit] of float4, the pieces being
+  // the unit's cosines (2 or 1 float4) and then its sines, so that neighbouring units are neighbours
+  // in memory.  kAny: [token][pair] of (cos, sin).
+  extern __shared__ __align__(16) unsigned char smem[];
+  float* tab = reinterpret_cast<float*>(smem);
+  // E4M3 keys: cos and sin in 64 bits, [token][pair]
+  double2* tab64 = reinterpret_cast<double2*>(smem + table_bytes(tok_per_block * a.half));
+  // element offset of each (token, KV head)'s key and value row in the pools, -1 for none
+  longlong2* dst = reinterpret_cast<longlong2*>(tab64 + (MODE == kPagesE4m3 ? tok_per_block * a.half : 0));
+  __shared__ int live[kMaxTok];
+  __shared__ __align__(16) __nv_bfloat16 stage[CUT == kAny ? kThreads * 8 : 8];
+
+  const int tid = threadIdx.x;
+  const long long m0 = (long long)blockIdx.x * tok_per_block;
+  const int nt = (int)(a.M - m0 < tok_per_block ? a.M - m0 : tok_per_block);
+  const int half = a.half, rd = 2 * half;
+  constexpr int P = CUT == kSplit ? 8 : 4;  // pairs per unit
+  const int rot_units = CUT == kSplit ? half / 8 : (CUT == kInter ? rd / 8 : 0);
+  const int units = CUT == kSplit ? rot_units + (a.d - rd) / 8 : a.d / 8;
+  const int lanes = kThreads / units;  // rows in flight
+  const int heads = a.Hq + a.Hk + (MODE == kTurn ? 0 : a.Hk);
+  const int u = tid % units;
+  const bool active = tid < lanes * units;
+
+  auto src_of = [&](int tok, int head) -> const __nv_bfloat16* {
+    const long long m = m0 + tok;
+    const long long b = MODE == kTurn ? m / a.N : 0, t = MODE == kTurn ? m - b * a.N : m;
+    if (head < a.Hq) return a.q + b * a.q_sb + t * a.q_st + head * a.q_sh;
+    if (MODE == kTurn || head < a.Hq + a.Hk) return a.k + b * a.k_sb + t * a.k_st + (head - a.Hq) * a.k_sh;
+    return a.v + t * a.v_st + (head - a.Hq - a.Hk) * a.v_sh;
+  };
+  auto fetch = [&](int tok, int head) -> Row {
+    const __nv_bfloat16* p = src_of(tok, head);
+    Row r;
+    r.hi = make_uint4(0, 0, 0, 0);
+    if (CUT == kSplit && u < rot_units) {
+      r.lo = *reinterpret_cast<const uint4*>(p + 8 * u);
+      r.hi = *reinterpret_cast<const uint4*>(p + half + 8 * u);
+    } else {
+      r.lo = *reinterpret_cast<const uint4*>(p + (CUT == kSplit ? rd + 8 * (u - rot_units) : 8 * u));
+    }
+    return r;
+  };
+  // rows in order of (token, head); this thread's next one
+  int tok = 0, head = tid / units;
+  auto settle = [&]() {
+    while (head >= heads) { head -= heads; ++tok; }
+  };
+  settle();
+  Row cur;
+  bool have = active && tok < nt;
+  if (have) cur = fetch(tok, head);
+
+  for (int x = tid; x < nt * half; x += kThreads) {
+    const int tk = x / half, i = x - tk * half;
+    const long long m = m0 + tk;
+    const int axis = (i >= a.end0) + (i >= a.end1) + (i >= a.end2);
+    int p;
+    if (a.pos) {
+      const long long b = MODE == kTurn ? m / a.N : 0, t = MODE == kTurn ? m - b * a.N : m;
+      p = a.pos[axis * a.pos_sa + b * a.pos_sb + t];
+    } else {
+      p = MODE == kTurn ? (int)(m % a.N) : a.cache_pos[m];
+    }
+    double turns = (double)p * (double)a.inv_freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
+    turns -= rint(turns);
+    float s, c;
+    sincospif((float)(2.0 * turns), &s, &c);
+    c *= a.scale;
+    s *= a.sin_scale;
+    if (CUT == kAny) {
+      reinterpret_cast<float2*>(tab)[x] = make_float2(c, s);
+    } else {
+      const int un = i / P, j = i % P;
+      float* base = tab + (size_t)tk * rd + 4 * un + (j & 3);
+      base[(j >> 2) * 4 * rot_units] = c;
+      base[((P / 4) + (j >> 2)) * 4 * rot_units] = s;
+    }
+    if (MODE == kPagesE4m3) {
+      double s64, c64;
+      sincospi(2.0 * turns, &s64, &c64);
+      tab64[x] = make_double2(c64 * (double)a.scale, s64 * (double)a.sin_scale);
+    }
+  }
+  if (MODE != kTurn) {
+    for (int x = tid; x < nt * a.Hk; x += kThreads) {
+      const int tk = x / a.Hk, g = x - tk * a.Hk;
+      const int p = a.cache_pos[m0 + tk];
+      const long long sq = a.seq ? a.seq[m0 + tk] : m0 + tk;
+      const bool on = p >= 0 && sq >= 0 && sq < a.tab.n_seq;
+      long long ok = -1, ov = -1;
+      if (on && p / a.tab.page_size < a.tab.max_pages) {
+        const int page = a.tab.ptr[sq * a.tab.sb + g * a.tab.sh + p / a.tab.page_size];
+        if (page >= 0 && page < a.tab.n_pages) {
+          const int slot = p % a.tab.page_size, gh = a.tab.sh ? 0 : g;
+          ok = page * a.kp_sp + slot * a.kp_st + gh * a.kp_sh;
+          ov = page * a.vp_sp + slot * a.vp_st + gh * a.vp_sh;
+        }
+      }
+      dst[x] = make_longlong2(ok, ov);
+      if (g == 0) live[tk] = on;
+    }
+  }
+  __syncthreads();
+
+  // a whole number of passes for every thread: kAny exchanges pieces within the block's warps
+  const int passes = (nt * heads + lanes - 1) / lanes;
+  for (int it = 0; it < passes; ++it) {
+    const int t0 = tok, h0 = head;
+    const Row r = cur;
+    const bool mine = have;
+    head += lanes;
+    settle();
+    have = active && tok < nt;
+    if (have) cur = fetch(tok, head);
+
+    if (CUT == kAny) {
+      // the row's pieces side by side in shared memory, for the partners of this one's elements
+      __syncthreads();
+      if (mine) *reinterpret_cast<uint4*>(stage + 8 * tid) = r.lo;
+      __syncthreads();
+    }
+    if (!mine) continue;
+    const bool is_q = h0 < a.Hq, is_v = MODE != kTurn && h0 >= a.Hq + a.Hk;
+    float lo[8], hi[8];
+    widen8(r.lo, lo);
+    if (CUT == kSplit) widen8(r.hi, hi);
+    const bool exact = MODE == kPagesE4m3 && !is_q;
+    if (!is_v) {
+      if (CUT == kAny) {
+        const __nv_bfloat16* row = stage + 8 * (tid - u);
+        for (int e = 0; e < 8; ++e) {
+          const int x = 8 * u + e;
+          if (x >= rd) break;
+          const int i = a.interleaved ? x >> 1 : (x < half ? x : x - half);
+          const bool second = a.interleaved ? (x & 1) : x >= half;
+          const int y = a.interleaved ? x ^ 1 : (second ? x - half : x + half);
+          const float other = __bfloat162float(row[y]);
+          if (exact) {
+            const double2 cs = tab64[t0 * half + i];
+            lo[e] = (float)(second ? fma((double)lo[e], cs.x, (double)other * cs.y)
+                                   : fma((double)lo[e], cs.x, -((double)other * cs.y)));
+          } else {
+            const float2 cs = reinterpret_cast<const float2*>(tab)[t0 * half + i];
+            lo[e] = second ? fmaf(lo[e], cs.x, other * cs.y) : fmaf(lo[e], cs.x, -(other * cs.y));
+          }
+        }
+      } else if (u < rot_units) {
+        if (exact) {
+          const double2* cs = tab64 + t0 * half + P * u;
+#pragma unroll
+          for (int j = 0; j < P; ++j) {
+            float& x = CUT == kSplit ? lo[j] : lo[2 * j];
+            float& y = CUT == kSplit ? hi[j] : lo[2 * j + 1];
+            const double xa = x, xb = y, c = cs[j].x, s = cs[j].y;
+            x = (float)fma(xa, c, -(xb * s));
+            y = (float)fma(xb, c, xa * s);
+          }
+        } else {
+          const float4* cs = reinterpret_cast<const float4*>(tab + (size_t)t0 * rd) + u;
+          float c[P], s[P];
+#pragma unroll
+          for (int w = 0; w < P / 4; ++w) {
+            const float4 cw = cs[w * rot_units], sw = cs[(P / 4 + w) * rot_units];
+            c[4 * w] = cw.x; c[4 * w + 1] = cw.y; c[4 * w + 2] = cw.z; c[4 * w + 3] = cw.w;
+            s[4 * w] = sw.x; s[4 * w + 1] = sw.y; s[4 * w + 2] = sw.z; s[4 * w + 3] = sw.w;
+          }
+#pragma unroll
+          for (int j = 0; j < P; ++j) {
+            float& x = CUT == kSplit ? lo[j] : lo[2 * j];
+            float& y = CUT == kSplit ? hi[j] : lo[2 * j + 1];
+            const float xa = x, xb = y;
+            x = fmaf(xa, c[j], -(xb * s[j]));
+            y = fmaf(xb, c[j], xa * s[j]);
+          }
+        }
+      }
+    }
+    // elements [at, at + 8) and, for a rotated kSplit unit, [at2, at2 + 8)
+    const bool two = CUT == kSplit && u < rot_units;
+    const int at = CUT == kSplit && !two ? rd + 8 * (u - rot_units) : 8 * u, at2 = half + 8 * u;
+    if (MODE == kTurn || is_q) {
+      const long long m = m0 + t0;
+      const long long b = MODE == kTurn ? m / a.N : 0, t = MODE == kTurn ? m - b * a.N : m;
+      if (MODE != kTurn && !live[t0]) continue;
+      __nv_bfloat16* o = is_q ? a.qo + b * a.qo_sb + t * a.qo_st + h0 * a.qo_sh
+                              : a.ko + b * a.ko_sb + t * a.ko_st + (h0 - a.Hq) * a.ko_sh;
+      *reinterpret_cast<uint4*>(o + at) = narrow8(lo);
+      if (two) *reinterpret_cast<uint4*>(o + at2) = narrow8(hi);
+    } else {
+      const int g = h0 - a.Hq - (is_v ? a.Hk : 0);
+      const longlong2 at_kv = dst[t0 * a.Hk + g];
+      const long long off = is_v ? at_kv.y : at_kv.x;
+      if (off < 0) continue;
+      if (MODE == kPagesBf16) {
+        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(is_v ? a.vp : a.kp) + off;
+        *reinterpret_cast<uint4*>(o + at) = narrow8(lo);
+        if (two) *reinterpret_cast<uint4*>(o + at2) = narrow8(hi);
+      } else {
+        uint8_t* o = static_cast<uint8_t*>(is_v ? a.vp : a.kp) + off;
+        const float inv = is_v ? a.inv_v : a.inv_k;
+        *reinterpret_cast<uint2*>(o + at) = codes8(lo, inv);
+        if (two) *reinterpret_cast<uint2*>(o + at2) = codes8(hi, inv);
+      }
+    }
+  }
+}
+
+template <int MODE>
+cudaError_t launch_turn(const RopeArgs& a, cudaStream_t s) {
+  const int rd = 2 * a.half;
+  const int cut = a.half == 0 || (a.interleaved && rd % 8 == 0) ? kInter
+                  : !a.interleaved && a.half % 8 == 0           ? kSplit
+                                                                : kAny;
+  const int units = cut == kSplit ? a.half / 8 + (a.d - rd) / 8 : a.d / 8;
+  const int heads = a.Hq + (MODE == kTurn ? 1 : 2) * a.Hk;
+  const int lanes = kThreads / units;
+  // tokens per block: enough rows to fill its threads, but no fewer blocks than the SMs can hold
+  int tok = 1;
+  while (tok < kMaxTok && (tok * heads < lanes || (a.M + 2 * tok - 1) / (2 * tok) >= 148 * 8) &&
+         smem_bytes(MODE, 2 * tok, a.half, a.Hk) <= 32 * 1024)
+    tok *= 2;
+  const long long blocks = (a.M + tok - 1) / tok;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const size_t smem = smem_bytes(MODE, tok, a.half, a.Hk);
+  if (cut == kSplit) turn_kernel<MODE, kSplit><<<(unsigned)blocks, kThreads, smem, s>>>(a, tok);
+  else if (cut == kInter) turn_kernel<MODE, kInter><<<(unsigned)blocks, kThreads, smem, s>>>(a, tok);
+  else turn_kernel<MODE, kAny><<<(unsigned)blocks, kThreads, smem, s>>>(a, tok);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s) { return launch_turn<kTurn>(a, s); }
+
+cudaError_t launch_paged_append(const RopeArgs& a, bool e4m3, cudaStream_t s) {
+  return e4m3 ? launch_turn<kPagesE4m3>(a, s) : launch_turn<kPagesBf16>(a, s);
+}
+
+}  // namespace cowa

@@ -1,0 +1,483 @@
+"""GPU parity of the paged cache: tokens written to pages (paged_append, bf16 and E4M3) and decode over
+them, against the fp64 oracle over the cache the pages stand for.
+
+Tolerances of decode, element by element.  P is rounded to bf16 (half a step 2^-8; f16 with E4M3
+pages, 2^-11), which moves o by at most that share of A = sum p |v| / sum p; o is rounded to bf16
+(2^-8 |o|).  Scores are sums of d products in 32 bits: with N(0,1) inputs and d = 128 they are off by
+less than 2^-13, as are the 32-bit sums of P and O together, so 2^-12 A more.  lse: 2^-13 of score
+error and a few roundings of a number below 32: 2e-4."""
+
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import cowa_oracle as orc
+from oracle import fp8_kv as f8
+from oracle import rope as orp
+from structured_sparse_attention_cowa_b200 import cowa as cw
+from structured_sparse_attention_cowa_b200 import synth
+from tests.gpu_helpers import host_and_device, oracle_pattern, to64
+from tests.test_gpu_rope import assert_rotated
+
+pytestmark = pytest.mark.gpu
+LSE_TOL = 2e-4
+
+
+def assert_decoded(o, lse, q64, k, v, pos, pat, p_eps=2.0 ** -8, has=None):
+    """o, lse (CUDA) against attention of q64 [B, Hq, d] over k, v [B, Hkv, T, d] (float64) at pos; `has`
+    [B, Hkv, T]: positions that have a page."""
+    B, Hq, d = q64.shape
+    Hkv, Tc = k.shape[1], k.shape[2]
+    op = oracle_pattern(pat)
+    scale = pat.softmax_scale or 1 / np.sqrt(d)
+    go, gl = to64(o), lse.double().cpu().numpy()
+    for b in range(B):
+        t = min(pos[b], Tc - 1)
+        for g in range(Hkv):
+            hs = slice(g * Hq // Hkv, (g + 1) * Hq // Hkv)
+            see = orc.visible_mask(np.array([max(t, 0)]), Tc, op, g, Hkv)[0] if t >= 0 else np.zeros(Tc, bool)
+            if has is not None:
+                see = see & has[b, g]
+            if not see.any():
+                assert (go[b, hs] == 0).all() and (gl[b, hs] == -np.inf).all(), (b, g)
+                continue
+            s = q64[b, hs] @ k[b, g, see].T * scale
+            m = s.max(1, keepdims=True)
+            p = np.exp(s - m)
+            want = p @ v[b, g, see] / p.sum(1, keepdims=True)
+            A = p @ np.abs(v[b, g, see]) / p.sum(1, keepdims=True)
+            err = np.abs(go[b, hs] - want)
+            assert (err <= p_eps * A + 2.0 ** -8 * np.abs(want) + 2.0 ** -12 * A).all(), (b, g, err.max())
+            lerr = np.abs(gl[b, hs] - (m[:, 0] + np.log(p.sum(1))))
+            assert (lerr <= LSE_TOL).all(), (b, g, lerr.max())
+
+
+def make_table(rng, B, n, spare=2, heads=None):
+    """A table [B(, heads), n] of distinct pages in random order and the pool's size."""
+    want = B * n * (heads or 1)
+    t = rng.permutation(want + spare)[:want].astype(np.int32)
+    return t.reshape((B, heads, n) if heads else (B, n)), want + spare
+
+
+def ws_for(fn, pat, B, Hq, Hkv, d, n, ps, dev):
+    size = getattr(cw.lib(), fn + "_workspace_size")(ctypes.byref(pat.c()), B, Hq, Hkv, d, n, ps)
+    return torch.zeros(size, dtype=torch.uint8, device=dev)
+
+
+DECODE = [
+    # Hq, Hkv, d, pattern, page, pages, per head, layout, positions
+    (8, 4, 128, cw.Pattern(64, 128, 1024, 4), 64, 16, False, "bhtd", [0, 63, 64, 200, 1023, 511, -1]),
+    (10, 2, 128, cw.Pattern(20, 100, 900, 2), 16, 63, False, "bthd", [899, 17, 1000, 5, 5000]),   # past T, past the end
+    (8, 8, 128, cw.Pattern(0, 1, 1024, 8), 8, 128, True, "bhtd", [1023, 0, 700]),                 # L = 1, no sink
+    (16, 2, 64, cw.Pattern(4, 60, 4, 1), 24, 43, False, "bthd", [1023, 3, 64, -1, -7]),           # sinks and band only
+    (7, 1, 64, cw.Pattern(33, 5000, 1024, 1), 48, 22, True, "bthd", [1000, 1]),                   # dense, group of 7
+    (24, 4, 128, cw.Pattern(100, 7, 700, 2), 256, 4, False, "bhtd", [1023, 650, 0]),              # pages over a tile, D < H
+    (6, 2, 128, cw.Pattern(30, 90, 1000, 4, kv_head_base=1, h_kv_global=4), 32, 32, False, "bthd", [999, 400]),
+    (40, 8, 128, cw.Pattern(128, 500, 4096, 8), 128, 32, False, "bhtd", [4095] * 3 + [17]),
+    (5, 1, 128, cw.Pattern(0, 1, 0, 1), 16, 4, False, "bthd", [40]),                              # one visible key
+    (3, 3, 64, cw.Pattern(10**6, 1, 10**6, 1), 40, 20, False, "bthd", [777, 39, 40]),             # all sink
+]
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,pat,ps,n,per_head,layout,pos", DECODE)
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_decode_matches_oracle(cuda_device, Hq, Hkv, d, pat, ps, n, per_head, layout, pos, e4m3):
+    if e4m3 and d != 128:
+        pytest.skip("E4M3 pages need d = 128")
+    B, rng = len(pos), np.random.default_rng(ps * n)
+    tab, n_pages = make_table(rng, B, n, heads=Hkv if per_head else None)
+    shape = (n_pages, ps, 1 if per_head else Hkv, d)
+    if e4m3:
+        kc, vc = (f8.f64_to_e4m3(rng.standard_normal(shape) * 3) for _ in range(2))
+        kd, vd = torch.from_numpy(kc).to(cuda_device), torch.from_numpy(vc).to(cuda_device)
+        k64, v64 = 0.4 * f8.e4m3_to_f64(kc), 0.25 * f8.e4m3_to_f64(vc)
+    else:
+        (k64, kd), (v64, vd) = (host_and_device(shape, x, cuda_device, 71) for x in ("k", "v"))
+    if layout == "bhtd":
+        kd, vd = kd.transpose(1, 2).contiguous(), vd.transpose(1, 2).contiguous()
+    q64, q = host_and_device((B, Hq, d), "q", cuda_device, 72)
+    fn = "cowa_decode_paged_fp8" if e4m3 else "cowa_decode_paged"
+    ws = ws_for(fn, pat, B, Hq, Hkv, d, n, ps, cuda_device)
+    o, lse = getattr(cw, fn)(q, kd, vd, torch.from_numpy(tab).to(cuda_device),
+                             torch.tensor(pos, dtype=torch.int32, device=cuda_device), pat,
+                             *((0.4, 0.25) if e4m3 else ()), layout=layout, workspace=ws)
+    assert cw.workspace_status(ws) == 0
+    k, _ = orp.gather_pages(k64, tab, n * ps)
+    v, _ = orp.gather_pages(v64, tab, n * ps)
+    assert_decoded(o, lse, q64, k, v, pos, pat, 2.0 ** -11 if e4m3 else 2.0 ** -8)
+
+
+def test_decode_equals_the_contiguous_decode(cuda_device):
+    """The same keys in one array per sequence: cowa_decode within both roundings."""
+    B, Hq, Hkv, d, Tc, ps = 3, 10, 2, 128, 2048, 64
+    pat = cw.Pattern(64, 300, 2048, 2)
+    kc, vc = (synth.cuda_normal_bf16((B, Hkv, Tc, d), synth.seed_of(x, 73), cuda_device) for x in ("k", "v"))
+    q = synth.cuda_normal_bf16((B, Hq, d), synth.seed_of("q", 73), cuda_device)
+    pos = torch.tensor([2047, 1000, 3], dtype=torch.int32, device=cuda_device)
+    pages = lambda x: x.view(B, Hkv, Tc // ps, ps, d).permute(0, 2, 1, 3, 4).reshape(-1, Hkv, ps, d).contiguous()
+    tab = torch.arange(B * Tc // ps, dtype=torch.int32, device=cuda_device).view(B, -1)
+    o, lse = cw.cowa_decode_paged(q, pages(kc), pages(vc), tab, pos, pat, layout="bhtd")
+    wo, wl = cw.cowa_decode(q, kc, vc, pos, pat)
+    assert (o.float() - wo.float()).abs().max() <= 2 * 2e-2
+    assert (lse - wl).abs().max() <= 2 * LSE_TOL
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("ps,layout", [(16, "bthd"), (64, "bhtd"), (24, "bthd")])
+def test_unseen_rows_may_hold_anything(cuda_device, e4m3, ps, layout):
+    """NaN and infinities in every row that no head sees, and pages of their own for each head, of which
+    only the needed ones are mapped: the same result, to the bit, as over clean pages."""
+    Hq, Hkv, d, n = 10, 2, 128, 512 // ps
+    pat, pos = cw.Pattern(20, 70, 500, 2), [500, 130, 60, 21, 0]
+    B, rng = len(pos), np.random.default_rng(74)
+    tab, n_pages = make_table(rng, B, n, heads=Hkv)
+    clean = tab.copy()
+    shape = (n_pages, ps, 1, d)
+    if e4m3:
+        pools = [torch.from_numpy(f8.f64_to_e4m3(rng.standard_normal(shape))).to(cuda_device) for _ in range(2)]
+        junk = [0x7f, 0xff]
+    else:
+        pools = [host_and_device(shape, x, cuda_device, 74)[1] for x in ("k", "v")]
+        junk = [float("nan"), float("inf")]
+    dirty = [p.clone() for p in pools]
+    for b in range(B):
+        for g in range(Hkv):
+            see = orc.visible_mask(np.array([pos[b]]), n * ps, oracle_pattern(pat), g, Hkv)[0]
+            for s in np.flatnonzero(~see):
+                for i, p in enumerate(dirty):
+                    p[int(tab[b, g, s // ps]), int(s % ps), 0] = junk[(i + int(s)) % 2]
+            tab[b, g, ~see.reshape(n, ps).any(1)] = [-1, 2**31 - 1, n_pages][g + 0 if b % 2 else 2]
+    for p in dirty:  # pages that no table names
+        p[torch.tensor(sorted(set(range(n_pages)) - set(tab[tab >= 0].tolist()) - {n_pages}), device=cuda_device)] = junk[0]
+    if layout == "bhtd":
+        pools, dirty = ([x.transpose(1, 2).contiguous() for x in y] for y in (pools, dirty))
+    q = synth.cuda_normal_bf16((B, Hq, d), synth.seed_of("q", 74), cuda_device)
+    fn = "cowa_decode_paged_fp8" if e4m3 else "cowa_decode_paged"
+    run = lambda pools, t, ws: getattr(cw, fn)(q, *pools, torch.from_numpy(t).to(cuda_device),
+                                               torch.tensor(pos, dtype=torch.int32, device=cuda_device), pat,
+                                               *((0.5, 0.5) if e4m3 else ()), layout=layout, workspace=ws)
+    ws = ws_for(fn, pat, B, Hq, Hkv, d, n, ps, cuda_device)
+    wo, wl = run(pools, clean, ws)
+    o, lse = run(dirty, tab, ws)
+    assert cw.workspace_status(ws) == 0
+    assert torch.isfinite(wo.float()).all()
+    assert torch.equal(o, wo) and torch.equal(lse, wl)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_bad_entries_are_left_out_and_reported(cuda_device, e4m3):
+    """Entries outside the pool on pages with visible keys: their keys are left out, the status says so
+    once, and a sequence whose every page is bad gives zeros and -inf."""
+    B, Hq, Hkv, d, ps, n = 4, 8, 2, 128, 16, 20
+    pat, pos = cw.Pattern(20, 70, 300, 2), [300, 250, 319, 15]
+    rng = np.random.default_rng(75)
+    tab, n_pages = make_table(rng, B, n)
+    tab[0, [1, 17]] = -1, n_pages
+    tab[1, 15] = 2**31 - 1
+    tab[3, :] = -2**31
+    shape = (n_pages, ps, Hkv, d)
+    if e4m3:
+        kc, vc = (f8.f64_to_e4m3(rng.standard_normal(shape) * 3) for _ in range(2))
+        kd, vd = torch.from_numpy(kc).to(cuda_device), torch.from_numpy(vc).to(cuda_device)
+        k64, v64 = f8.e4m3_to_f64(kc), f8.e4m3_to_f64(vc)
+    else:
+        (k64, kd), (v64, vd) = (host_and_device(shape, x, cuda_device, 75) for x in ("k", "v"))
+    q64, q = host_and_device((B, Hq, d), "q", cuda_device, 75)
+    fn = "cowa_decode_paged_fp8" if e4m3 else "cowa_decode_paged"
+    ws = ws_for(fn, pat, B, Hq, Hkv, d, n, ps, cuda_device)
+    o, lse = getattr(cw, fn)(q, kd, vd, torch.from_numpy(tab).to(cuda_device),
+                             torch.tensor(pos, dtype=torch.int32, device=cuda_device), pat,
+                             *((1.0, 1.0) if e4m3 else ()), workspace=ws)
+    assert cw.workspace_status(ws) == 8
+    assert cw.workspace_status(ws) == 0
+    k, has = orp.gather_pages(k64, tab, n * ps)
+    v, _ = orp.gather_pages(v64, tab, n * ps)
+    assert_decoded(o, lse, q64, k, v, pos, pat, 2.0 ** -11 if e4m3 else 2.0 ** -8, has=has)
+
+
+def test_growing_scores_rescale(cuda_device):
+    """Keys that grow along the sequence push the running maximum past its threshold again and again."""
+    B, Hq, Hkv, d, ps, n = 1, 8, 1, 128, 64, 32
+    pat, pos = cw.Pattern(0, 5000, 0, 1), [n * ps - 1]
+    _, k = host_and_device((n, ps, Hkv, d), "k", cuda_device, 76)
+    k = (k.float() * torch.linspace(0.1, 6, n, device=cuda_device)[:, None, None, None]).bfloat16()
+    k64 = to64(k)
+    v64, v = host_and_device((n, ps, Hkv, d), "v", cuda_device, 76)
+    q64, q = host_and_device((B, Hq, d), "q", cuda_device, 76)
+    tab = torch.arange(n, dtype=torch.int32, device=cuda_device)[None]
+    o, lse = cw.cowa_decode_paged(q, k, v, tab, torch.tensor(pos, dtype=torch.int32, device=cuda_device), pat)
+    flat = lambda x: x.transpose(2, 0, 1, 3).reshape(1, Hkv, n * ps, d)
+    # scores up to about 6 sqrt(d) / sqrt(d) * 5: their 32-bit sums are off by six times as much
+    go, gl = to64(o), lse.double().cpu().numpy()
+    s = q64[0] @ flat(k64)[0, 0].T / np.sqrt(d)
+    p = np.exp(s - s.max(1, keepdims=True))
+    want, A = p @ flat(v64)[0, 0] / p.sum(1, keepdims=True), p @ np.abs(flat(v64)[0, 0]) / p.sum(1, keepdims=True)
+    assert (np.abs(go[0] - want) <= 2.0 ** -8 * (A + np.abs(want)) + 6 * 2.0 ** -12 * A).all()
+    assert np.abs(gl[0] - (s.max(1) + np.log(p.sum(1)))).max() <= 6 * LSE_TOL
+
+
+def test_many_sequences_and_one_long_one(cuda_device):
+    """300 short sequences beside one of 40,000 positions: shares of the work that hold many pairs, and
+    pairs that many CTAs share; the same bits twice."""
+    B, Hq, Hkv, d, ps = 301, 2, 2, 64, 32
+    pat = cw.Pattern(40, 20000, 40000, 2)
+    pos = [int(x) for x in np.random.default_rng(77).integers(-1, 90, B)]
+    pos[150] = 39999
+    n = 40000 // ps
+    rng = np.random.default_rng(78)
+    n_pages = 3000
+    tab = rng.integers(0, n_pages, (B, n)).astype(np.int32)  # sequences may share pages
+    (k64, kd), (v64, vd) = (host_and_device((n_pages, ps, Hkv, d), x, cuda_device, 77) for x in ("k", "v"))
+    q64, q = host_and_device((B, Hq, d), "q", cuda_device, 77)
+    tabd, posd = torch.from_numpy(tab).to(cuda_device), torch.tensor(pos, dtype=torch.int32, device=cuda_device)
+    o, lse = cw.cowa_decode_paged(q, kd, vd, tabd, posd, pat)
+    o2, lse2 = cw.cowa_decode_paged(q, kd, vd, tabd, posd, pat)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    for b in list(range(0, 12)) + [149, 150, 151, 300]:
+        k, _ = orp.gather_pages(k64, tab[b:b + 1], pos[b] + 1 if pos[b] >= 0 else 1)
+        v, _ = orp.gather_pages(v64, tab[b:b + 1], pos[b] + 1 if pos[b] >= 0 else 1)
+        assert_decoded(o[b:b + 1], lse[b:b + 1], q64[b:b + 1], k, v, [pos[b]], pat)
+
+
+# ------------------------------------------------------------------------------------------ append
+APPEND = [
+    # Hq, Hkv, d, r, sections, interleaved, page, pages, per head, layout
+    (8, 4, 64, 64, (32,), False, 16, 6, False, "bthd"),
+    (5, 1, 128, 96, (20, 20, 8), False, 24, 5, False, "bhtd"),
+    (8, 2, 128, 128, (64,), True, 64, 2, True, "bthd"),
+    (4, 4, 64, 22, (6, 5), False, 8, 12, True, "bhtd"),
+    (0, 3, 128, 128, (64,), False, 32, 4, False, "bthd"),   # no queries
+    (6, 2, 128, 0, (), False, 16, 8, False, "bthd"),        # no rotation
+]
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,r,sec,inter,ps,n,per_head,layout", APPEND)
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("chunks", [False, True])
+def test_append_matches_oracle(cuda_device, Hq, Hkv, d, r, sec, inter, ps, n, per_head, layout, e4m3, chunks):
+    """Rows of several sequences, some of them padding, past the capacity or without a page: pages hold
+    exactly the rotated keys and the values (E4M3: the quantiser's codes, bit for bit), everything else
+    of pools and q_out stays as it was."""
+    if e4m3 and d != 128:
+        pytest.skip("E4M3 pages need d = 128")
+    rng = np.random.default_rng(81)
+    n_seq, cap = 5, n * ps
+    tab, n_pages = make_table(rng, n_seq, n, heads=Hkv if per_head else None)
+    tab[(0, 0, 1) if per_head else (0, 1)] = -1
+    tab[(2, Hkv - 1, 0) if per_head else (2, 0)] = n_pages
+    if chunks:
+        seq = np.repeat(np.arange(n_seq), [20, 1, cap, 3, 7])
+        pos = np.concatenate([np.arange(s, s + c) for s, c in zip((5, 0, 0, cap - 2, 9), (20, 1, cap, 3, 7))])
+        seq, pos = np.r_[seq, [-1, n_seq, 3, 3]], np.r_[pos, [0, 0, -1, -2**31]]
+    else:
+        seq, pos = None, np.array([0, cap - 1, cap // 2, -1, 2**31 - 1])
+    total = len(pos)
+    f, f64 = (cw.rope_frequencies(r, device=cuda_device), None) if r else (None, None)
+    rope = cw.Rope(f, sec, interleaved=inter) if r else None
+    rp = rng.integers(0, 5000, (max(1, len(sec)), total)).astype(np.int32)
+    qkv64, qkv = host_and_device((total, Hq + 2 * Hkv, d), "q", cuda_device, 81)
+    q, k, v = qkv.split([Hq, Hkv, Hkv], dim=1)
+    q64, k64, v64 = np.split(qkv64, [Hq, Hq + Hkv], axis=1)
+    shape = (n_pages, ps, 1 if per_head else Hkv, d)
+    view = (lambda x: x.transpose(1, 2).contiguous()) if layout == "bhtd" else (lambda x: x)
+    if e4m3:
+        pools = [view(torch.from_numpy(rng.integers(0, 255, shape).astype(np.uint8)).to(cuda_device)) for _ in range(2)]
+    else:
+        pools = [view(host_and_device(shape, x, cuda_device, 82)[1]) for x in ("k", "v")]
+    before = [p.clone() for p in pools]
+    i32 = lambda x: None if x is None else torch.from_numpy(x.astype(np.int32)).to(cuda_device)
+    q_out = torch.full((total, Hq, d), 7.0, dtype=torch.bfloat16, device=cuda_device) if Hq else None
+    args = dict(rope=rope, seq=i32(seq), rope_pos=i32(rp) if r else None, q_out=q_out, layout=layout)
+    if e4m3:
+        got = cw.paged_append_fp8(q if Hq else None, k, v, i32(pos), *pools, i32(tab), 0.02, 0.03, **args)
+    else:
+        got = cw.paged_append(q if Hq else None, k, v, i32(pos), *pools, i32(tab), **args)
+    assert got is q_out
+    fr = f.cpu().numpy() if r else None
+    turn = (lambda x: orp.rope(x, rp, fr, sec, inter)) if r else (lambda x: x)
+    kr, qr = turn(k64), turn(q64)
+    row_seq = seq if seq is not None else np.arange(total)
+    live = (pos >= 0) & (row_seq >= 0) & (row_seq < n_seq)
+    if Hq:
+        g = to64(q_out)
+        assert (g[~live] == 7.0).all()
+        assert_rotated(g[live], q64[live], qr[live], r, inter) if r else np.testing.assert_array_equal(g[live], q64[live])
+    back = (lambda x: x.transpose(1, 2)) if layout == "bhtd" else (lambda x: x)
+    want_at = {}
+    for i in np.flatnonzero(live):
+        for h in range(Hkv):
+            if pos[i] >= cap:
+                continue
+            page = (tab[row_seq[i], h] if per_head else tab[row_seq[i]])[pos[i] // ps]
+            if 0 <= page < n_pages:
+                want_at[(int(page), int(pos[i] % ps), 0 if per_head else h)] = (i, h)
+    for pool, was, new, scale in zip(pools, before, (kr, v64), (0.02, 0.03)):
+        now, old = back(pool).cpu(), back(was).cpu().clone()
+        idx = np.array(list(want_at)).reshape(-1, 3).T
+        src = np.array(list(want_at.values())).reshape(-1, 2).T
+        rows = new[src[0], src[1]]
+        if e4m3:
+            codes = f8.quantize_e4m3_f32(rows.astype(np.float32), scale)
+            np.testing.assert_array_equal(now.numpy()[tuple(idx)], codes)
+            old.numpy()[tuple(idx)] = codes
+            np.testing.assert_array_equal(now.numpy(), old.numpy())
+        else:
+            have = now[tuple(torch.from_numpy(idx))]
+            if new is kr and r:
+                assert_rotated(to64(have)[:, None], k64[src[0], src[1]][:, None], rows[:, None], r, inter)
+            else:
+                np.testing.assert_array_equal(to64(have), rows)
+            old[tuple(torch.from_numpy(idx))] = have
+            assert torch.equal(now, old)
+
+
+def test_append_rotates_queries_in_place(cuda_device):
+    f = cw.rope_frequencies(128, device=cuda_device)
+    q, k, v = (synth.cuda_normal_bf16((9, h, 128), synth.seed_of(n, 83), cuda_device) for n, h in (("q", 4), ("k", 2), ("v", 2)))
+    pos = torch.arange(9, dtype=torch.int32, device=cuda_device)
+    tab = torch.zeros((9, 1), dtype=torch.int32, device=cuda_device) + torch.arange(9, device=cuda_device, dtype=torch.int32)[:, None]
+    kp, vp = (torch.zeros((9, 16, 2, 128), dtype=torch.bfloat16, device=cuda_device) for _ in range(2))
+    want = cw.paged_append(q, k, v, pos, kp, vp, tab, rope=cw.Rope(f))
+    got = cw.paged_append(q, k, v, pos, kp, vp, tab, rope=cw.Rope(f), q_out=q)
+    assert got is q and torch.equal(q, want)
+
+
+# ------------------------------------------------------------------------------------------ together
+@pytest.mark.parametrize("per_head,layout,ps", [(False, "bhtd", 32), (True, "bthd", 16)])
+def test_prompt_then_decode_steps(cuda_device, per_head, layout, ps):
+    """A prompt written to pages, then tokens appended and decoded one by one, heads giving back the pages
+    they no longer need: every step against the fp64 row of the whole sequence's attention."""
+    B, Hq, Hkv, d, N0, steps = 2, 8, 2, 128, 200, 60
+    pat = cw.Pattern(20, 40, 300, 2)
+    f = cw.rope_frequencies(d, device=cuda_device)
+    rope, fr = cw.Rope(f), f.cpu().numpy()
+    N = N0 + steps
+    (q64, q), (k64, k), (v64, v) = (host_and_device((B, N, h, d), n, cuda_device, 84)
+                                    for n, h in (("q", Hq), ("k", Hkv), ("v", Hkv)))
+    n = -(-N // ps)
+    tab, n_pages = make_table(np.random.default_rng(84), B, n, heads=Hkv if per_head else None)
+    shape = (n_pages, ps, 1 if per_head else Hkv, d) if layout == "bthd" else (n_pages, 1 if per_head else Hkv, ps, d)
+    kp, vp = (torch.full(shape, float("nan"), dtype=torch.bfloat16, device=cuda_device) for _ in range(2))
+    tabd = torch.from_numpy(tab).to(cuda_device)
+    flat = lambda x: x[:, :N0].reshape(B * N0, -1, d)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=cuda_device)
+    cw.paged_append(flat(q), flat(k), flat(v), i32(list(range(N0)) * B), kp, vp, tabd, rope=rope,
+                    seq=i32([b for b in range(B) for _ in range(N0)]), layout=layout)
+    turn = lambda x: np.stack([orp.rope(x[b], np.arange(N)[None], fr) for b in range(B)])
+    # the cache holds bf16 keys and the queries are bf16: what the attention is computed on
+    bf = lambda x: orc.bf16_bits_to_f64(synth.f32_to_bf16_bits(x.astype(np.float32)))
+    qr, kr = bf(turn(q64)), bf(turn(k64))
+    ws = ws_for("cowa_decode_paged", pat, B, Hq, Hkv, d, n, ps, cuda_device)
+    for t in range(N0, N):
+        pos = i32([t] * B)
+        qt = cw.paged_append(q[:, t], k[:, t], v[:, t], pos, kp, vp, tabd, rope=rope, layout=layout)
+        o, lse = cw.cowa_decode_paged(qt, kp, vp, tabd, pos, pat, layout=layout, workspace=ws)
+        if per_head and t % 7 == 0:  # give pages back, and let somebody write to them
+            for g, keep in enumerate(cw.pages_needed(pat, Hkv, ps, n, t + 1)):
+                gone = tabd[:, g, torch.from_numpy(~keep).to(cuda_device)].long().reshape(-1)
+                kp[gone[gone >= 0]] = float("nan")
+                vp[gone[gone >= 0]] = float("inf")
+                tabd[:, g, torch.from_numpy(~keep).to(cuda_device)] = -1
+        # a key or query next to a rounding border may differ by a bf16 step from the oracle's
+        c = lambda x: x[:, :t + 1].transpose(0, 2, 1, 3)
+        go, gl = to64(o), lse.double().cpu().numpy()
+        wo, wl = orc.decode(qr[:, t], c(kr), c(v64), [t] * B, oracle_pattern(pat))
+        assert np.abs(go - wo).max() <= 2e-2, t
+        assert np.abs(gl - wl).max() <= 1e-3, t
+    assert cw.workspace_status(ws) == 0
+
+
+def test_step_in_two_graphs_that_share_a_workspace(cuda_device):
+    """append + decode captured twice, over two caches, with one workspace: replayed in turn, each gives
+    the bits of the direct calls; and on a stream of their own, next to each other with two workspaces."""
+    B, Hq, Hkv, d, ps, n = 4, 10, 2, 128, 32, 64
+    pat = cw.Pattern(64, 300, 2048, 2)
+    rope = cw.Rope(cw.rope_frequencies(d, device=cuda_device))
+    pos = torch.tensor([2047, 31, 1000, -1], dtype=torch.int32, device=cuda_device)
+    tab = torch.randperm(B * n, device=cuda_device).int().view(B, n)
+    size = 1 << 23
+    sets = []
+    for x in range(2):
+        r = lambda *s, nm: synth.cuda_normal_bf16(s, synth.seed_of(nm, 90 + x), cuda_device)
+        sets.append(dict(q=r(B, Hq, d, nm="q"), k=r(B, Hkv, d, nm="k"), v=r(B, Hkv, d, nm="v"),
+                         kp=r(B * n, ps, Hkv, d, nm="k_cache"), vp=r(B * n, ps, Hkv, d, nm="v_cache"),
+                         qo=torch.zeros((B, Hq, d), dtype=torch.bfloat16, device=cuda_device),
+                         o=torch.zeros((B, Hq, d), dtype=torch.bfloat16, device=cuda_device),
+                         lse=torch.zeros((B, Hq), device=cuda_device),
+                         ws=torch.zeros(size, dtype=torch.uint8, device=cuda_device)))
+
+    def step(s, ws, stream=None):
+        cw.paged_append(s["q"], s["k"], s["v"], pos, s["kp"], s["vp"], tab, rope=rope, q_out=s["qo"], stream=stream)
+        cw.cowa_decode_paged(s["qo"], s["kp"], s["vp"], tab, pos, pat, out=s["o"], lse=s["lse"], workspace=ws, stream=stream)
+
+    want = []
+    for s in sets:
+        step(s, s["ws"])
+        torch.cuda.synchronize()
+        want.append((s["o"].clone(), s["lse"].clone()))
+    graphs = []
+    for s in sets:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step(s, sets[0]["ws"])
+        graphs.append(g)
+    for _ in range(3):
+        for s in sets:
+            s["o"].zero_(), s["lse"].zero_()
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for s, (o, lse) in zip(sets, want):
+            assert torch.equal(s["o"], o) and torch.equal(s["lse"], lse)
+    streams = [torch.cuda.Stream() for _ in sets]
+    for s in sets:
+        s["o"].zero_()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, st in zip(sets, streams):
+            step(s, s["ws"], st)
+    torch.cuda.synchronize()
+    for s, (o, lse) in zip(sets, want):
+        assert torch.equal(s["o"], o) and torch.equal(s["lse"], lse)
+        assert cw.workspace_status(s["ws"]) == 0
+    # a workspace that the call allocates belongs to the call's stream
+    o, lse = cw.cowa_decode_paged(sets[0]["qo"], sets[0]["kp"], sets[0]["vp"], tab, pos, pat, stream=streams[1])
+    streams[1].synchronize()
+    assert torch.equal(o, want[0][0]) and torch.equal(lse, want[0][1])
+
+
+def test_refusals_of_the_binding(cuda_device):
+    q = torch.zeros((2, 4, 64), dtype=torch.bfloat16, device=cuda_device)
+    k = torch.zeros((2, 2, 64), dtype=torch.bfloat16, device=cuda_device)
+    pool = torch.zeros((6, 16, 2, 64), dtype=torch.bfloat16, device=cuda_device)
+    tab = torch.zeros((2, 3), dtype=torch.int32, device=cuda_device)
+    pos = torch.zeros(2, dtype=torch.int32, device=cuda_device)
+    pat = cw.Pattern(4, 8, 48, 2)
+    dec = lambda **c: cw.cowa_decode_paged(**{**dict(q_t=q, k_pages=pool, v_pages=pool, page_table=tab, pos=pos,
+                                                     pattern=pat), **c})
+    app = lambda **c: cw.paged_append(**{**dict(q=q, k=k, v=k, pos=pos, k_pages=pool, v_pages=pool, page_table=tab), **c})
+    for bad in (dict(page_table=tab[:1]), dict(pos=pos[:1]), dict(layout="thbd"), dict(v_pages=pool[:5]),
+                dict(page_table=torch.zeros((2, 2, 3), dtype=torch.int32, device=cuda_device)),
+                dict(page_table=tab.t().contiguous().t()), dict(out=q[:1]), dict(lse=torch.zeros(2, 4)),
+                dict(q_t=q.transpose(0, 1)), dict(lse=torch.zeros((2, 4), dtype=torch.float64, device=cuda_device))):
+        with pytest.raises(ValueError):
+            dec(**bad)
+    for bad in (dict(pos=pos.long()), dict(page_table=tab.long()), dict(k_pages=pool.float()), dict(out=q.half())):
+        with pytest.raises(TypeError):
+            dec(**bad)
+    with pytest.raises(cw.CowaError):
+        dec(workspace=torch.zeros(300, dtype=torch.uint8, device=cuda_device))
+    with pytest.raises(cw.CowaError):  # pages of 12 positions
+        dec(k_pages=pool[:, :12].contiguous(), v_pages=pool[:, :12].contiguous())
+    with pytest.raises(cw.CowaError):  # E4M3 needs d = 128
+        cw.cowa_decode_paged_fp8(q, pool.to(torch.uint8), pool.to(torch.uint8), tab, pos, pat, 1.0, 1.0)
+    for bad in (dict(v=k[:1]), dict(q=q[:1]), dict(pos=pos[:1]), dict(seq=pos[:1]), dict(q_out=q[:, :2]),
+                dict(rope_pos=pos), dict(k_pages=pool[:, :, :1], v_pages=pool[:, :, :1])):
+        with pytest.raises(ValueError):
+            app(**bad)
+    with pytest.raises(cw.CowaError):  # more rows than sequences, and no seq
+        app(page_table=tab[:1])
+    with pytest.raises(TypeError):
+        app(v_pages=pool.half())
