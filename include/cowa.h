@@ -416,6 +416,23 @@ cowa_status cowa_decode_paged_fp8(const cowa_pattern* pat, int B, int H_q, int H
                                   cowa_page_table table, const int32_t* pos, void* o, float* lse_or_null, void* ws,
                                   size_t ws_bytes, void* stream);
 
+/* The forward for a packed batch of query chunks over the pages: sequence s has the query rows
+ * cu_seqlens[s] .. cu_seqlens[s+1]-1 of q [total, H_q, d], the first at position q_start[s], against its
+ * keys at positions 0 .. q_start[s] + len_s - 1, the chunk's own among them (cowa_paged_append first).
+ * Outputs o [total, H_q, d] and lse fp32 [H_q, total] as cowa_fwd_varlen, whose rules hold for
+ * cu_seqlens (device int32 [n_seq + 1]), strides and workspace; rows behind the last sequence are left
+ * as they are.  q_start: device int32 [n_seq], clamped into [0, capacity - len_s] (rows of a sequence
+ * longer than the capacity see the keys there are).  Bad entries of pages with visible keys as for
+ * cowa_decode_paged; a row that sees nothing has o 0 and lse -inf.  Entries of pages that a query tile
+ * of 128 rows does not see are not read.  Keys and values below q_start[s] + len_s on mapped pages must
+ * be finite where they share a tile of 128 positions with visible ones; what stands behind them is
+ * never used.  bf16 pages only.  The workspace's first 256 bytes must be zero before its first call. */
+size_t cowa_fwd_paged_workspace_size(const cowa_pattern* pat, int n_seq, int total, int H_q, int H_kv, int d);
+cowa_status cowa_fwd_paged(const cowa_pattern* pat, int n_seq, int total, int H_q, int H_kv, int d,
+                           const int32_t* cu_seqlens, const int32_t* q_start, cowa_tensor q, cowa_tensor k_pages,
+                           cowa_tensor v_pages, cowa_page_table table, cowa_tensor o, float* lse, void* ws,
+                           size_t ws_bytes, void* stream);
+
 /* ---- status --------------------------------------------------------------------------------
  * Synchronizes `stream`, reads and clears the device status word in `ws` (the workspace of an
  * earlier call), and returns COWA_OK, COWA_ERR_TIMEOUT, COWA_ERR_PAGE (paged calls), or (debug

@@ -7,10 +7,10 @@ backward kernels, a split-KV decode kernel); `cowa` is its ctypes binding.
 from .cowa import (CowaError, Pattern, Rope, compact_append, compact_cache, compact_rows, cowa_bwd,  # noqa: F401
                    cowa_bwd_varlen,
                    cowa_decode, cowa_decode_compact, cowa_decode_paged, cowa_decode_paged_fp8, cowa_fwd, cowa_fwd_chunk,
-                   cowa_fwd_varlen, cowa_rope, cowa_rope_bwd, lib, paged_append, paged_append_fp8, pages_needed,
+                   cowa_fwd_paged, cowa_fwd_varlen, cowa_rope, cowa_rope_bwd, lib, paged_append, paged_append_fp8, pages_needed,
                    plan_debug, rope_frequencies, visible_counts, workspace_status)
 
 __all__ = ["Pattern", "CowaError", "cowa_fwd", "cowa_fwd_chunk", "cowa_fwd_varlen", "cowa_bwd", "cowa_bwd_varlen", "cowa_decode", "cowa_decode_compact",
            "compact_rows", "compact_cache", "compact_append", "lib", "plan_debug", "visible_counts",
            "workspace_status", "Rope", "rope_frequencies", "cowa_rope", "cowa_rope_bwd", "paged_append",
-           "paged_append_fp8", "cowa_decode_paged", "cowa_decode_paged_fp8", "pages_needed"]
+           "paged_append_fp8", "cowa_decode_paged", "cowa_decode_paged_fp8", "cowa_fwd_paged", "pages_needed"]

@@ -17,7 +17,7 @@ cowa_fwd_varlen, cowa_bwd, cowa_bwd_varlen, cowa_decode, cowa_decode_compact (wi
 compact_append), the E4M3-cache decodes (cowa_decode_fp8, cowa_decode_fp8_compact, with
 quantize_e4m3, compact_cache_fp8, compact_append_fp8), cowa_decode_noalloc, the rotary positions
 (cowa_rope, cowa_rope_bwd), the paged cache (paged_append, cowa_decode_paged, their E4M3 forms
-paged_append_fp8, cowa_decode_paged_fp8, and pages_needed), plus the planner introspection helpers.
+paged_append_fp8, cowa_decode_paged_fp8, cowa_fwd_paged and pages_needed), plus the planner introspection helpers.
 """
 
 from __future__ import annotations
@@ -172,6 +172,10 @@ def lib() -> ctypes.CDLL:
     L.cowa_decode_paged_fp8_workspace_size.restype = sz
     L.cowa_decode_paged_fp8.argtypes = [P, i, i, i, i, vp, T, T, f, f, PT, vp, vp, vp, vp, sz, vp]
     L.cowa_decode_paged_fp8.restype = i
+    L.cowa_fwd_paged_workspace_size.argtypes = [P, i, i, i, i, i]
+    L.cowa_fwd_paged_workspace_size.restype = sz
+    L.cowa_fwd_paged.argtypes = [P, i, i, i, i, i, vp, vp, T, T, T, PT, T, vp, vp, sz, vp]
+    L.cowa_fwd_paged.restype = i
     L.cowa_workspace_status.argtypes = [vp, vp]
     L.cowa_workspace_status.restype = i
     L.cowa_status_string.argtypes = [i]
@@ -873,6 +877,49 @@ def cowa_decode_paged_fp8(q_t, k_pages, v_pages, page_table, pos, pattern: Patte
     _u8_cuda("v_pages", v_pages)
     return _decode_paged("cowa_decode_paged_fp8", q_t, k_pages, v_pages, page_table, pos, pattern,
                          (float(k_scale), float(v_scale)), layout, out, lse, workspace, stream, want_lse)
+
+
+def cowa_fwd_paged(q, k_pages, v_pages, page_table, cu_seqlens, q_start, pattern: Pattern, layout: str = "bthd",
+                   out=None, lse=None, workspace=None, stream=None):
+    """Packed query chunks over a paged cache that already holds their keys: q [total, H_q, d],
+    cu_seqlens CUDA int32 [n_seq + 1], q_start CUDA int32 [n_seq] the position of each chunk's first row;
+    pools and page_table as for paged_append (bf16).  Returns o [total, H_q, d] bf16 and lse [H_q, total]
+    fp32."""
+    import torch
+
+    for n_, x_ in (("q", q), ("k_pages", k_pages), ("v_pages", v_pages)):
+        _bf16_cuda(n_, x_)
+    total, Hq, d = q.shape
+    if layout not in ("bthd", "bhtd") or k_pages.dim() != 4 or page_table.dim() not in (2, 3):
+        raise ValueError("k_pages is 4-D in layout 'bthd' or 'bhtd', page_table [n_seq, max_pages] or [n_seq, H_kv, max_pages]")
+    n_seq = page_table.shape[0]
+    Hkv = page_table.shape[1] if page_table.dim() == 3 else k_pages.shape[2 if layout == "bthd" else 1]
+    kp, vp, tab = _pages(k_pages, v_pages, page_table, layout, Hkv, d)
+    _int32("cu_seqlens", cu_seqlens, (n_seq + 1,))
+    _int32("q_start", q_start, (n_seq,))
+    if out is not None:
+        _bf16_cuda("out", out)
+        if out.shape != q.shape:
+            raise ValueError("out must have the shape of q")
+    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (Hq, total) or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous float32 [H_q, total] tensor")
+    _same_device(q, k_pages=k_pages, v_pages=v_pages, page_table=page_table, cu_seqlens=cu_seqlens, q_start=q_start,
+                 out=out, lse=lse, workspace=workspace)
+    pat = pattern.c()
+    L = lib()
+    with _launch_on(q, stream):
+        if out is None:
+            out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        if lse is None:
+            lse = torch.empty((Hq, total), dtype=torch.float32, device=q.device)
+        if workspace is None:
+            workspace = _workspace(L.cowa_fwd_paged_workspace_size(ctypes.byref(pat), n_seq, total, Hq, Hkv, d), q.device)
+        t4 = lambda x: _t4(x.unsqueeze(0))
+        _check("cowa_fwd_paged", L.cowa_fwd_paged(ctypes.byref(pat), n_seq, total, Hq, Hkv, d, cu_seqlens.data_ptr(),
+                                                  q_start.data_ptr(), t4(q), kp, vp, tab, t4(out), lse.data_ptr(),
+                                                  workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                                  _stream(None)))
+    return out, lse
 
 
 def decode_noalloc_status(stream=None) -> int:

@@ -831,6 +831,46 @@ cowa_status decode_paged(const cowa_pattern* pat, int B, int Hq, int Hkv, int d,
 }
 }  // namespace
 
+size_t cowa_fwd_paged_workspace_size(const cowa_pattern* pat, int n_seq, int total, int H_q, int H_kv, int d) {
+  return cowa_fwd_varlen_workspace_size(pat, n_seq, total, H_q, H_kv, d);
+}
+
+cowa_status cowa_fwd_paged(const cowa_pattern* pat, int n_seq, int total, int Hq, int Hkv, int d,
+                           const int32_t* cu_seqlens, const int32_t* q_start, cowa_tensor q, cowa_tensor k_pages,
+                           cowa_tensor v_pages, cowa_page_table table, cowa_tensor o, float* lse, void* ws,
+                           size_t ws_bytes, void* stream) {
+  Pat p;
+  COWA_TRY(check_pattern(pat, Hkv, &p));
+  COWA_TRY(check_heads(1, total, Hq, Hkv, d));
+  if (n_seq < 1 || !cu_seqlens || !q_start || !lse) return COWA_ERR_INVALID_ARG;
+  for (const void* x : {(const void*)cu_seqlens, (const void*)q_start, (const void*)lse})
+    if (reinterpret_cast<uintptr_t>(x) & 3u) return COWA_ERR_ALIGNMENT;
+  for (const cowa_tensor* t : {&q, &k_pages, &v_pages, &o}) COWA_TRY(check_tensor(*t));
+  FwdArgs a;
+  memset(&a, 0, sizeof(a));
+  COWA_TRY(check_page_table(table, n_seq, &a.tab));
+  COWA_TRY(check_ws(ws, ws_bytes, cowa_fwd_paged_workspace_size(pat, n_seq, total, Hq, Hkv, d)));
+  a.pat = p; a.B = 1; a.Hq = Hq; a.Hkv = Hkv; a.d = d;
+  a.Nq = total; a.Nk = total;
+  a.varlen = 1; a.n_seq = n_seq; a.total = total; a.cu_seqlens = cu_seqlens;
+  a.seq_tab = reinterpret_cast<int32_t*>(reinterpret_cast<char*>(ws) + kWsHeader);
+  a.paged = 1;
+  a.q_start = q_start;
+  a.box_rows = page_box_rows(table.page_size, 128);
+  a.o = o.ptr; a.o_st = o.stride_t; a.o_sh = o.stride_h;
+  a.lse = lse;
+  a.status = reinterpret_cast<uint32_t*>(ws);
+  a.scale_log2 = scale_of(pat, d) * 1.4426950408889634f;
+  const int h = table.per_head ? 1 : Hkv;
+  if (!make_tmap_bf16(&a.tm_q, q.ptr, d, total, Hq, 1, q.stride_t, q.stride_h, q.stride_b, 128) ||
+      !make_tmap_bf16(&a.tm_k, k_pages.ptr, d, table.page_size, h, table.n_pages, k_pages.stride_t, k_pages.stride_h,
+                      k_pages.stride_b, a.box_rows) ||
+      !make_tmap_bf16(&a.tm_v, v_pages.ptr, d, table.page_size, h, table.n_pages, v_pages.stride_t, v_pages.stride_h,
+                      v_pages.stride_b, a.box_rows))
+    return COWA_ERR_CUDA;
+  return launch_fwd(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? COWA_OK : COWA_ERR_CUDA;
+}
+
 cowa_status cowa_pages_needed(const cowa_pattern* pat, int Hkv, int page_size, int n, int pos, uint8_t* out) {
   Pat p;
   if (Hkv < 1) return COWA_ERR_INVALID_ARG;

@@ -14,6 +14,10 @@
 // The same kernel serves a block of queries at an offset against keys already written
 // (chunked prefill: query rows q_off.., keys 0..Nk-1) and packed variable-length batches (each
 // CTA finds its sequence in per-sequence tile offsets and works on that sequence's rows).
+// PAGED: a packed batch of query chunks against a paged cache.  The K/V tiles keep their places
+// (128 positions each); the producer warp looks up the pages of a tile, one lane per TMA box of 8 to
+// 128 rows, and fetches the boxes that some row of the query tile sees.  V rows that are not fetched,
+// or lie past the last key, are zeroed (their P is 0, but 0 times what memory holds may be NaN).
 // Registers: the kernel is compiled for 168 per thread (384 * 168 = 64512 at launch); the two
 // softmax warpgroups then raise theirs to 216 and the third lowers to 72
 // (2*128*216 + 128*72 = 64512), so a whole 128-column score row stays in registers.  The
@@ -56,6 +60,7 @@ static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsOther == kFwdThreads * kRegsLa
 constexpr int kRingMax = 8;
 constexpr int kProducerWarp = 8, kMmaWarp = 9;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
+constexpr int kBadRing = 16;  // more than the tiles between the producer and the softmax (kRingMax / 2 + 2)
 
 template <int D>
 struct FwdGeom {
@@ -71,7 +76,7 @@ struct FwdGeom {
   static constexpr int kColO = 256;
 };
 
-template <int D>
+template <int D, bool PAGED>
 __global__ void __launch_bounds__(kFwdThreads, 1) cowa_fwd_kernel(const __grid_constant__ FwdArgs a) {
   using Geo = FwdGeom<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -85,6 +90,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cowa_fwd_kernel(const __grid_c
   __shared__ float merge_m[kBM], merge_l[kBM];
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_flag;
+  // PAGED: per tile (a ring that the producer cannot lap), the 8-row groups whose page is bad; and
+  // the barrier on which a V tile lands that still needs rows zeroed
+  __shared__ uint32_t bad_rows[PAGED ? kBadRing : 1];
+  __shared__ __align__(8) uint64_t landed;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -93,6 +102,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cowa_fwd_kernel(const __grid_c
   const int npair = (grp + 1) >> 1;
   const int per_i = a.B * a.Hkv * npair;
   int i, row0 = 0, Nq = a.Nq, Nk = a.Nk, q_off = a.q_off;  // row0: first row of the sequence
+  int pg_seq = 0;
   if (!a.varlen) {
     i = (a.Nq + kBM - 1) / kBM - 1 - (int)(blockIdx.x / per_i);
   } else {
@@ -105,6 +115,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cowa_fwd_kernel(const __grid_c
     row0 = a.seq_tab[a.n_seq + 1 + sq];
     Nq = Nk = a.seq_tab[2 * a.n_seq + 1 + sq];
     q_off = 0;
+    if constexpr (PAGED) {
+      const int cap = a.tab.max_pages * a.tab.page_size;
+      pg_seq = sq;
+      q_off = imax(0, imin(a.q_start[sq], cap - Nq));
+      Nk = imin(q_off + Nq, cap);
+    }
   }
   int rem = blockIdx.x % per_i;
   const int pair = rem % npair; rem /= npair;
@@ -115,7 +131,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cowa_fwd_kernel(const __grid_c
   // query rows of the tile: local q rows [i*BM, ...), absolute positions [t0, t1)
   const int t0 = q_off + i * kBM, t1 = imin(q_off + Nq, t0 + kBM);
   const Range iv = interval_of(a.pat, g);
-  const Tiles T = plan_tiles(a.pat, iv, t0, t1);
+  // (a paged sequence longer than its cache: its last rows see the keys that there are)
+  const Tiles T = plan_tiles(a.pat, iv, t0, PAGED ? imin(t1, Nk) : t1);
 
   uint8_t* sQ = smem + Geo::kOffQ;
   uint8_t* sRing = smem + Geo::kOffRing;
@@ -130,6 +147,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cowa_fwd_kernel(const __grid_c
     }
     ptx::mbar_init(&mma_final, 1);
     ptx::mbar_init(&merge_ready, 4);
+    if (PAGED) ptx::mbar_init(&landed, 1);
     abort_flag = 0;
     ptx::fence_mbar_init();
   }
@@ -148,7 +166,93 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cowa_fwd_kernel(const __grid_c
   }
   if (warp == kProducerWarp) {
     // ------------------------------------------------------------------ TMA producer
-    if (lane == 0) {
+    if constexpr (PAGED) {
+      if (lane == 0) {
+        ptx::mbar_arrive_expect_tx(&q_full, (has1 ? 2 : 1) * Geo::kQBytes);
+        for (int u = 0; u < D / 64; ++u) {
+          ptx::tma_load_4d(sQ + u * 16384, &a.tm_q, &q_full, u * 64, row0 + i * kBM, h0, 0);
+          if (has1) ptx::tma_load_4d(sQ + Geo::kQBytes + u * 16384, &a.tm_q, &q_full, u * 64, row0 + i * kBM, h0 + 1, 0);
+        }
+      }
+      const int rows = a.box_rows, nbox = kBN / rows;
+      const int32_t* table = a.tab.ptr + pg_seq * a.tab.sb + g * a.tab.sh;
+      const int tl = imin(t1, Nk);
+      TileCursor cur;
+      cur.init(T);
+      int page = -1, slot = 0;
+      bool want = false;
+      auto look = [&](int j) {  // the page of box `lane` of key tile j, if some row of the query tile sees a key in it
+        const int p = j * kBN + lane * rows, e = imin(p + rows, tl);
+        want = lane < nbox && p < e && (p < a.pat.S || e > t0 - a.pat.L + 1 || (p < iv.hi && e > iv.lo));
+        page = -1;
+        slot = 0;
+        if (want) {
+          const int x = p / a.tab.page_size;
+          slot = p - x * a.tab.page_size;
+          page = table[x];
+        }
+      };
+      if (ntiles > 0) look(cur.j);
+      int issued = 0, fixed = -1;
+      bool ok = true;
+      for (int n = 0; ok && n < ntiles; ++n) {
+        const int j = cur.j;
+        const bool good = want && page >= 0 && page < a.tab.n_pages;
+        const uint32_t fetch = __ballot_sync(0xffffffffu, good), bad = __ballot_sync(0xffffffffu, want && !good);
+        const int my_page = page, my_slot = slot;
+        cur.next(T);
+        if (n + 1 < ntiles) look(cur.j);  // the next tile's pages, while this one waits for its slots
+        const int bytes = __popc(fetch) * rows * 128 * (D / 64);
+        uint32_t lost = 0;
+        if (bad) {
+          for (int x = 0; x < nbox; ++x)
+            if ((bad >> x) & 1) lost |= ((1u << (rows / 8)) - 1) << (x * (rows / 8));
+          if (lane == 0) a.status[3] = 1u;
+        }
+        for (int is_v = 0; is_v < 2; ++is_v) {
+          const int idx = 2 * n + is_v, s = idx % Geo::kRing;
+          if (idx >= Geo::kRing &&
+              !(ok = ptx::mbar_wait_warp(&kv_empty[s], ((idx / Geo::kRing) - 1) & 1, &abort_flag, a.status)))
+            break;
+          uint8_t* dst = sRing + s * Geo::kKVBytes;
+          // rows of V past the last key: the tile lands on a barrier of its own and they are zeroed
+          const bool tail = is_v && tl - j * kBN < kBN;
+          uint64_t* bar = tail ? &landed : &kv_full[s];
+          if (is_v && __popc(fetch) < nbox) {
+            for (int x = lane; x < kBN * 8; x += 32)  // 16-byte pieces of 128 rows
+              if (!((fetch >> (x / 8 / rows)) & 1))
+                for (int u = 0; u < D / 64; ++u) *reinterpret_cast<uint4*>(dst + u * 16384 + x * 16) = make_uint4(0, 0, 0, 0);
+            ptx::fence_proxy_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) {
+            if (!is_v) bad_rows[n % kBadRing] = lost;
+            ptx::mbar_arrive_expect_tx(bar, bytes);
+          }
+          __syncwarp();
+          if (good) {
+            for (int u = 0; u < D / 64; ++u)
+              ptx::tma_load_4d(dst + u * 16384 + lane * rows * 128, is_v ? &a.tm_v : &a.tm_k, bar, u * 64, my_slot,
+                               a.tab.sh ? 0 : g, my_page);
+          }
+          issued = idx + 1;
+          if (tail) {
+            // the last key tile (tiles come in order), so nothing is left to fetch meanwhile
+            if (!(ok = ptx::mbar_wait_warp(&landed, 0, &abort_flag, a.status))) { fixed = idx; break; }
+            for (int x = (tl - j * kBN) * 8 + lane; x < kBN * 8; x += 32)
+              for (int u = 0; u < D / 64; ++u) *reinterpret_cast<uint4*>(dst + u * 16384 + x * 16) = make_uint4(0, 0, 0, 0);
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&kv_full[s]);
+          }
+        }
+      }
+      // drain: no copy may still be landing in shared memory when the CTA exits
+      ptx::mbar_wait(&q_full, 0, nullptr, a.status);
+      for (int idx = (issued > Geo::kRing ? issued - Geo::kRing : 0); idx < issued; ++idx)
+        ptx::mbar_wait(idx == fixed ? &landed : &kv_full[idx % Geo::kRing], idx == fixed ? 0 : (idx / Geo::kRing) & 1,
+                       nullptr, a.status);
+    } else if (lane == 0) {
       ptx::tma_prefetch_desc(&a.tm_q);
       ptx::tma_prefetch_desc(&a.tm_k);
       ptx::tma_prefetch_desc(&a.tm_v);
@@ -337,14 +441,20 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cowa_fwd_kernel(const __grid_c
       for (int n = 0; n < ntiles; ++n, cur.next(T)) {
         if (split && (n & 1) != k) continue;
         const int s0 = cur.j * kBN;
-        const bool need_mask = (s0 + kBN > Nk) || !tile_full(a.pat, iv, t0, t1, s0, imin(Nk, s0 + kBN));
+        bool need_mask = (s0 + kBN > Nk) || !tile_full(a.pat, iv, t0, t1, s0, imin(Nk, s0 + kBN));
         if (!(ok = ptx::mbar_wait_warp(&s_full[k], cnt & 1, &abort_flag, a.status))) break;
         ptx::tc_fence_after();
         // visible key columns of row t within [s0, s0+128), relative to s0 (partial tiles only)
-        const int sink_end = imin(a.pat.S, t + 1) - s0;
+        const int t_end = PAGED ? imin(t + 1, Nk) : t + 1;
+        const int sink_end = imin(a.pat.S, t_end) - s0;
         const int band_lo = imax(0, t - a.pat.L + 1) - s0;
-        const int diag_end = t + 1 - s0;
-        const int lr_lo = iv.lo - s0, lr_hi = imin(iv.hi, t + 1) - s0;
+        const int diag_end = t_end - s0;
+        const int lr_lo = iv.lo - s0, lr_hi = imin(iv.hi, t_end) - s0;
+        uint32_t lost = 0;  // 8-column groups whose page is bad
+        if constexpr (PAGED) {
+          lost = reinterpret_cast<volatile uint32_t*>(bad_rows)[n % kBadRing];
+          need_mask |= lost != 0;
+        }
         uint32_t xr[128];
 #pragma unroll
         for (int q = 0; q < 4; ++q) ptx::tmem_ld32(s_tm + q * 32, xr + q * 32);
@@ -353,7 +463,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cowa_fwd_kernel(const __grid_c
 #pragma unroll
           for (int c = 0; c < 128; ++c) {
             const bool vis = (c < sink_end) || (c >= band_lo && c < diag_end) || (c >= lr_lo && c < lr_hi);
-            if (!vis) xr[c] = 0xff800000u;  // -inf: gives exactly 0
+            if (!vis || (PAGED && ((lost >> (c / 8)) & 1))) xr[c] = 0xff800000u;  // -inf: gives exactly 0
           }
         }
         // P = 2^(s*scale*log2e - m) with m the running max from before this tile, rounded to
@@ -430,6 +540,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cowa_fwd_kernel(const __grid_c
       ptx::f2_unpack(lsum, la, lb);
       const float l = la + lb;
       // ---- epilogue
+      if constexpr (PAGED) {
+        if (ntiles == 0 && t < t1 && k < (has1 ? 2 : 1)) {  // a query tile past a full cache and its band
+          __nv_bfloat16* z = reinterpret_cast<__nv_bfloat16*>(a.o) + (size_t)(row0 + t - q_off) * a.o_st + (size_t)(h0 + k) * a.o_sh;
+          for (int c = 0; c < D / 8; ++c) reinterpret_cast<uint4*>(z)[c] = make_uint4(0, 0, 0, 0);
+          a.lse[(size_t)(h0 + k) * a.total + row0 + t - q_off] = -INFINITY;
+        }
+      }
       const int rl = t - q_off;  // query row within the call's (or the sequence's) rows
       __nv_bfloat16* orow = reinterpret_cast<__nv_bfloat16*>(a.o) + (size_t)b * a.o_sb + (size_t)(row0 + rl) * a.o_st +
                             (size_t)h0 * a.o_sh;
@@ -439,8 +556,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cowa_fwd_kernel(const __grid_c
       if (!split) {
         if (ok && ntiles > 0 && ptx::mbar_wait_warp(&o_done[k], 0, &abort_flag, a.status)) {
           ptx::tc_fence_after();
-          const float inv = 1.f / l;
-          if (t < t1) a.lse[lse_h0 + k * lse_step] = (m_used + log2f(l)) * 0.69314718055994530942f;
+          // (a paged row may see nothing: its pages are bad, or it lies past the cache)
+          const float inv = PAGED && m_used == -INFINITY ? 0.f : 1.f / l;
+          if (t < t1)
+            a.lse[lse_h0 + k * lse_step] =
+                PAGED && m_used == -INFINITY ? -INFINITY : (m_used + log2f(l)) * 0.69314718055994530942f;
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
             uint32_t ov[32];
@@ -477,9 +597,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cowa_fwd_kernel(const __grid_c
         const float f0 = m_used == -INFINITY ? 0.f : ptx::ex2(m_used - m);
         const float f1 = m1 == -INFINITY ? 0.f : ptx::ex2(m1 - m);
         const float lt = l * f0 + l1 * f1;
-        const float inv = 1.f / lt, g0 = f0 * inv, g1 = f1 * inv;
+        const float inv = PAGED && m == -INFINITY ? 0.f : 1.f / lt, g0 = f0 * inv, g1 = f1 * inv;
         const bool two = ntiles > 1;  // slot 1 has tiles (uniform over the CTA)
-        if (t < t1) a.lse[lse_h0] = (m + log2f(lt)) * 0.69314718055994530942f;
+        if (t < t1) a.lse[lse_h0] = PAGED && m == -INFINITY ? -INFINITY : (m + log2f(lt)) * 0.69314718055994530942f;
         const uint32_t o1_tm = lane_base + Geo::kColO + D;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
@@ -534,10 +654,10 @@ __global__ void seq_table_kernel(const int32_t* cu, int n_seq, int total, int32_
   tab[n_seq] = off;
 }
 
-template <int D>
+template <int D, bool PAGED>
 cudaError_t launch_fwd_d(const FwdArgs& a, cudaStream_t s) {
   using Geo = FwdGeom<D>;
-  auto kern = cowa_fwd_kernel<D>;
+  auto kern = cowa_fwd_kernel<D, PAGED>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo::kSmem);
   if (e != cudaSuccess) return e;
   const int grp = a.Hq / a.Hkv;
@@ -569,8 +689,8 @@ cudaError_t launch_seq_table(const int32_t* cu_seqlens, int n_seq, int total, in
 }
 
 cudaError_t launch_fwd(const FwdArgs& a, cudaStream_t s) {
-  if (a.d == 64) return launch_fwd_d<64>(a, s);
-  if (a.d == 128) return launch_fwd_d<128>(a, s);
+  if (a.d == 64) return a.paged ? launch_fwd_d<64, true>(a, s) : launch_fwd_d<64, false>(a, s);
+  if (a.d == 128) return a.paged ? launch_fwd_d<128, true>(a, s) : launch_fwd_d<128, false>(a, s);
   return cudaErrorInvalidValue;
 }
 

@@ -132,6 +132,11 @@ struct FwdArgs {
   int varlen, n_seq, total;
   const int32_t* cu_seqlens;
   int32_t* seq_tab;
+  // paged != 0 (a packed batch): keys and values in pages (tm_k, tm_v over the pools), sequence s's
+  // query rows at positions q_start[s]..
+  int paged, box_rows;
+  PageTab tab;
+  const int32_t* q_start;
   void* o;
   int64_t o_sb, o_st, o_sh;
   float* lse;

@@ -481,3 +481,156 @@ def test_refusals_of_the_binding(cuda_device):
         app(page_table=tab[:1])
     with pytest.raises(TypeError):
         app(v_pages=pool.half())
+
+
+# ------------------------------------------------------------------------------------------ chunks
+def assert_chunk(o, lse, q64, k, v, start, pat, has=None):
+    """One sequence's rows o [n, Hq, d], lse [Hq, n] (CUDA) at positions start.. against k, v [Hkv, T, d]."""
+    n, Hq, d = q64.shape
+    Hkv, Tc = k.shape[0], k.shape[1]
+    op = oracle_pattern(pat)
+    go, gl = to64(o), lse.double().cpu().numpy()
+    for g in range(Hkv):
+        see = orc.visible_mask(np.arange(start, start + n), Tc, op, g, Hkv)
+        if has is not None:
+            see = see & has[g]
+        for h in range(g * Hq // Hkv, (g + 1) * Hq // Hkv):
+            s = np.where(see, q64[:, h] @ k[g].T * (pat.softmax_scale or 1 / np.sqrt(d)), -np.inf)
+            m = np.where(see.any(1), s.max(1), 0.0)
+            p = np.exp(s - m[:, None])
+            l = p.sum(1)
+            none = l == 0
+            assert (go[none, h] == 0).all() and (gl[h, none] == -np.inf).all()
+            l = np.where(none, 1.0, l)[:, None]
+            want, A = p @ v[g] / l, p @ np.abs(v[g]) / l
+            err = np.abs(go[:, h] - want)
+            assert (err <= 2.0 ** -8 * (A + np.abs(want)) + 2.0 ** -12 * A).all(), (h, err.max())
+            assert (np.abs(gl[h] - (m + np.log(l[:, 0])))[~none] <= LSE_TOL).all(), h
+
+
+CHUNK = [
+    # Hq, Hkv, d, pattern, page, pages, per head, layout, (start, rows) of each sequence
+    (8, 4, 64, cw.Pattern(64, 128, 1024, 4), 16, 64, False, "bthd", [(824, 200)]),
+    (10, 2, 128, cw.Pattern(20, 100, 900, 2), 64, 16, False, "bhtd", [(0, 1), (1000, 24), (500, 0), (37, 300), (0, 128)]),
+    (3, 3, 128, cw.Pattern(0, 1, 1024, 3), 8, 96, True, "bthd", [(767, 1), (13, 130)]),       # single heads, L = 1
+    (7, 1, 64, cw.Pattern(33, 5000, 600, 1), 24, 30, False, "bhtd", [(100, 257), (719, 1)]),  # dense, odd group
+    (8, 2, 128, cw.Pattern(4, 60, 4, 1), 128, 8, False, "bthd", [(896, 128), (1, 127)]),      # sinks and band only
+    (4, 2, 128, cw.Pattern(100, 7, 700, 2), 256, 3, True, "bhtd", [(301, 400)]),
+    (6, 2, 64, cw.Pattern(30, 90, 1000, 4, kv_head_base=1, h_kv_global=4), 32, 32, False, "bthd", [(600, 333), (5, 5)]),
+    (40, 8, 128, cw.Pattern(128, 500, 2048, 8), 48, 43, False, "bthd", [(1500, 500)]),
+]
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,pat,ps,n,per_head,layout,chunks", CHUNK)
+def test_chunks_match_oracle(cuda_device, Hq, Hkv, d, pat, ps, n, per_head, layout, chunks):
+    """Packed chunks against their pages; rows past each sequence's last key hold NaN, rows of q behind the
+    last sequence are left as they were, heads of their own map only what some row of the chunk sees."""
+    B, rng = len(chunks), np.random.default_rng(ps * n)
+    tab, n_pages = make_table(rng, B, n, heads=Hkv if per_head else None)
+    shape = (n_pages, ps, 1 if per_head else Hkv, d)
+    (k64, kd), (v64, vd) = (host_and_device(shape, x, cuda_device, 91) for x in ("k", "v"))
+    k, _ = orp.gather_pages(k64, tab, n * ps)
+    v, _ = orp.gather_pages(v64, tab, n * ps)
+    for b, (start, rows) in enumerate(chunks):
+        for s in range(start + rows, n * ps):
+            page = tab[b, ..., s // ps]
+            kd[torch.from_numpy(np.atleast_1d(page)).long().to(cuda_device), s % ps] = float("nan")
+            vd[torch.from_numpy(np.atleast_1d(page)).long().to(cuda_device), s % ps] = float("inf")
+        if per_head:
+            for g in range(Hkv):
+                see = orc.visible_mask(np.arange(start, start + rows), n * ps, oracle_pattern(pat), g, Hkv).any(0)
+                tab[b, g, ~see.reshape(n, ps).any(1)] = -1
+    if layout == "bhtd":
+        kd, vd = kd.transpose(1, 2).contiguous(), vd.transpose(1, 2).contiguous()
+    lens = [r for _, r in chunks]
+    total = sum(lens) + 3
+    q64, q = host_and_device((total, Hq, d), "q", cuda_device, 92)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=cuda_device)
+    cu = np.cumsum([0] + lens)
+    ws = torch.zeros(cw.lib().cowa_fwd_paged_workspace_size(ctypes.byref(pat.c()), B, total, Hq, Hkv, d),
+                     dtype=torch.uint8, device=cuda_device)
+    out = torch.full((total, Hq, d), 3.0, dtype=torch.bfloat16, device=cuda_device)
+    lse = torch.full((Hq, total), 5.0, device=cuda_device)
+    o, l = cw.cowa_fwd_paged(q, kd, vd, torch.from_numpy(tab).to(cuda_device), i32(cu.tolist()),
+                             i32([s for s, _ in chunks]), pat, layout=layout, out=out, lse=lse, workspace=ws)
+    assert cw.workspace_status(ws) == 0
+    assert o is out and (out[cu[-1]:] == 3.0).all() and (lse[:, cu[-1]:] == 5.0).all()
+    for b, (start, rows) in enumerate(chunks):
+        r = slice(cu[b], cu[b + 1])
+        assert_chunk(o[r], l[:, r], q64[r], k[b, :, :start + rows], v[b, :, :start + rows], start, pat)
+
+
+def test_chunks_equal_the_contiguous_forward(cuda_device):
+    """Over pages of 128 in order the tiles and their masks are those of cowa_fwd_chunk: the same bits."""
+    N, Hq, Hkv, d, start = 1100, 10, 2, 128, 640
+    pat = cw.Pattern(64, 300, 1100, 2)
+    k, v = (synth.cuda_normal_bf16((1, 1152, Hkv, d), synth.seed_of(x, 93), cuda_device) for x in ("k", "v"))
+    q = synth.cuda_normal_bf16((1, N - start, Hq, d), synth.seed_of("q", 93), cuda_device)
+    wo, wl = cw.cowa_fwd_chunk(q, k, v, pat, start, n_k=N)
+    pages = lambda x: x.view(9, 128, Hkv, d)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=cuda_device)
+    o, lse = cw.cowa_fwd_paged(q[0], pages(k), pages(v), i32([list(range(9))]), i32([0, N - start]), i32([start]), pat)
+    assert torch.equal(o, wo[0]) and torch.equal(lse, wl[0])
+
+
+@pytest.mark.parametrize("Hq", [2, 3, 4])
+def test_chunk_bad_entries_and_overlong_sequences(cuda_device, Hq):
+    """Bad entries: their keys left out and reported; a sequence without a page: zeros and -inf.  A chunk
+    longer than the cache starts at 0, and its rows past the capacity see what there is (none, if the band
+    has passed it); a start past the end is moved back."""
+    Hkv, d, ps, n = 1, 64, 16, 20
+    cap = n * ps
+    pat = cw.Pattern(0, 40, 0, 1)
+    tab, n_pages = make_table(np.random.default_rng(94), 4, n)
+    tab[0, [3, 9]] = -1, n_pages
+    tab[1, :] = 2**31 - 1
+    (k64, kd), (v64, vd) = (host_and_device((n_pages, ps, Hkv, d), x, cuda_device, 94) for x in ("k", "v"))
+    chunks = [(20, 200), (50, 70), (-5, cap + 90), (10**9, 30)]
+    real = [(20, 200), (50, 70), (0, cap + 90), (cap - 30, 30)]
+    lens = [r for _, r in chunks]
+    cu = np.cumsum([0] + lens)
+    q64, q = host_and_device((int(cu[-1]), Hq, d), "q", cuda_device, 94)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=cuda_device)
+    ws = torch.zeros(4096, dtype=torch.uint8, device=cuda_device)
+    o, lse = cw.cowa_fwd_paged(q, kd, vd, torch.from_numpy(tab).to(cuda_device), i32(cu.tolist()),
+                               i32([s for s, _ in chunks]), pat, workspace=ws)
+    assert cw.workspace_status(ws) == 8 and cw.workspace_status(ws) == 0
+    k, has = orp.gather_pages(k64, tab, cap)
+    v, _ = orp.gather_pages(v64, tab, cap)
+    for b, (start, rows) in enumerate(real):
+        r = slice(cu[b], cu[b + 1])
+        assert_chunk(o[r], lse[:, r], q64[r], k[b], v[b], start, pat, has[b])
+
+
+def test_chunk_graph_stream_and_refusals(cuda_device):
+    Hq, Hkv, d, ps, n = 4, 2, 64, 32, 16
+    pat = cw.Pattern(16, 60, 512, 2)
+    r = lambda s, nm: synth.cuda_normal_bf16(s, synth.seed_of(nm, 95), cuda_device)
+    q, kp, vp = r((200, Hq, d), "q"), r((2 * n, ps, Hkv, d), "k"), r((2 * n, ps, Hkv, d), "v")
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=cuda_device)
+    tab, cu, start = torch.randperm(2 * n, device=cuda_device).int().view(2, n), i32([0, 150, 200]), i32([300, 0])
+    wo, wl = cw.cowa_fwd_paged(q, kp, vp, tab, cu, start, pat)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    o, lse = cw.cowa_fwd_paged(q, kp, vp, tab, cu, start, pat, stream=side)
+    side.synchronize()
+    assert torch.equal(o, wo) and torch.equal(lse, wl)
+    ws = torch.zeros(4096, dtype=torch.uint8, device=cuda_device)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        cw.cowa_fwd_paged(q, kp, vp, tab, cu, start, pat, out=o, lse=lse, workspace=ws)
+    o.zero_(), lse.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o, wo) and torch.equal(lse, wl)
+    run = lambda **c: cw.cowa_fwd_paged(**{**dict(q=q, k_pages=kp, v_pages=vp, page_table=tab, cu_seqlens=cu,
+                                                  q_start=start, pattern=pat), **c})
+    for bad in (dict(cu_seqlens=cu[:2]), dict(q_start=cu), dict(out=o[:5]), dict(lse=lse[:, :5]), dict(layout="hd"),
+                dict(v_pages=vp[:3]), dict(page_table=tab.view(2, 4, 4))):
+        with pytest.raises(ValueError):
+            run(**bad)
+    for bad in (dict(q=q.half()), dict(q_start=start.long()), dict(k_pages=kp.to(torch.uint8))):
+        with pytest.raises(TypeError):
+            run(**bad)
+    with pytest.raises(cw.CowaError):
+        run(workspace=torch.zeros(256, dtype=torch.uint8, device=cuda_device))

@@ -53,12 +53,7 @@ def test_rope_refusals(fn, status, change):
 def test_append_refusals(status, change):
     base = dict(rot=rotary(), total=8, n_seq=8, Hq=8, Hkv=4, d=128, q=T(), k=T(), v=T(), qo=T(), pos=0x9000, seq=None,
                 rp=0x9000, rs=8, kp=T(), vp=T(), ks=1.0, vs=1.0, tab=table())
-    base.update(change)
-    if change == dict(total=9):
-        base["seq"] = None
-    a, L = base, cw.lib()
-    if "seq" in change:
-        a["seq"] = change["seq"]
+    a, L = {**base, **change}, cw.lib()
     args = (ctypes.byref(a["rot"]), a["total"], a["n_seq"], a["Hq"], a["Hkv"], a["d"], a["q"], a["k"], a["v"], a["qo"],
             a["pos"], a["seq"], a["rp"], a["rs"], a["kp"], a["vp"])
     assert L.cowa_paged_append_fp8(*args, a["ks"], a["vs"], a["tab"], None) == status
@@ -88,6 +83,24 @@ def test_decode_refusals(status, change):
                              a["tab"], a["pos"], a["o"], a["lse"], a["ws"], n - a["less"], None)
         assert got == status, fn
     assert L.cowa_decode_paged_fp8_workspace_size(ctypes.byref(cw.Pattern(64, 100, 1024, 4).c()), 3, 8, 4, 64, 64, 16) == 0
+
+
+@pytest.mark.parametrize("status,change", [
+    (1, dict(n_seq=0)), (1, dict(total=0)), (1, dict(Hq=7)), (2, dict(Hq=36)), (2, dict(d=96)), (1, dict(cu=None)),
+    (1, dict(start=None)), (1, dict(lse=None)), (3, dict(cu=0x9002)), (3, dict(start=0x9001)), (3, dict(lse=0x9003)),
+    (1, dict(q=T(None))), (3, dict(o=T(0x10004))), (3, dict(kp=T(sb=4))), (1, dict(vp=T(None))),
+    (1, dict(tab=table(page=4))), (1, dict(tab=table(ptr=None))), (4, dict(less=1)), (4, dict(ws=0x40010)),
+    (1, dict(pat=cw.Pattern(10, 4, 5, 1))),
+])
+def test_chunk_refusals(status, change):
+    a = dict(pat=cw.Pattern(64, 100, 1024, 4), n_seq=3, total=500, Hq=8, Hkv=4, d=128, cu=0x9000, start=0x9100, q=T(),
+             kp=T(), vp=T(), tab=table(), o=T(), lse=0x30000, ws=0x40000, less=0)
+    a.update(change)
+    L = cw.lib()
+    n = L.cowa_fwd_paged_workspace_size(ctypes.byref(cw.Pattern(64, 100, 1024, 4).c()), 3, 500, 8, 4, 128)
+    assert L.cowa_fwd_paged(ctypes.byref(a["pat"].c()), a["n_seq"], a["total"], a["Hq"], a["Hkv"], a["d"], a["cu"],
+                            a["start"], a["q"], a["kp"], a["vp"], a["tab"], a["o"], a["lse"], a["ws"], n - a["less"],
+                            None) == status
 
 
 def test_workspace_is_bounded_and_grows_with_the_group():
