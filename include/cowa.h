@@ -422,11 +422,12 @@ cowa_status cowa_decode_paged_fp8(const cowa_pattern* pat, int B, int H_q, int H
  * Outputs o [total, H_q, d] and lse fp32 [H_q, total] as cowa_fwd_varlen, whose rules hold for
  * cu_seqlens (device int32 [n_seq + 1]), strides and workspace; rows behind the last sequence are left
  * as they are.  q_start: device int32 [n_seq], clamped into [0, capacity - len_s] (rows of a sequence
- * longer than the capacity see the keys there are).  Bad entries of pages with visible keys as for
- * cowa_decode_paged; a row that sees nothing has o 0 and lse -inf.  Entries of pages that a query tile
- * of 128 rows does not see are not read.  Keys and values below q_start[s] + len_s on mapped pages must
- * be finite where they share a tile of 128 positions with visible ones; what stands behind them is
- * never used.  bf16 pages only.  The workspace's first 256 bytes must be zero before its first call. */
+ * longer than the capacity see the keys there are); a row that sees nothing has o 0 and lse -inf.
+ * Where an entry of a page with a key that some row of a query tile (128 rows of a sequence) sees lies
+ * outside [0, n_pages), the tile's rows of that KV head's group are left empty (o 0, lse -inf) and
+ * COWA_ERR_PAGE is reported as for cowa_decode_paged; other entries may hold anything.  Keys and values
+ * below q_start[s] + len_s on mapped pages must be finite where they share a tile of 128 positions with
+ * visible ones; what stands behind them is never used.  bf16 pages only.  The workspace's first 256 bytes must be zero before its first call. */
 size_t cowa_fwd_paged_workspace_size(const cowa_pattern* pat, int n_seq, int total, int H_q, int H_kv, int d);
 cowa_status cowa_fwd_paged(const cowa_pattern* pat, int n_seq, int total, int H_q, int H_kv, int d,
                            const int32_t* cu_seqlens, const int32_t* q_start, cowa_tensor q, cowa_tensor k_pages,

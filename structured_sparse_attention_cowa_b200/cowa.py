@@ -615,35 +615,76 @@ def cowa_decode_fp8_compact(q_t, kc, vc, pos, pattern: Pattern, k_scale: float, 
 
 
 # ---------------------------------------------------------------------------- rotary positions, paged cache
-def _launch_on(x, stream):
-    """Context in which x's device is current and allocations and launches go to `stream` (the
+# A step of one token makes these calls in a few microseconds of GPU time, so their checks are kept
+# short: one comparison per property, device indices instead of device objects.
+def _device_of(x, *others) -> int:
+    """Index of x's CUDA device, which must be that of the others (None: not given) too."""
+    dev = x.get_device()
+    for y in others:
+        if y is not None and y.get_device() != dev:
+            raise ValueError(f"tensors are on different devices: {x.device} and {y.device}")
+    return dev
+
+
+def _launch_on(dev: int, stream):
+    """Context in which device `dev` is current and allocations and launches go to `stream` (the
     device's current stream if None): what a call allocates then belongs to the stream that uses it."""
     import torch
 
     if stream is not None:
-        if stream.device != x.device:
+        if stream.device.index != dev:
             raise ValueError("stream and tensors are on different devices")
         return torch.cuda.stream(stream)
-    if torch.cuda.current_device() != x.device.index:
-        return torch.cuda.device(x.device)
-    return contextlib.nullcontext()
+    if torch.cuda.current_device() != dev:
+        return torch.cuda.device(dev)
+    return _HERE_ALREADY
 
 
-def _same_device(x, **others):
-    for name, y in others.items():
-        if y is not None and y.device != x.device:
-            raise ValueError(f"{name} is on {y.device}, not on {x.device}")
+_HERE_ALREADY = contextlib.nullcontext()
+_raw_stream = None
+
+
+def _stream_of(dev: int) -> int:
+    """Handle of device dev's current stream."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+
+        # torch's own accessor of the handle, without a Stream object (20 times cheaper) where it has one
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda d: torch.cuda.current_stream(d).cuda_stream)
+    return _raw_stream(dev)
 
 
 def _int32(name, x, shape):
     import torch
 
-    if x.dtype != torch.int32 or not x.is_cuda:
+    if x.dtype is not torch.int32 or not x.is_cuda:
         raise TypeError(f"{name} must be a CUDA int32 tensor")
-    if tuple(x.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(x.shape)}, expected {tuple(shape)}")
-    if x.shape[-1] > 1 and x.stride(-1) != 1:
+    if x.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(x.shape)}, expected {shape}")
+    if x.stride(-1) != 1 and shape[-1] > 1:
         raise ValueError(f"{name} must be contiguous along its last dimension")
+    return x.data_ptr()
+
+
+def _bf16(name, x, shape):
+    import torch
+
+    if x.dtype is not torch.bfloat16 or not x.is_cuda:
+        raise TypeError(f"{name} must be a CUDA bfloat16 tensor")
+    if x.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(x.shape)}, expected {shape}")
+
+
+def _rows(name, x) -> c_tensor:
+    """[B, N, H, d] or packed [total, H, d] tensor (d contiguous) -> cowa_tensor."""
+    s = x.stride()
+    if s[-1] != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    if len(s) == 3:
+        return c_tensor(x.data_ptr(), s[0] * max(1, x.shape[0]), s[0], s[1])
+    return c_tensor(x.data_ptr(), s[0], s[1], s[2])
 
 
 _NO_TENSOR = c_tensor(None, 0, 0, 0)
@@ -682,37 +723,37 @@ class Rope:
 def _rope(fn, q, k, rope, positions, q_out, k_out, stream):
     import torch
 
-    if q is None and k is None:
-        raise ValueError("q or k is needed")
     x = q if q is not None else k
+    if x is None:
+        raise ValueError("q or k is needed")
+    if x.dim() != 4:
+        raise ValueError("q and k are [B, N, H, d]")
     B, N, _, d = x.shape
-    for n_, x_, o_ in (("q", q, q_out), ("k", k, k_out)):
-        if x_ is None:
-            continue
-        _bf16_cuda(n_, x_)
-        if x_.dim() != 4 or x_.shape[0] != B or x_.shape[1] != N or x_.shape[3] != d:
-            raise ValueError("q and k are [B, N, H, d] with the same B, N and d")
-        if o_ is not None:
-            _bf16_cuda(n_ + "_out", o_)
-            if o_.shape != x_.shape:
-                raise ValueError(f"{n_}_out must have the shape of {n_}")
-    _same_device(x, k=k, positions=positions, q_out=q_out, k_out=k_out, inv_freq=rope.inv_freq)
-    sa = sb = 0
+    heads = [0, 0]
+    for i, (name, y, y_out) in enumerate((("q", q, q_out), ("k", k, k_out))):
+        if y is not None:
+            heads[i] = y.shape[2] if y.dim() == 4 else -1
+            _bf16(name, y, (B, N, heads[i], d))
+            if y_out is not None:
+                _bf16(name + "_out", y_out, y.shape)
+        elif y_out is not None:
+            raise ValueError(f"{name}_out without {name}")
+    dev = _device_of(x, k, positions, q_out, k_out, rope.inv_freq)
+    pos, sa, sb = None, 0, 0
     if positions is not None:
         if positions.dim() == 2 and rope.n_axes == 1:
-            positions = positions.unsqueeze(0)
-        _int32("positions", positions, (rope.n_axes, B, N))
-        sa, sb = positions.stride(0), positions.stride(1)
-    with _launch_on(x, stream):
+            pos, sb = _int32("positions", positions, (B, N)), positions.stride(0)
+        else:
+            pos = _int32("positions", positions, (rope.n_axes, B, N))
+            sa, sb, _ = positions.stride()
+    with _launch_on(dev, stream):
         if q is not None and q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
         if k is not None and k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        t = lambda y: _NO_TENSOR if y is None else _t4(y)
-        _check(fn, getattr(lib(), fn)(ctypes.byref(rope.c()), B, N, 0 if q is None else q.shape[2],
-                                      0 if k is None else k.shape[2], d, t(q), t(k), t(q_out) if q is not None else t(None),
-                                      t(k_out) if k is not None else t(None),
-                                      positions.data_ptr() if positions is not None else None, sa, sb, _stream(None)))
+            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+        t = lambda name, y: _NO_TENSOR if y is None else _rows(name, y)
+        _check(fn, getattr(lib(), fn)(ctypes.byref(rope._c), B, N, *heads, d, t("q", q), t("k", k), t("q_out", q_out),
+                                      t("k_out", k_out), pos, sa, sb, _stream_of(dev)))
     return q_out, k_out
 
 
@@ -730,70 +771,78 @@ def cowa_rope_bwd(dq, dk, rope: Rope, positions=None, dq_out=None, dk_out=None, 
 def pages_needed(pattern: Pattern, h_kv: int, page_size: int, n_pages: int, pos: int) -> np.ndarray:
     """bool [h_kv, n_pages]: the pages that hold a key each KV head sees from position pos on, or a
     position past pos; a head with pages of its own may give the others back."""
-    out = np.zeros((h_kv, n_pages), dtype=np.uint8)
+    out = np.zeros((max(0, h_kv), max(0, n_pages)), dtype=np.uint8)
     _check("cowa_pages_needed", lib().cowa_pages_needed(ctypes.byref(pattern.c()), h_kv, page_size, n_pages, pos,
                                                         out.ctypes.data_as(ctypes.c_void_p)))
     return out.astype(bool)
 
 
-def _pages(k_pages, v_pages, page_table, layout, h_kv, d, n_seq=None):
-    """(k, v as cowa_tensor, cowa_page_table) of pools [n_pages, page_size, H, d] ("bthd") or
-    [n_pages, H, page_size, d] ("bhtd"), H = h_kv or, with a table [n_seq, h_kv, max_pages], 1."""
+def _pages(k_pages, v_pages, page_table, layout, d, h_kv=None):
+    """(H_kv, k and v as cowa_tensor, cowa_page_table) of pools [n_pages, page_size, H, d] ("bthd") or
+    [n_pages, H, page_size, d] ("bhtd"), H = H_kv or, with a table [n_seq, H_kv, max_pages], 1."""
     import torch
 
-    if layout not in ("bthd", "bhtd"):
+    if layout == "bthd":
+        t, h = 1, 2
+    elif layout == "bhtd":
+        t, h = 2, 1
+    else:
         raise ValueError("layout must be 'bhtd' or 'bthd'")
-    if page_table.dtype != torch.int32 or not page_table.is_cuda:
+    if page_table.dtype is not torch.int32 or not page_table.is_cuda:
         raise TypeError("page_table must be a CUDA int32 tensor")
-    per_head = page_table.dim() == 3
-    ax_t, ax_h = (1, 2) if layout == "bthd" else (2, 1)
-    if page_table.dim() not in (2, 3) or (per_head and page_table.shape[1] != h_kv):
-        raise ValueError("page_table is [n_seq, max_pages] or [n_seq, H_kv, max_pages]")
-    if n_seq is not None and page_table.shape[0] != n_seq:
-        raise ValueError(f"page_table has {page_table.shape[0]} sequences, expected {n_seq}")
-    if page_table.shape[-1] > 1 and page_table.stride(-1) != 1:
-        raise ValueError("page_table must be contiguous along its last dimension")
-    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.shape[3] != d or \
-            k_pages.shape[ax_h] != (1 if per_head else h_kv):
-        raise ValueError("k_pages and v_pages must be pools of this layout, with one head per page if the table is per head")
-    tab = c_page_table(page_table.data_ptr(), page_table.stride(0), page_table.stride(1) if per_head else 0,
-                       page_table.shape[-1], k_pages.shape[ax_t], k_pages.shape[0], int(per_head))
-    return _cache_tensor(k_pages, layout), _cache_tensor(v_pages, layout), tab
+    ts, shape, dims = page_table.stride(), k_pages.shape, page_table.dim()
+    if not 2 <= dims <= 3 or (ts[-1] != 1 and page_table.shape[-1] > 1):
+        raise ValueError("page_table is [n_seq, max_pages] or [n_seq, H_kv, max_pages], contiguous along the last dimension")
+    if len(shape) != 4 or shape != v_pages.shape or shape[3] != d:
+        raise ValueError("k_pages and v_pages must be 4-D pools of the same shape and head dimension")
+    heads = page_table.shape[1] if dims == 3 else shape[h]
+    if (h_kv is not None and heads != h_kv) or (dims == 3 and shape[h] != 1):
+        raise ValueError("the pools hold all KV heads, or one, if the table has entries for each")
+    ks, vs = k_pages.stride(), v_pages.stride()
+    if ks[3] != 1 or vs[3] != 1:
+        raise ValueError("the last dimension of the pools must be contiguous")
+    return (heads, c_tensor(k_pages.data_ptr(), ks[0], ks[t], ks[h]), c_tensor(v_pages.data_ptr(), vs[0], vs[t], vs[h]),
+            c_page_table(page_table.data_ptr(), ts[0], ts[1] if dims == 3 else 0, page_table.shape[-1], shape[t],
+                         shape[0], dims == 3))
 
 
 def _paged_append(fn, q, k, v, pos, k_pages, v_pages, page_table, rope, seq, rope_pos, q_out, layout, scales, stream):
     import torch
 
-    total, Hkv, d = k.shape
-    for n_, x_ in (("q", q), ("k", k), ("v", v), ("q_out", q_out)):
-        if x_ is not None:
-            _bf16_cuda(n_, x_)
-    if v.shape != k.shape or (q is not None and (q.dim() != 3 or q.shape[0] != total or q.shape[2] != d)):
+    if k.dim() != 3 or (q is not None and q.dim() != 3):
         raise ValueError("q is [total, H_q, d], k and v are [total, H_kv, d]")
-    if q is not None and q_out is not None and q_out.shape != q.shape:
-        raise ValueError("q_out must have the shape of q")
-    _int32("pos", pos, (total,))
+    total, Hkv, d = shape = k.shape
+    _bf16("k", k, shape)
+    _bf16("v", v, shape)
+    Hq = 0
+    if q is not None:
+        Hq = q.shape[1]
+        _bf16("q", q, (total, Hq, d))
+        if q_out is not None:
+            _bf16("q_out", q_out, q.shape)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    pos_p, seq_p, rp, rs = _int32("pos", pos, (total,)), None, None, 0
     if seq is not None:
-        _int32("seq", seq, (total,))
+        seq_p = _int32("seq", seq, (total,))
     if rope_pos is not None:
         if rope is None:
             raise ValueError("rope_pos without rope")
         if rope_pos.dim() == 1 and rope.n_axes == 1:
-            rope_pos = rope_pos.unsqueeze(0)
-        _int32("rope_pos", rope_pos, (rope.n_axes, total))
-    _same_device(k, q=q, v=v, pos=pos, seq=seq, rope_pos=rope_pos, q_out=q_out, k_pages=k_pages, v_pages=v_pages,
-                 page_table=page_table, inv_freq=None if rope is None else rope.inv_freq)
-    kp, vp, tab = _pages(k_pages, v_pages, page_table, layout, Hkv, d)
-    with _launch_on(k, stream):
+            rp = _int32("rope_pos", rope_pos, (total,))
+        else:
+            rp, rs = _int32("rope_pos", rope_pos, (rope.n_axes, total)), rope_pos.stride(0)
+    _, kp, vp, tab = _pages(k_pages, v_pages, page_table, layout, d, Hkv)
+    dev = _device_of(k, q, v, pos, seq, rope_pos, q_out, k_pages, v_pages, page_table,
+                     None if rope is None else rope.inv_freq)
+    with _launch_on(dev, stream):
         if q is not None and q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        t = lambda y: _NO_TENSOR if y is None else _t4(y.unsqueeze(0))
-        ptr = lambda y: None if y is None else y.data_ptr()
-        _check(fn, getattr(lib(), fn)(None if rope is None else ctypes.byref(rope.c()), total, page_table.shape[0],
-                                      0 if q is None else q.shape[1], Hkv, d, t(q), t(k), t(v),
-                                      t(q_out) if q is not None else t(None), pos.data_ptr(), ptr(seq), ptr(rope_pos),
-                                      0 if rope_pos is None else rope_pos.stride(0), kp, vp, *scales, tab, _stream(None)))
-    return q_out if q is not None else None
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        _check(fn, getattr(lib(), fn)(None if rope is None else ctypes.byref(rope._c), total, page_table.shape[0], Hq, Hkv,
+                                      d, _NO_TENSOR if q is None else _rows("q", q), _rows("k", k), _rows("v", v),
+                                      _NO_TENSOR if q is None else _rows("q_out", q_out), pos_p, seq_p, rp, rs, kp, vp,
+                                      *scales, tab, _stream_of(dev)))
+    return q_out
 
 
 def paged_append(q, k, v, pos, k_pages, v_pages, page_table, rope: Rope = None, seq=None, rope_pos=None, q_out=None,
@@ -821,40 +870,45 @@ def paged_append_fp8(q, k, v, pos, k_pages, v_pages, page_table, k_scale: float,
                          q_out, layout, (float(k_scale), float(v_scale)), stream)
 
 
+def _lse(lse, shape):
+    import torch
+
+    if lse.dtype is not torch.float32 or lse.shape != shape or not lse.is_contiguous():
+        raise ValueError(f"lse must be a contiguous float32 tensor of shape {shape}")
+
+
 def _decode_paged(fn, q_t, k_pages, v_pages, page_table, pos, pattern, scales, layout, out, lse, workspace, stream,
                   want_lse):
     import torch
 
-    _bf16_cuda("q_t", q_t)
-    B, Hq, d = q_t.shape
+    B, Hq, d = shape = q_t.shape
+    _bf16("q_t", q_t, shape)
     if not q_t.is_contiguous():
         raise ValueError("q_t must be contiguous [B, H_q, d]")
-    if layout not in ("bthd", "bhtd") or k_pages.dim() != 4 or page_table.dim() not in (2, 3):
-        raise ValueError("k_pages is 4-D in layout 'bthd' or 'bhtd', page_table [B, max_pages] or [B, H_kv, max_pages]")
-    Hkv = page_table.shape[1] if page_table.dim() == 3 else k_pages.shape[2 if layout == "bthd" else 1]
-    kp, vp, tab = _pages(k_pages, v_pages, page_table, layout, Hkv, d, B)
-    _int32("pos", pos, (B,))
+    Hkv, kp, vp, tab = _pages(k_pages, v_pages, page_table, layout, d)
+    pos_p = _int32("pos", pos, (B,))
+    if page_table.shape[0] != B:
+        raise ValueError(f"page_table has {page_table.shape[0]} sequences, expected {B}")
     if out is not None:
-        _bf16_cuda("out", out)
-        if out.shape != q_t.shape or not out.is_contiguous():
+        _bf16("out", out, shape)
+        if not out.is_contiguous():
             raise ValueError("out must be contiguous [B, H_q, d]")
-    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (B, Hq) or not lse.is_contiguous()):
-        raise ValueError("lse must be a contiguous float32 [B, H_q] tensor")
-    _same_device(q_t, k_pages=k_pages, v_pages=v_pages, page_table=page_table, pos=pos, out=out, lse=lse,
-                 workspace=workspace)
-    pat = pattern.c()
+    if lse is not None:
+        _lse(lse, (B, Hq))
+    dev = _device_of(q_t, k_pages, v_pages, page_table, pos, out, lse, workspace)
+    pat = ctypes.byref(pattern.c())
     L = lib()
-    with _launch_on(q_t, stream):
+    with _launch_on(dev, stream):
         if out is None:
-            out = torch.empty((B, Hq, d), dtype=torch.bfloat16, device=q_t.device)
+            out = torch.empty_like(q_t)
         if lse is None and want_lse:
             lse = torch.empty((B, Hq), dtype=torch.float32, device=q_t.device)
         if workspace is None:
-            workspace = _workspace(getattr(L, fn + "_workspace_size")(ctypes.byref(pat), B, Hq, Hkv, d, tab.max_pages,
-                                                                      tab.page_size), q_t.device)
-        _check(fn, getattr(L, fn)(ctypes.byref(pat), B, Hq, Hkv, d, q_t.data_ptr(), kp, vp, *scales, tab,
-                                  pos.data_ptr(), out.data_ptr(), lse.data_ptr() if lse is not None else None,
-                                  workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(None)))
+            workspace = _workspace(getattr(L, fn + "_workspace_size")(pat, B, Hq, Hkv, d, tab.max_pages, tab.page_size),
+                                   q_t.device)
+        _check(fn, getattr(L, fn)(pat, B, Hq, Hkv, d, q_t.data_ptr(), kp, vp, *scales, tab, pos_p, out.data_ptr(),
+                                  lse.data_ptr() if lse is not None else None, workspace.data_ptr(), workspace.nbytes,
+                                  _stream_of(dev)))
     return out, lse
 
 
@@ -887,38 +941,30 @@ def cowa_fwd_paged(q, k_pages, v_pages, page_table, cu_seqlens, q_start, pattern
     fp32."""
     import torch
 
-    for n_, x_ in (("q", q), ("k_pages", k_pages), ("v_pages", v_pages)):
+    for n_, x_ in (("k_pages", k_pages), ("v_pages", v_pages)):
         _bf16_cuda(n_, x_)
-    total, Hq, d = q.shape
-    if layout not in ("bthd", "bhtd") or k_pages.dim() != 4 or page_table.dim() not in (2, 3):
-        raise ValueError("k_pages is 4-D in layout 'bthd' or 'bhtd', page_table [n_seq, max_pages] or [n_seq, H_kv, max_pages]")
+    total, Hq, d = shape = q.shape
+    _bf16("q", q, shape)
+    Hkv, kp, vp, tab = _pages(k_pages, v_pages, page_table, layout, d)
     n_seq = page_table.shape[0]
-    Hkv = page_table.shape[1] if page_table.dim() == 3 else k_pages.shape[2 if layout == "bthd" else 1]
-    kp, vp, tab = _pages(k_pages, v_pages, page_table, layout, Hkv, d)
-    _int32("cu_seqlens", cu_seqlens, (n_seq + 1,))
-    _int32("q_start", q_start, (n_seq,))
+    cu_p, start_p = _int32("cu_seqlens", cu_seqlens, (n_seq + 1,)), _int32("q_start", q_start, (n_seq,))
     if out is not None:
-        _bf16_cuda("out", out)
-        if out.shape != q.shape:
-            raise ValueError("out must have the shape of q")
-    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (Hq, total) or not lse.is_contiguous()):
-        raise ValueError("lse must be a contiguous float32 [H_q, total] tensor")
-    _same_device(q, k_pages=k_pages, v_pages=v_pages, page_table=page_table, cu_seqlens=cu_seqlens, q_start=q_start,
-                 out=out, lse=lse, workspace=workspace)
-    pat = pattern.c()
+        _bf16("out", out, shape)
+    if lse is not None:
+        _lse(lse, (Hq, total))
+    dev = _device_of(q, k_pages, v_pages, page_table, cu_seqlens, q_start, out, lse, workspace)
+    pat = ctypes.byref(pattern.c())
     L = lib()
-    with _launch_on(q, stream):
+    with _launch_on(dev, stream):
         if out is None:
-            out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
         if lse is None:
             lse = torch.empty((Hq, total), dtype=torch.float32, device=q.device)
         if workspace is None:
-            workspace = _workspace(L.cowa_fwd_paged_workspace_size(ctypes.byref(pat), n_seq, total, Hq, Hkv, d), q.device)
-        t4 = lambda x: _t4(x.unsqueeze(0))
-        _check("cowa_fwd_paged", L.cowa_fwd_paged(ctypes.byref(pat), n_seq, total, Hq, Hkv, d, cu_seqlens.data_ptr(),
-                                                  q_start.data_ptr(), t4(q), kp, vp, tab, t4(out), lse.data_ptr(),
-                                                  workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                                  _stream(None)))
+            workspace = _workspace(L.cowa_fwd_paged_workspace_size(pat, n_seq, total, Hq, Hkv, d), q.device)
+        _check("cowa_fwd_paged", L.cowa_fwd_paged(pat, n_seq, total, Hq, Hkv, d, cu_p, start_p, _rows("q", q), kp, vp, tab,
+                                                  _rows("out", out), lse.data_ptr(), workspace.data_ptr(),
+                                                  workspace.nbytes, _stream_of(dev)))
     return out, lse
 
 

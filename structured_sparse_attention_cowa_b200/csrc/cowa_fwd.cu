@@ -60,7 +60,6 @@ static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsOther == kFwdThreads * kRegsLa
 constexpr int kRingMax = 8;
 constexpr int kProducerWarp = 8, kMmaWarp = 9;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
-constexpr int kBadRing = 16;  // more than the tiles between the producer and the softmax (kRingMax / 2 + 2)
 
 template <int D>
 struct FwdGeom {
@@ -90,9 +89,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cowa_fwd_kernel(const __grid_c
   __shared__ float merge_m[kBM], merge_l[kBM];
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_flag;
-  // PAGED: per tile (a ring that the producer cannot lap), the 8-row groups whose page is bad; and
-  // the barrier on which a V tile lands that still needs rows zeroed
-  __shared__ uint32_t bad_rows[PAGED ? kBadRing : 1];
+  // PAGED: set when a page with a visible key is not in the pool; and the barrier on which the box
+  // of V lands whose last rows still need to be zeroed
+  __shared__ int bad_page;
   __shared__ __align__(8) uint64_t landed;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -139,7 +138,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cowa_fwd_kernel(const __grid_c
 
   if (threadIdx.x == 0) {
     ptx::mbar_init(&q_full, 1);
-    for (int s = 0; s < Geo::kRing; ++s) { ptx::mbar_init(&kv_full[s], 1); ptx::mbar_init(&kv_empty[s], 1); }
+    for (int s = 0; s < Geo::kRing; ++s) {
+      ptx::mbar_init(&kv_full[s], PAGED ? kBN / a.box_rows : 1);
+      ptx::mbar_init(&kv_empty[s], 1);
+    }
     for (int k = 0; k < 2; ++k) {
       ptx::mbar_init(&s_full[k], 1);
       ptx::mbar_init(&p_ready[k], 4);
@@ -147,7 +149,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cowa_fwd_kernel(const __grid_c
     }
     ptx::mbar_init(&mma_final, 1);
     ptx::mbar_init(&merge_ready, 4);
-    if (PAGED) ptx::mbar_init(&landed, 1);
+    if (PAGED) {
+      ptx::mbar_init(&landed, 1);
+      bad_page = 0;
+    }
     abort_flag = 0;
     ptx::fence_mbar_init();
   }
@@ -168,90 +173,78 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cowa_fwd_kernel(const __grid_c
     // ------------------------------------------------------------------ TMA producer
     if constexpr (PAGED) {
       if (lane == 0) {
+        ptx::tma_prefetch_desc(&a.tm_q);
+        ptx::tma_prefetch_desc(&a.tm_k);
+        ptx::tma_prefetch_desc(&a.tm_v);
         ptx::mbar_arrive_expect_tx(&q_full, (has1 ? 2 : 1) * Geo::kQBytes);
         for (int u = 0; u < D / 64; ++u) {
           ptx::tma_load_4d(sQ + u * 16384, &a.tm_q, &q_full, u * 64, row0 + i * kBM, h0, 0);
           if (has1) ptx::tma_load_4d(sQ + Geo::kQBytes + u * 16384, &a.tm_q, &q_full, u * 64, row0 + i * kBM, h0 + 1, 0);
         }
       }
+      // Each of the first nbox lanes is the producer of one box of every tile: it looks up the box's page
+      // (a tile ahead), waits for the slot, announces and issues its own copies, so that no lane waits
+      // for another (a slot refilled late stalls the MMAs; with warp-wide steps in between, a 4K chunk
+      // of a 32K prompt took 6% longer).  A tile is there when all nbox lanes have arrived.
       const int rows = a.box_rows, nbox = kBN / rows;
       const int32_t* table = a.tab.ptr + pg_seq * a.tab.sb + g * a.tab.sh;
-      const int tl = imin(t1, Nk);
-      TileCursor cur;
-      cur.init(T);
-      int page = -1, slot = 0;
-      bool want = false;
-      auto look = [&](int j) {  // the page of box `lane` of key tile j, if some row of the query tile sees a key in it
-        const int p = j * kBN + lane * rows, e = imin(p + rows, tl);
-        want = lane < nbox && p < e && (p < a.pat.S || e > t0 - a.pat.L + 1 || (p < iv.hi && e > iv.lo));
-        page = -1;
-        slot = 0;
-        if (want) {
-          const int x = p / a.tab.page_size;
-          slot = p - x * a.tab.page_size;
-          page = table[x];
-        }
-      };
-      if (ntiles > 0) look(cur.j);
-      int issued = 0, fixed = -1;
-      bool ok = true;
-      for (int n = 0; ok && n < ntiles; ++n) {
-        const int j = cur.j;
-        const bool good = want && page >= 0 && page < a.tab.n_pages;
-        const uint32_t fetch = __ballot_sync(0xffffffffu, good), bad = __ballot_sync(0xffffffffu, want && !good);
-        const int my_page = page, my_slot = slot;
-        cur.next(T);
-        if (n + 1 < ntiles) look(cur.j);  // the next tile's pages, while this one waits for its slots
-        const int bytes = __popc(fetch) * rows * 128 * (D / 64);
-        uint32_t lost = 0;
-        if (bad) {
-          for (int x = 0; x < nbox; ++x)
-            if ((bad >> x) & 1) lost |= ((1u << (rows / 8)) - 1) << (x * (rows / 8));
-          if (lane == 0) a.status[3] = 1u;
-        }
-        for (int is_v = 0; is_v < 2; ++is_v) {
-          const int idx = 2 * n + is_v, s = idx % Geo::kRing;
-          if (idx >= Geo::kRing &&
-              !(ok = ptx::mbar_wait_warp(&kv_empty[s], ((idx / Geo::kRing) - 1) & 1, &abort_flag, a.status)))
-            break;
-          uint8_t* dst = sRing + s * Geo::kKVBytes;
-          // rows of V past the last key: the tile lands on a barrier of its own and they are zeroed
-          const bool tail = is_v && tl - j * kBN < kBN;
-          uint64_t* bar = tail ? &landed : &kv_full[s];
-          if (is_v && __popc(fetch) < nbox) {
-            for (int x = lane; x < kBN * 8; x += 32)  // 16-byte pieces of 128 rows
-              if (!((fetch >> (x / 8 / rows)) & 1))
+      const int tl = imin(t1, Nk), gp = a.tab.sh ? 0 : g;
+      const int box_bytes = rows * 128 * (D / 64);
+      int issued = 0;
+      if (lane < nbox && ntiles > 0) {
+        TileCursor cur;
+        cur.init(T);
+        // (the load is unconditional, at a clamped place: nothing waits for it before its tile's turn)
+        auto look = [&](int j) { return table[imin((j * kBN + lane * rows) / a.tab.page_size, a.tab.max_pages - 1)]; };
+        int next_page = look(cur.j);
+        for (int n = 0; n < ntiles; ++n) {
+          const int p = cur.j * kBN + lane * rows, e = imin(p + rows, tl);  // this box's positions
+          const int page = next_page;
+          cur.next(T);
+          if (n + 1 < ntiles) next_page = look(cur.j);
+          // some row of the query tile sees a key of the box
+          const bool want = p < e && (p < a.pat.S || e > t0 - a.pat.L + 1 || (p < iv.hi && e > iv.lo));
+          const bool good = want && page >= 0 && page < a.tab.n_pages;
+          if (want && !good) {
+            a.status[3] = 1u;
+            *reinterpret_cast<volatile int*>(&bad_page) = 1;
+          }
+          const int slot = p % a.tab.page_size;
+          bool ok = true;
+#pragma unroll
+          for (int is_v = 0; is_v < 2; ++is_v) {
+            const int idx = 2 * n + is_v, s = idx % Geo::kRing;
+            uint8_t* dst = sRing + s * Geo::kKVBytes + lane * rows * 128;
+            if (idx >= Geo::kRing &&
+                !(ok = ptx::mbar_wait(&kv_empty[s], ((idx / Geo::kRing) - 1) & 1, &abort_flag, a.status)))
+              break;
+            // rows of V without a key must be zero: not fetched, or behind the last key of the last tile
+            const int keys = is_v ? (good ? e - p : 0) : rows;
+            if (good) {
+              uint64_t* bar = keys < rows ? &landed : &kv_full[s];
+              ptx::mbar_arrive_expect_tx(bar, box_bytes);
+#pragma unroll
+              for (int u = 0; u < D / 64; ++u)
+                ptx::tma_load_4d(dst + u * 16384, is_v ? &a.tm_v : &a.tm_k, bar, u * 64, slot, gp, page);
+            }
+            if (!good || keys < rows) {
+              // at most one box of a query tile ends behind its first row (the last key's)
+              if (good) ok = ptx::mbar_wait(&landed, 0, nullptr, a.status);
+              for (int x = keys * 8; x < rows * 8; ++x)
                 for (int u = 0; u < D / 64; ++u) *reinterpret_cast<uint4*>(dst + u * 16384 + x * 16) = make_uint4(0, 0, 0, 0);
-            ptx::fence_proxy_async_smem();
+              ptx::fence_proxy_async_smem();
+              ptx::mbar_arrive(&kv_full[s]);
+            }
+            issued = idx + 1;
           }
-          __syncwarp();
-          if (lane == 0) {
-            if (!is_v) bad_rows[n % kBadRing] = lost;
-            ptx::mbar_arrive_expect_tx(bar, bytes);
-          }
-          __syncwarp();
-          if (good) {
-            for (int u = 0; u < D / 64; ++u)
-              ptx::tma_load_4d(dst + u * 16384 + lane * rows * 128, is_v ? &a.tm_v : &a.tm_k, bar, u * 64, my_slot,
-                               a.tab.sh ? 0 : g, my_page);
-          }
-          issued = idx + 1;
-          if (tail) {
-            // the last key tile (tiles come in order), so nothing is left to fetch meanwhile
-            if (!(ok = ptx::mbar_wait_warp(&landed, 0, &abort_flag, a.status))) { fixed = idx; break; }
-            for (int x = (tl - j * kBN) * 8 + lane; x < kBN * 8; x += 32)
-              for (int u = 0; u < D / 64; ++u) *reinterpret_cast<uint4*>(dst + u * 16384 + x * 16) = make_uint4(0, 0, 0, 0);
-            ptx::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&kv_full[s]);
-          }
+          if (!ok) break;
         }
       }
+      __syncwarp();
       // drain: no copy may still be landing in shared memory when the CTA exits
       ptx::mbar_wait(&q_full, 0, nullptr, a.status);
       for (int idx = (issued > Geo::kRing ? issued - Geo::kRing : 0); idx < issued; ++idx)
-        ptx::mbar_wait(idx == fixed ? &landed : &kv_full[idx % Geo::kRing], idx == fixed ? 0 : (idx / Geo::kRing) & 1,
-                       nullptr, a.status);
+        ptx::mbar_wait(&kv_full[idx % Geo::kRing], (idx / Geo::kRing) & 1, nullptr, a.status);
     } else if (lane == 0) {
       ptx::tma_prefetch_desc(&a.tm_q);
       ptx::tma_prefetch_desc(&a.tm_k);
@@ -441,7 +434,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cowa_fwd_kernel(const __grid_c
       for (int n = 0; n < ntiles; ++n, cur.next(T)) {
         if (split && (n & 1) != k) continue;
         const int s0 = cur.j * kBN;
-        bool need_mask = (s0 + kBN > Nk) || !tile_full(a.pat, iv, t0, t1, s0, imin(Nk, s0 + kBN));
+        const bool need_mask = (s0 + kBN > Nk) || !tile_full(a.pat, iv, t0, t1, s0, imin(Nk, s0 + kBN));
         if (!(ok = ptx::mbar_wait_warp(&s_full[k], cnt & 1, &abort_flag, a.status))) break;
         ptx::tc_fence_after();
         // visible key columns of row t within [s0, s0+128), relative to s0 (partial tiles only)
@@ -450,11 +443,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cowa_fwd_kernel(const __grid_c
         const int band_lo = imax(0, t - a.pat.L + 1) - s0;
         const int diag_end = t_end - s0;
         const int lr_lo = iv.lo - s0, lr_hi = imin(iv.hi, t_end) - s0;
-        uint32_t lost = 0;  // 8-column groups whose page is bad
-        if constexpr (PAGED) {
-          lost = reinterpret_cast<volatile uint32_t*>(bad_rows)[n % kBadRing];
-          need_mask |= lost != 0;
-        }
         uint32_t xr[128];
 #pragma unroll
         for (int q = 0; q < 4; ++q) ptx::tmem_ld32(s_tm + q * 32, xr + q * 32);
@@ -463,7 +451,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cowa_fwd_kernel(const __grid_c
 #pragma unroll
           for (int c = 0; c < 128; ++c) {
             const bool vis = (c < sink_end) || (c >= band_lo && c < diag_end) || (c >= lr_lo && c < lr_hi);
-            if (!vis || (PAGED && ((lost >> (c / 8)) & 1))) xr[c] = 0xff800000u;  // -inf: gives exactly 0
+            if (!vis) xr[c] = 0xff800000u;  // -inf: gives exactly 0
           }
         }
         // P = 2^(s*scale*log2e - m) with m the running max from before this tile, rounded to
@@ -541,7 +529,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cowa_fwd_kernel(const __grid_c
       const float l = la + lb;
       // ---- epilogue
       if constexpr (PAGED) {
-        if (ntiles == 0 && t < t1 && k < (has1 ? 2 : 1)) {  // a query tile past a full cache and its band
+        if (ntiles == 0 && t < t1 && k < (has1 ? 2 : 1)) {  // a query tile whose band begins past the cache
           __nv_bfloat16* z = reinterpret_cast<__nv_bfloat16*>(a.o) + (size_t)(row0 + t - q_off) * a.o_st + (size_t)(h0 + k) * a.o_sh;
           for (int c = 0; c < D / 8; ++c) reinterpret_cast<uint4*>(z)[c] = make_uint4(0, 0, 0, 0);
           a.lse[(size_t)(h0 + k) * a.total + row0 + t - q_off] = -INFINITY;
@@ -556,11 +544,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cowa_fwd_kernel(const __grid_c
       if (!split) {
         if (ok && ntiles > 0 && ptx::mbar_wait_warp(&o_done[k], 0, &abort_flag, a.status)) {
           ptx::tc_fence_after();
-          // (a paged row may see nothing: its pages are bad, or it lies past the cache)
-          const float inv = PAGED && m_used == -INFINITY ? 0.f : 1.f / l;
+          // (a paged row may see nothing, or its query tile a bad page)
+          const bool none = PAGED && (m_used == -INFINITY || *reinterpret_cast<volatile int*>(&bad_page));
+          const float inv = 1.f / l;
           if (t < t1)
-            a.lse[lse_h0 + k * lse_step] =
-                PAGED && m_used == -INFINITY ? -INFINITY : (m_used + log2f(l)) * 0.69314718055994530942f;
+            a.lse[lse_h0 + k * lse_step] = none ? -INFINITY : (m_used + log2f(l)) * 0.69314718055994530942f;
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
             uint32_t ov[32];
@@ -574,6 +562,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cowa_fwd_kernel(const __grid_c
                 for (int e = 0; e < 4; ++e)
                   w[e] = ptx::pack_bf16(__uint_as_float(ov[c8 * 8 + 2 * e]) * inv,
                                         __uint_as_float(ov[c8 * 8 + 2 * e + 1]) * inv);
+                if (none) w[0] = w[1] = w[2] = w[3] = 0u;
                 reinterpret_cast<uint4*>(orow + (size_t)k * a.o_sh)[c * 4 + c8] = make_uint4(w[0], w[1], w[2], w[3]);
               }
             }
@@ -597,9 +586,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cowa_fwd_kernel(const __grid_c
         const float f0 = m_used == -INFINITY ? 0.f : ptx::ex2(m_used - m);
         const float f1 = m1 == -INFINITY ? 0.f : ptx::ex2(m1 - m);
         const float lt = l * f0 + l1 * f1;
-        const float inv = PAGED && m == -INFINITY ? 0.f : 1.f / lt, g0 = f0 * inv, g1 = f1 * inv;
+        const bool none = PAGED && (m == -INFINITY || *reinterpret_cast<volatile int*>(&bad_page));
+        const float inv = 1.f / lt, g0 = f0 * inv, g1 = f1 * inv;
         const bool two = ntiles > 1;  // slot 1 has tiles (uniform over the CTA)
-        if (t < t1) a.lse[lse_h0] = PAGED && m == -INFINITY ? -INFINITY : (m + log2f(lt)) * 0.69314718055994530942f;
+        if (t < t1) a.lse[lse_h0] = none ? -INFINITY : (m + log2f(lt)) * 0.69314718055994530942f;
         const uint32_t o1_tm = lane_base + Geo::kColO + D;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
@@ -621,6 +611,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cowa_fwd_kernel(const __grid_c
                 }
                 w[e] = ptx::pack_bf16(x0, x1);
               }
+              if (none) w[0] = w[1] = w[2] = w[3] = 0u;
               reinterpret_cast<uint4*>(orow)[c * 4 + c8] = make_uint4(w[0], w[1], w[2], w[3]);
             }
           }

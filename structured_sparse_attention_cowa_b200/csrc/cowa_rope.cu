@@ -87,6 +87,7 @@ __global__ void __launch_bounds__(kThreads) turn_kernel(const __grid_constant__ 
   const int tid = threadIdx.x;
   const long long m0 = (long long)blockIdx.x * tok_per_block;
   const int nt = (int)(a.M - m0 < tok_per_block ? a.M - m0 : tok_per_block);
+  const int b0 = MODE == kTurn ? (int)(m0 / a.N) : 0, t0 = (int)(m0 - (long long)b0 * a.N);  // of the first token
   const int half = a.half, rd = 2 * half;
   constexpr int P = CUT == kSplit ? 8 : 4;  // pairs per unit
   const int rot_units = CUT == kSplit ? half / 8 : (CUT == kInter ? rd / 8 : 0);
@@ -96,15 +97,31 @@ __global__ void __launch_bounds__(kThreads) turn_kernel(const __grid_constant__ 
   const int u = tid % units;
   const bool active = tid < lanes * units;
 
-  auto src_of = [&](int tok, int head) -> const __nv_bfloat16* {
-    const long long m = m0 + tok;
-    const long long b = MODE == kTurn ? m / a.N : 0, t = MODE == kTurn ? m - b * a.N : m;
-    if (head < a.Hq) return a.q + b * a.q_sb + t * a.q_st + head * a.q_sh;
-    if (MODE == kTurn || head < a.Hq + a.Hk) return a.k + b * a.k_sb + t * a.k_st + (head - a.Hq) * a.k_sh;
-    return a.v + t * a.v_st + (head - a.Hq - a.Hk) * a.v_sh;
+  // The block's rows in order of (token, head); a thread's next one is `lanes` further on.
+  struct At {
+    int tok, head, b, t;
   };
-  auto fetch = [&](int tok, int head) -> Row {
-    const __nv_bfloat16* p = src_of(tok, head);
+  const int step_tok = lanes / heads, step_head = lanes % heads;
+  At at{(tid / units) / heads, (tid / units) % heads, b0, t0};
+  at.t += at.tok;
+  auto wrap = [&](At& x) {
+    if (MODE == kTurn)
+      while (x.t >= a.N) { x.t -= a.N; ++x.b; }
+  };
+  wrap(at);
+  auto next = [&](At& x) {
+    int n = step_tok;
+    x.head += step_head;
+    if (x.head >= heads) { x.head -= heads; ++n; }
+    x.tok += n;
+    x.t += n;
+    wrap(x);
+  };
+  auto fetch = [&](const At& x) -> Row {
+    const __nv_bfloat16* p;
+    if (x.head < a.Hq) p = a.q + x.b * a.q_sb + x.t * a.q_st + x.head * a.q_sh;
+    else if (MODE == kTurn || x.head < a.Hq + a.Hk) p = a.k + x.b * a.k_sb + x.t * a.k_st + (x.head - a.Hq) * a.k_sh;
+    else p = a.v + x.t * a.v_st + (x.head - a.Hq - a.Hk) * a.v_sh;
     Row r;
     r.hi = make_uint4(0, 0, 0, 0);
     if (CUT == kSplit && u < rot_units) {
@@ -115,33 +132,52 @@ __global__ void __launch_bounds__(kThreads) turn_kernel(const __grid_constant__ 
     }
     return r;
   };
-  // rows in order of (token, head); this thread's next one
-  int tok = 0, head = tid / units;
-  auto settle = [&]() {
-    while (head >= heads) { head -= heads; ++tok; }
+  // the rows at hand, fetched before the angles are computed; kRows of them, so that enough bytes
+  // are on their way
+  constexpr int kRows = CUT == kSplit ? 1 : 2;
+  Row cur[kRows];
+  At where[kRows];
+  auto refill = [&]() {
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      where[i] = at;
+      if (active && at.tok < nt) cur[i] = fetch(at);
+      next(at);
+    }
   };
-  settle();
-  Row cur;
-  bool have = active && tok < nt;
-  if (have) cur = fetch(tok, head);
+  refill();
 
   for (int x = tid; x < nt * half; x += kThreads) {
     const int tk = x / half, i = x - tk * half;
-    const long long m = m0 + tk;
     const int axis = (i >= a.end0) + (i >= a.end1) + (i >= a.end2);
     int p;
     if (a.pos) {
-      const long long b = MODE == kTurn ? m / a.N : 0, t = MODE == kTurn ? m - b * a.N : m;
-      p = a.pos[axis * a.pos_sa + b * a.pos_sb + t];
+      At x0{0, 0, b0, t0 + tk};
+      wrap(x0);
+      p = a.pos[axis * a.pos_sa + x0.b * a.pos_sb + x0.t];
+    } else if (MODE == kTurn) {
+      At x0{0, 0, b0, t0 + tk};
+      wrap(x0);
+      p = x0.t;
     } else {
-      p = MODE == kTurn ? (int)(m % a.N) : a.cache_pos[m];
+      p = a.cache_pos[m0 + tk];
     }
     double turns = (double)p * (double)a.inv_freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
     turns -= rint(turns);
     float s, c;
-    sincospif((float)(2.0 * turns), &s, &c);
-    c *= a.scale;
-    s *= a.sin_scale;
+    if (MODE == kPagesE4m3) {
+      double s64, c64;
+      sincospi(2.0 * turns, &s64, &c64);
+      s64 *= (double)a.sin_scale;
+      c64 *= (double)a.scale;
+      tab64[x] = make_double2(c64, s64);
+      s = (float)s64;
+      c = (float)c64;
+    } else {
+      sincospif((float)(2.0 * turns), &s, &c);
+      c *= a.scale;
+      s *= a.sin_scale;
+    }
     if (CUT == kAny) {
       reinterpret_cast<float2*>(tab)[x] = make_float2(c, s);
     } else {
@@ -149,11 +185,6 @@ __global__ void __launch_bounds__(kThreads) turn_kernel(const __grid_constant__ 
       float* base = tab + (size_t)tk * rd + 4 * un + (j & 3);
       base[(j >> 2) * 4 * rot_units] = c;
       base[((P / 4) + (j >> 2)) * 4 * rot_units] = s;
-    }
-    if (MODE == kPagesE4m3) {
-      double s64, c64;
-      sincospi(2.0 * turns, &s64, &c64);
-      tab64[x] = make_double2(c64 * (double)a.scale, s64 * (double)a.sin_scale);
     }
   }
   if (MODE != kTurn) {
@@ -177,61 +208,52 @@ __global__ void __launch_bounds__(kThreads) turn_kernel(const __grid_constant__ 
   }
   __syncthreads();
 
-  // a whole number of passes for every thread: kAny exchanges pieces within the block's warps
-  const int passes = (nt * heads + lanes - 1) / lanes;
-  for (int it = 0; it < passes; ++it) {
-    const int t0 = tok, h0 = head;
-    const Row r = cur;
-    const bool mine = have;
-    head += lanes;
-    settle();
-    have = active && tok < nt;
-    if (have) cur = fetch(tok, head);
-
+  // turns one row's unit and writes it where it belongs
+  auto put = [&](const Row& r, const At& x, bool mine) {
     if (CUT == kAny) {
       // the row's pieces side by side in shared memory, for the partners of this one's elements
       __syncthreads();
       if (mine) *reinterpret_cast<uint4*>(stage + 8 * tid) = r.lo;
       __syncthreads();
     }
-    if (!mine) continue;
-    const bool is_q = h0 < a.Hq, is_v = MODE != kTurn && h0 >= a.Hq + a.Hk;
+    if (!mine) return;
+    const bool is_q = x.head < a.Hq, is_v = MODE != kTurn && x.head >= a.Hq + a.Hk;
     float lo[8], hi[8];
     widen8(r.lo, lo);
     if (CUT == kSplit) widen8(r.hi, hi);
     const bool exact = MODE == kPagesE4m3 && !is_q;
     if (!is_v) {
       if (CUT == kAny) {
-        const __nv_bfloat16* row = stage + 8 * (tid - u);
+        const __nv_bfloat16* whole = stage + 8 * (tid - u);
         for (int e = 0; e < 8; ++e) {
-          const int x = 8 * u + e;
-          if (x >= rd) break;
-          const int i = a.interleaved ? x >> 1 : (x < half ? x : x - half);
-          const bool second = a.interleaved ? (x & 1) : x >= half;
-          const int y = a.interleaved ? x ^ 1 : (second ? x - half : x + half);
-          const float other = __bfloat162float(row[y]);
+          const int n = 8 * u + e;
+          if (n >= rd) break;
+          const int i = a.interleaved ? n >> 1 : (n < half ? n : n - half);
+          const bool second = a.interleaved ? (n & 1) : n >= half;
+          const int y = a.interleaved ? n ^ 1 : (second ? n - half : n + half);
+          const float other = __bfloat162float(whole[y]);
           if (exact) {
-            const double2 cs = tab64[t0 * half + i];
+            const double2 cs = tab64[x.tok * half + i];
             lo[e] = (float)(second ? fma((double)lo[e], cs.x, (double)other * cs.y)
                                    : fma((double)lo[e], cs.x, -((double)other * cs.y)));
           } else {
-            const float2 cs = reinterpret_cast<const float2*>(tab)[t0 * half + i];
+            const float2 cs = reinterpret_cast<const float2*>(tab)[x.tok * half + i];
             lo[e] = second ? fmaf(lo[e], cs.x, other * cs.y) : fmaf(lo[e], cs.x, -(other * cs.y));
           }
         }
       } else if (u < rot_units) {
         if (exact) {
-          const double2* cs = tab64 + t0 * half + P * u;
+          const double2* cs = tab64 + x.tok * half + P * u;
 #pragma unroll
           for (int j = 0; j < P; ++j) {
-            float& x = CUT == kSplit ? lo[j] : lo[2 * j];
-            float& y = CUT == kSplit ? hi[j] : lo[2 * j + 1];
-            const double xa = x, xb = y, c = cs[j].x, s = cs[j].y;
-            x = (float)fma(xa, c, -(xb * s));
-            y = (float)fma(xb, c, xa * s);
+            float& ea = CUT == kSplit ? lo[j] : lo[2 * j];
+            float& eb = CUT == kSplit ? hi[j] : lo[2 * j + 1];
+            const double xa = ea, xb = eb, c = cs[j].x, s = cs[j].y;
+            ea = (float)fma(xa, c, -(xb * s));
+            eb = (float)fma(xb, c, xa * s);
           }
         } else {
-          const float4* cs = reinterpret_cast<const float4*>(tab + (size_t)t0 * rd) + u;
+          const float4* cs = reinterpret_cast<const float4*>(tab + (size_t)x.tok * rd) + u;
           float c[P], s[P];
 #pragma unroll
           for (int w = 0; w < P / 4; ++w) {
@@ -241,42 +263,52 @@ __global__ void __launch_bounds__(kThreads) turn_kernel(const __grid_constant__ 
           }
 #pragma unroll
           for (int j = 0; j < P; ++j) {
-            float& x = CUT == kSplit ? lo[j] : lo[2 * j];
-            float& y = CUT == kSplit ? hi[j] : lo[2 * j + 1];
-            const float xa = x, xb = y;
-            x = fmaf(xa, c[j], -(xb * s[j]));
-            y = fmaf(xb, c[j], xa * s[j]);
+            float& ea = CUT == kSplit ? lo[j] : lo[2 * j];
+            float& eb = CUT == kSplit ? hi[j] : lo[2 * j + 1];
+            const float xa = ea, xb = eb;
+            ea = fmaf(xa, c[j], -(xb * s[j]));
+            eb = fmaf(xb, c[j], xa * s[j]);
           }
         }
       }
     }
-    // elements [at, at + 8) and, for a rotated kSplit unit, [at2, at2 + 8)
+    // elements [e1, e1 + 8) and, for a rotated kSplit unit, [e2, e2 + 8)
     const bool two = CUT == kSplit && u < rot_units;
-    const int at = CUT == kSplit && !two ? rd + 8 * (u - rot_units) : 8 * u, at2 = half + 8 * u;
+    const int e1 = CUT == kSplit && !two ? rd + 8 * (u - rot_units) : 8 * u, e2 = half + 8 * u;
     if (MODE == kTurn || is_q) {
-      const long long m = m0 + t0;
-      const long long b = MODE == kTurn ? m / a.N : 0, t = MODE == kTurn ? m - b * a.N : m;
-      if (MODE != kTurn && !live[t0]) continue;
-      __nv_bfloat16* o = is_q ? a.qo + b * a.qo_sb + t * a.qo_st + h0 * a.qo_sh
-                              : a.ko + b * a.ko_sb + t * a.ko_st + (h0 - a.Hq) * a.ko_sh;
-      *reinterpret_cast<uint4*>(o + at) = narrow8(lo);
-      if (two) *reinterpret_cast<uint4*>(o + at2) = narrow8(hi);
+      if (MODE != kTurn && !live[x.tok]) return;
+      __nv_bfloat16* o = is_q ? a.qo + x.b * a.qo_sb + x.t * a.qo_st + x.head * a.qo_sh
+                              : a.ko + x.b * a.ko_sb + x.t * a.ko_st + (x.head - a.Hq) * a.ko_sh;
+      *reinterpret_cast<uint4*>(o + e1) = narrow8(lo);
+      if (two) *reinterpret_cast<uint4*>(o + e2) = narrow8(hi);
     } else {
-      const int g = h0 - a.Hq - (is_v ? a.Hk : 0);
-      const longlong2 at_kv = dst[t0 * a.Hk + g];
+      const int g = x.head - a.Hq - (is_v ? a.Hk : 0);
+      const longlong2 at_kv = dst[x.tok * a.Hk + g];
       const long long off = is_v ? at_kv.y : at_kv.x;
-      if (off < 0) continue;
+      if (off < 0) return;
       if (MODE == kPagesBf16) {
         __nv_bfloat16* o = static_cast<__nv_bfloat16*>(is_v ? a.vp : a.kp) + off;
-        *reinterpret_cast<uint4*>(o + at) = narrow8(lo);
-        if (two) *reinterpret_cast<uint4*>(o + at2) = narrow8(hi);
+        *reinterpret_cast<uint4*>(o + e1) = narrow8(lo);
+        if (two) *reinterpret_cast<uint4*>(o + e2) = narrow8(hi);
       } else {
         uint8_t* o = static_cast<uint8_t*>(is_v ? a.vp : a.kp) + off;
         const float inv = is_v ? a.inv_v : a.inv_k;
-        *reinterpret_cast<uint2*>(o + at) = codes8(lo, inv);
-        if (two) *reinterpret_cast<uint2*>(o + at2) = codes8(hi, inv);
+        *reinterpret_cast<uint2*>(o + e1) = codes8(lo, inv);
+        if (two) *reinterpret_cast<uint2*>(o + e2) = codes8(hi, inv);
       }
     }
+  };
+
+  // a whole number of passes for every thread: kAny exchanges pieces within the block
+  const int passes = (nt * heads + kRows * lanes - 1) / (kRows * lanes);
+  for (int it = 0; it < passes; ++it) {
+    Row row[kRows];
+    At of[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) { row[i] = cur[i]; of[i] = where[i]; }
+    if (it + 1 < passes) refill();
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) put(row[i], of[i], active && of[i].tok < nt);
   }
 }
 

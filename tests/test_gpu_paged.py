@@ -574,19 +574,20 @@ def test_chunks_equal_the_contiguous_forward(cuda_device):
 
 
 @pytest.mark.parametrize("Hq", [2, 3, 4])
-def test_chunk_bad_entries_and_overlong_sequences(cuda_device, Hq):
-    """Bad entries: their keys left out and reported; a sequence without a page: zeros and -inf.  A chunk
-    longer than the cache starts at 0, and its rows past the capacity see what there is (none, if the band
-    has passed it); a start past the end is moved back."""
-    Hkv, d, ps, n = 1, 64, 16, 20
+@pytest.mark.parametrize("ps", [16, 64])
+def test_chunk_bad_entries_and_overlong_sequences(cuda_device, Hq, ps):
+    """A bad entry leaves the query tiles (128 rows) that see a key of its page empty and is reported; the
+    other tiles are not touched by it.  A chunk longer than the cache starts at 0, and its rows past the
+    capacity see what there is (none, if the band has passed it); a start past the end is moved back."""
+    Hkv, d, n = 1, 64, 320 // ps
     cap = n * ps
     pat = cw.Pattern(0, 40, 0, 1)
     tab, n_pages = make_table(np.random.default_rng(94), 4, n)
-    tab[0, [3, 9]] = -1, n_pages
+    tab[0, [64 // ps, 300 // ps]] = -1, n_pages
     tab[1, :] = 2**31 - 1
     (k64, kd), (v64, vd) = (host_and_device((n_pages, ps, Hkv, d), x, cuda_device, 94) for x in ("k", "v"))
-    chunks = [(20, 200), (50, 70), (-5, cap + 90), (10**9, 30)]
-    real = [(20, 200), (50, 70), (0, cap + 90), (cap - 30, 30)]
+    chunks = [(20, 240), (50, 70), (-5, cap + 90), (10**9, 30)]
+    real = [(20, 240), (50, 70), (0, cap + 90), (cap - 30, 30)]
     lens = [r for _, r in chunks]
     cu = np.cumsum([0] + lens)
     q64, q = host_and_device((int(cu[-1]), Hq, d), "q", cuda_device, 94)
@@ -597,9 +598,17 @@ def test_chunk_bad_entries_and_overlong_sequences(cuda_device, Hq):
     assert cw.workspace_status(ws) == 8 and cw.workspace_status(ws) == 0
     k, has = orp.gather_pages(k64, tab, cap)
     v, _ = orp.gather_pages(v64, tab, cap)
+    empty = []
     for b, (start, rows) in enumerate(real):
-        r = slice(cu[b], cu[b + 1])
-        assert_chunk(o[r], lse[:, r], q64[r], k[b], v[b], start, pat, has[b])
+        for i in range(0, rows, 128):
+            m = min(128, rows - i)
+            r = slice(cu[b] + i, cu[b] + i + m)
+            see = orc.visible_mask(np.arange(start + i, start + i + m), cap, oracle_pattern(pat), 0, 1).any(0)
+            ok = np.full((1, cap), (see <= has[b, 0]).all())
+            empty.append(not ok.all())
+            assert_chunk(o[r], lse[:, r], q64[r], k[b], v[b], start + i, pat, ok)
+    # (with pages of 64 the second tile of sequence 0 sees both bad entries' pages, with 16 neither)
+    assert empty == [True, ps == 64, True] + [False] * (len(empty) - 3)
 
 
 def test_chunk_graph_stream_and_refusals(cuda_device):
