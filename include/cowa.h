@@ -402,7 +402,8 @@ cowa_status cowa_paged_append_fp8(const cowa_rotary* rot, int total, int n_seq, 
  * [0, n_pages) is left out of the softmax and reported as COWA_ERR_PAGE by cowa_workspace_status (a row
  * with no key left: o 0, lse -inf).  Rows of the pages that are not visible are never used, whatever
  * they hold.  The workspace's first 256 bytes must be zero before its first call.
- * Other arguments, ownership and errors as for cowa_decode. */
+ * COWA_ERR_UNSUPPORTED (size 0) if the call could have 2^31 tiles of 64 visible positions or more, over
+ * all sequences and KV heads.  Other arguments, ownership and errors as for cowa_decode. */
 size_t cowa_decode_paged_workspace_size(const cowa_pattern* pat, int B, int H_q, int H_kv, int d, int max_pages,
                                         int page_size);
 cowa_status cowa_decode_paged(const cowa_pattern* pat, int B, int H_q, int H_kv, int d, const void* q_t,

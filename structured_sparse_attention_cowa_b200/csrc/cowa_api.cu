@@ -789,7 +789,8 @@ size_t paged_workspace(const cowa_pattern* pat, int B, int Hq, int Hkv, int d, b
   if (check_pattern(pat, Hkv, &p) != COWA_OK || check_heads(B, 1, Hq, Hkv, d) != COWA_OK || (e4m3 && d != 128) ||
       max_pages < 1 || page_size < 8 || page_size % 8 != 0 || (int64_t)max_pages * page_size > (1 << 30))
     return 0;
-  return kWsHeader + paged_decode_bytes(paged_decode_grid(p, B, Hq, Hkv, d, e4m3, max_pages, page_size), Hq / Hkv, d);
+  const int grid = paged_decode_grid(p, B, Hq, Hkv, d, e4m3, max_pages, page_size);
+  return grid > 0 ? kWsHeader + paged_decode_bytes(grid, Hq / Hkv, d) : 0;
 }
 
 cowa_status decode_paged(const cowa_pattern* pat, int B, int Hq, int Hkv, int d, const void* q_t, const cowa_tensor& kp,
@@ -798,7 +799,6 @@ cowa_status decode_paged(const cowa_pattern* pat, int B, int Hq, int Hkv, int d,
   Pat p;
   COWA_TRY(check_pattern(pat, Hkv, &p));
   COWA_TRY(check_heads(B, 1, Hq, Hkv, d));
-  if ((int64_t)B * Hkv > 0x3fffffff) return COWA_ERR_INVALID_ARG;
   if (e4m3 && d != 128) return COWA_ERR_UNSUPPORTED;
   if (!q_t || !pos || !o) return COWA_ERR_INVALID_ARG;
   if (e4m3 && (!(k_scale > 0.f) || !(v_scale > 0.f) || !isfinite(k_scale) || !isfinite(v_scale)))
@@ -811,16 +811,21 @@ cowa_status decode_paged(const cowa_pattern* pat, int B, int Hq, int Hkv, int d,
   if (!aligned16(q_t) || !aligned16(o) || (reinterpret_cast<uintptr_t>(pos) & 3u) ||
       (reinterpret_cast<uintptr_t>(lse) & 3u))
     return COWA_ERR_ALIGNMENT;
-  COWA_TRY(check_ws(ws, ws_bytes, paged_workspace(pat, B, Hq, Hkv, d, e4m3, table.max_pages, table.page_size)));
+  a.grid = paged_decode_grid(p, B, Hq, Hkv, d, e4m3, table.max_pages, table.page_size);
+  if (a.grid == 0 || (int64_t)B * Hq > 0x7fffffff) return COWA_ERR_UNSUPPORTED;
+  COWA_TRY(check_ws(ws, ws_bytes, kWsHeader + paged_decode_bytes(a.grid, Hq / Hkv, d)));
   a.pat = p; a.B = B; a.Hkv = Hkv; a.grp = Hq / Hkv;
   a.q_t = q_t; a.pos = pos; a.o = o; a.lse = lse;
   a.status = reinterpret_cast<uint32_t*>(ws);
-  a.grid = paged_decode_grid(p, B, Hq, Hkv, d, e4m3, table.max_pages, table.page_size);
+  for (int g = 0; g < Hkv && g < kPagedIv; ++g) a.iv[g] = interval_of(p, g);
   a.rec = reinterpret_cast<int4*>(reinterpret_cast<char*>(ws) + kWsHeader);
   a.part = reinterpret_cast<float*>(reinterpret_cast<char*>(a.rec) + align_up((size_t)a.grid * sizeof(int4), 256));
   a.scale_log2 = scale_of(pat, d) * 1.4426950408889634f * (e4m3 ? k_scale : 1.f);
   a.v_scale = v_scale;
   a.box_rows = page_box_rows(table.page_size, 64);
+  a.page_shift = -1;
+  for (int x = 3; x < 31; ++x)
+    if (table.page_size == 1 << x) a.page_shift = x;
   const int h = table.per_head ? 1 : Hkv;
   auto map = e4m3 ? make_tmap_u8 : make_tmap_bf16;
   if (!map(&a.tm_k, kp.ptr, d, table.page_size, h, table.n_pages, kp.stride_t, kp.stride_h, kp.stride_b, a.box_rows) ||

@@ -74,8 +74,10 @@ struct PageTab {
   int64_t sb, sh;
   int max_pages, page_size, n_pages, n_seq;
 };
+constexpr int kPagedIv = 64;  // heads whose intervals travel with the arguments
 struct PagedDecodeArgs {
   Pat pat;
+  Range iv[kPagedIv];  // interval_of each KV head (more than kPagedIv heads: worked out on the device)
   int B, Hkv, grp;   // grp: query heads per KV head
   PageTab tab;
   const void* q_t;
@@ -83,11 +85,12 @@ struct PagedDecodeArgs {
   void* o;
   float* lse;        // may be null
   uint32_t* status;  // word 3: a visible page's entry was outside the pool
-  int4* rec;         // [grid]: {b, g, last CTA} of the pair that begins in CTA c and does not end there; x = -1: none
+  int4* rec;         // [grid]: {pair, last CTA} of the (b, g) that begins in CTA c and does not end there; x = -1: none
   float* part;       // [2 grid][grp][d + 2] fp32 partials: m, l, o
   float scale_log2, v_scale;
   int grid;
   int box_rows;      // rows per TMA box: the largest power of two up to 64 that divides the page size
+  int page_shift;    // log2 of the page size, -1 if it is not a power of two
   CUtensorMap tm_k, tm_v;
 };
 int paged_decode_grid(const Pat& p, int B, int Hq, int Hkv, int d, bool kv8, int max_pages, int page_size);

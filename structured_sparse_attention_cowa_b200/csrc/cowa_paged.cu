@@ -11,9 +11,12 @@
 //     the tile counts itself (integer arithmetic on pos) and takes an equal, contiguous share of the
 //     list.  A pair that lies inside one CTA's share is finished there; one that several CTAs share
 //     leaves fp32 partials (at most two per CTA), which a second kernel joins in order.
-//   * A producer warp looks up the pages (one lane per box of 8 to 64 rows, one tile ahead of the
+//   * A producer warp looks up the pages (one lane per box of 8 to 64 rows, two tiles ahead of the
 //     copies) and streams K and V tiles into a shared-memory ring with TMA; boxes that hold no
 //     visible key are not fetched.
+//   * Short sequences make short segments, so a segment costs little: the intervals of the heads are
+//     arguments, each warp works out 32 pairs at once (a lane each) and hands them on by shuffles, and
+//     the query rows of the next segment are fetched while the warps of this one are joined.
 //   * 4 compute warps each take 16 tokens of a tile.  Tokens are the 16 rows of the warp MMAs
 //     (m16n8k16) and the query heads of the group (at most 8) their 8 columns, so no MMA row is
 //     wasted: S^T = K Q^T and O^T += V^T P^T, the scores turned into the P^T operand with two 8x8
@@ -56,48 +59,81 @@ struct Geo {
   static int ctas(int grp) { return imin(kCtas, (228 * 1024) / (smem(grp) + 1024)); }
 };
 
-// the (sequence, KV head) pair `item`: its visible ranges at pos[b] and their 64-position tiles
+// A (sequence, KV head) pair: its visible ranges at pos[b] and their 64-position tiles.
 struct Pair {
-  int b, g, n;
-  int lo0, hi0, lo1, hi1, lo2, hi2;  // visible ranges, sorted and disjoint (empty: hi <= lo)
-  int n0, n1;                        // tiles of the first two
+  int b, n;
+  int lo0, hi0, lo1, hi1, lo2, hi2;  // visible ranges, sorted and disjoint (empty: 0, 0)
   __device__ __forceinline__ void tile(int i, int& base, int& lo, int& hi) const {
-    int first = lo0 / kTok;
     lo = lo0; hi = hi0;
+    int n0 = tiles_of(lo0, hi0);
     if (i >= n0) {
       i -= n0;
       lo = lo1; hi = hi1;
-      if (i >= n1) { i -= n1; lo = lo2; hi = hi2; }
-      first = lo / kTok;
+      n0 = tiles_of(lo1, hi1);
+      if (i >= n0) { i -= n0; lo = lo2; hi = hi2; }
     }
-    base = (first + i) * kTok;
+    base = (lo / kTok + i) * kTok;
     lo = imax(lo, base);
     hi = imin(hi, base + kTok);
   }
+  __device__ __forceinline__ static int tiles_of(int lo, int hi) {
+    return hi > lo ? (hi + kTok - 1) / kTok - lo / kTok : 0;
+  }
 };
-
-__device__ __forceinline__ int tiles_of(int lo, int hi) { return hi > lo ? (hi + kTok - 1) / kTok - lo / kTok : 0; }
 
 __device__ __forceinline__ Pair pair_of(const PagedDecodeArgs& a, int item) {
   Pair s;
   s.b = item / a.Hkv;
-  s.g = item - s.b * a.Hkv;
+  const int g = item - s.b * a.Hkv;
   int t = a.pos[s.b];
   const int cap = a.tab.max_pages * a.tab.page_size;
   if (t >= cap) t = cap - 1;
+  const Range iv = a.Hkv <= kPagedIv ? a.iv[g] : interval_of(a.pat, g);
   Range r[3] = {{0, 0}, {0, 0}, {0, 0}};
   if (t >= 0) {
-    const int n = row_ranges(a.pat, interval_of(a.pat, s.g), t, r);
+    const int n = row_ranges(a.pat, iv, t, r);
 #pragma unroll
     for (int i = 0; i < 3; ++i)
       if (i >= n) r[i] = Range{0, 0};
   }
   s.lo0 = r[0].lo; s.hi0 = r[0].hi; s.lo1 = r[1].lo; s.hi1 = r[1].hi; s.lo2 = r[2].lo; s.hi2 = r[2].hi;
-  s.n0 = tiles_of(s.lo0, s.hi0);
-  s.n1 = tiles_of(s.lo1, s.hi1);
-  s.n = s.n0 + s.n1 + tiles_of(s.lo2, s.hi2);
+  s.n = Pair::tiles_of(s.lo0, s.hi0) + Pair::tiles_of(s.lo1, s.hi1) + Pair::tiles_of(s.lo2, s.hi2);
   return s;
 }
+
+// 32 pairs, one per lane, handed to the whole warp one at a time (all lanes call with the same item,
+// items not decreasing): the tile counts alone, or everything.
+struct Counts {
+  int first, n;
+  __device__ __forceinline__ void fill(const PagedDecodeArgs& a, int from, int n_items) {
+    first = from;
+    const int i = from + (threadIdx.x & 31);
+    n = i < n_items ? pair_of(a, i).n : 0;
+  }
+  __device__ __forceinline__ int get(const PagedDecodeArgs& a, int item, int n_items) {
+    if (item - first >= 32) fill(a, item, n_items);
+    return __shfl_sync(0xffffffffu, n, item - first);
+  }
+};
+struct Window {
+  int first;
+  Pair p;
+  __device__ __forceinline__ void fill(const PagedDecodeArgs& a, int from, int n_items) {
+    first = from;
+    const int i = from + (threadIdx.x & 31);
+    p = pair_of(a, i < n_items ? i : n_items - 1);
+    if (i >= n_items) p.n = 0;
+  }
+  __device__ __forceinline__ Pair get(const PagedDecodeArgs& a, int item, int n_items) {
+    if (item - first >= 32) fill(a, item, n_items);
+    const int l = item - first;
+    auto sh = [&](int x) { return __shfl_sync(0xffffffffu, x, l); };
+    Pair s;
+    s.b = sh(p.b); s.n = sh(p.n);
+    s.lo0 = sh(p.lo0); s.hi0 = sh(p.hi0); s.lo1 = sh(p.lo1); s.hi1 = sh(p.hi1); s.lo2 = sh(p.lo2); s.hi2 = sh(p.hi2);
+    return s;
+  }
+};
 
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
   uint32_t r;
@@ -173,9 +209,15 @@ struct State {
   }
 };
 
-// First tile of CTA c's share of W tiles cut into G shares (none of a cut into more shares than tiles
-// is empty: G is then W).
-__device__ __forceinline__ long long share(long long W, int G, int c) { return c >= G ? W : W * c / G; }
+// W tiles in G shares: the first `more` shares hold one tile more than the `each` of the others.
+struct Shares {
+  int each, more;
+  __device__ __forceinline__ int begin(int c) const { return c * each + imin(c, more); }
+  __device__ __forceinline__ int of(int w) const {  // the share that holds tile w
+    const int big = more * (each + 1);
+    return w < big ? w / (each + 1) : more + (w - big) / each;
+  }
+};
 
 template <int D, bool KV8>
 __global__ void __launch_bounds__(kThreads, Geo<D, KV8>::kCtas)
@@ -187,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV8>::kCtas)
   uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + G_::kOffBar);
   uint64_t* empty_bar = full_bar + kStages;
   volatile uint64_t* seen = empty_bar + kStages;  // per stage: the tile's visible positions
-  long long* warp_sum = reinterpret_cast<long long*>(full_bar + 16);  // [5]
+  int* warp_sum = reinterpret_cast<int*>(full_bar + 16);  // [5]
   volatile int& abort_flag = *reinterpret_cast<volatile int*>(full_bar + 24);
   int& first_item = *reinterpret_cast<int*>(full_bar + 25);
   int& first_off = *reinterpret_cast<int*>(full_bar + 26);
@@ -203,36 +245,42 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV8>::kCtas)
     }
     abort_flag = 0;
     ptx::fence_mbar_init();
+    ptx::tma_prefetch_desc(&a.tm_k);
+    ptx::tma_prefetch_desc(&a.tm_v);
   }
-  // the joining kernel may be set up while this one runs (it waits for this one's results)
+  // this kernel was set up while the one before it in the stream ran; the joining kernel may be set up
+  // while this one runs (each waits for the results of the one before)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // ---- this CTA's share: tiles [w0, w1) of the list
   const int per = (n_items + kThreads - 1) / kThreads;
   const int i0 = imin(n_items, (int)threadIdx.x * per), i1 = imin(n_items, i0 + per);
-  long long mine = 0;
+  int mine = 0;
   for (int i = i0; i < i1; ++i) mine += pair_of(a, i).n;
-  long long incl = mine;
+  int incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += y;
   }
   if (lane == 31) warp_sum[warp] = incl;
   __syncthreads();
-  long long before = incl - mine, W = 0;
+  int before = incl - mine, W = 0;
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) before += warp_sum[w];
     W += warp_sum[w];
   }
-  const int G = W < (long long)gridDim.x ? (int)W : (int)gridDim.x;
-  const long long w0 = share(W, G, c), w1 = share(W, G, c + 1);
+  // no share is empty: with fewer tiles than CTAs the last CTAs have none
+  const int G = W < (int)gridDim.x ? W : (int)gridDim.x;
+  const Shares sh{G ? W / G : 0, G ? W % G : 0};
+  const int w0 = c < G ? sh.begin(c) : W, w1 = c < G ? sh.begin(c + 1) : W;
   if (w0 < w1 && before <= w0 && w0 < before + mine) {
-    long long p = before;
+    int p = before;
     for (int i = i0; i < i1; ++i) {
-      const int n = pair_of(a, i).n;
-      if (w0 < p + n) { first_item = i; first_off = (int)(w0 - p); break; }
+      const int n = per == 1 ? mine : pair_of(a, i).n;
+      if (w0 < p + n) { first_item = i; first_off = w0 - p; break; }
       p += n;
     }
   }
@@ -242,48 +290,43 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV8>::kCtas)
   if (warp == kWarps) {
     // ------------------------------------------------------------------ producer
     if (w0 < w1 && pool_ok) {
-      if (lane == 0) {
-        ptx::tma_prefetch_desc(&a.tm_k);
-        ptx::tma_prefetch_desc(&a.tm_v);
-      }
       const int nbox = kTok / a.box_rows;
-      const int ntile = (int)(w1 - w0);
+      const int ntile = w1 - w0;
+      Window win;
+      win.fill(a, first_item, n_items);
       int item = first_item, off = first_off;
-      Pair s = pair_of(a, item);
-      // box `lane` of the tile at hand: its first position, its page (-1: nothing to fetch)
-      int base, lo, hi, page, slot;
-      bool want;
-      auto look = [&]() {
-        while (off >= s.n) { s = pair_of(a, ++item); off = 0; }
-        s.tile(off, base, lo, hi);
-        const int p = base + lane * a.box_rows;
-        want = lane < nbox && p < hi && p + a.box_rows > lo;
-        page = -1;
-        slot = 0;
-        if (want) {
-          const int i = p / a.tab.page_size;
-          slot = p - i * a.tab.page_size;
-          page = a.tab.ptr[s.b * a.tab.sb + s.g * a.tab.sh + i];
-        }
+      Pair s = win.get(a, item, n_items);
+      // Box `lane` of a tile: the page it lies in.  The load is unconditional, at a clamped place, and
+      // what it gave is looked at when the tile's turn comes, two tiles later.
+      struct Look {
+        int base, lo, hi, g, slot, page;
+        bool want;
       };
-      look();
+      auto look = [&](Look& k) {
+        while (off >= s.n) { s = win.get(a, ++item, n_items); off = 0; }
+        s.tile(off++, k.base, k.lo, k.hi);
+        k.g = item - s.b * a.Hkv;
+        const int p = k.base + (lane & (nbox - 1)) * a.box_rows;
+        k.want = lane < nbox && p < k.hi && p + a.box_rows > k.lo;
+        const int i = a.page_shift >= 0 ? p >> a.page_shift : p / a.tab.page_size;
+        k.slot = p - i * a.tab.page_size;
+        k.page = a.tab.ptr[s.b * a.tab.sb + k.g * a.tab.sh + imin(i, a.tab.max_pages - 1)];
+      };
       int issued = 0;
-      for (int st = 0; st < ntile; ++st) {
+      auto put = [&](const Look& k, int st) -> bool {
         const int sl = st % kStages;
-        const bool good = want && page >= 0 && page < a.tab.n_pages;
+        const bool good = k.want && k.page >= 0 && k.page < a.tab.n_pages;
         const uint32_t fetch = __ballot_sync(0xffffffffu, good);
-        const uint32_t bad = __ballot_sync(0xffffffffu, want && !good);
-        const int my_page = page, my_slot = slot, g = a.tab.sh ? 0 : s.g;
-        uint64_t vis = (hi - base >= kTok ? ~0ull : (1ull << (hi - base)) - 1) & ~((1ull << (lo - base)) - 1);
+        const uint32_t bad = __ballot_sync(0xffffffffu, k.want && !good);
+        uint64_t vis = (k.hi - k.base >= kTok ? ~0ull : (1ull << (k.hi - k.base)) - 1) & ~((1ull << (k.lo - k.base)) - 1);
         if (bad) {  // entries outside the pool: reported, their keys left out
           const uint64_t rows = a.box_rows == kTok ? ~0ull : (1ull << a.box_rows) - 1;
           for (int x = 0; x < nbox; ++x)
             if ((bad >> x) & 1) vis &= ~(rows << (x * a.box_rows));
           if (lane == 0) a.status[3] = 1u;
         }
-        ++off;
-        if (st + 1 < ntile) look();  // the next tile's pages, while this one waits for its slot
-        if (st >= kStages && !ptx::mbar_wait_warp(&empty_bar[sl], ((st / kStages) & 1) ^ 1, &abort_flag, a.status)) break;
+        if (st >= kStages && !ptx::mbar_wait_warp(&empty_bar[sl], ((st / kStages) & 1) ^ 1, &abort_flag, a.status))
+          return false;
         uint8_t* ks = smem + sl * 2 * G_::kTileBytes;
         uint8_t* vs = ks + G_::kTileBytes;
         if (lane == 0) {
@@ -292,14 +335,24 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV8>::kCtas)
         }
         __syncwarp();
         if (good) {
-          const int at = lane * a.box_rows * 128;
+          const int at = lane * a.box_rows * 128, g = a.tab.sh ? 0 : k.g;
 #pragma unroll
           for (int u = 0; u < G_::kUnits; ++u) {
-            ptx::tma_load_4d(ks + u * kBoxBytes + at, &a.tm_k, &full_bar[sl], u * (KV8 ? 128 : 64), my_slot, g, my_page);
-            ptx::tma_load_4d(vs + u * kBoxBytes + at, &a.tm_v, &full_bar[sl], u * (KV8 ? 128 : 64), my_slot, g, my_page);
+            ptx::tma_load_4d(ks + u * kBoxBytes + at, &a.tm_k, &full_bar[sl], u * (KV8 ? 128 : 64), k.slot, g, k.page);
+            ptx::tma_load_4d(vs + u * kBoxBytes + at, &a.tm_v, &full_bar[sl], u * (KV8 ? 128 : 64), k.slot, g, k.page);
           }
         }
         issued = st + 1;
+        return true;
+      };
+      Look even, odd;
+      look(even);
+      if (ntile > 1) look(odd);
+      for (int st = 0; st < ntile; st += 2) {  // by twos, so that nothing has to be moved between the two
+        if (!put(even, st)) break;
+        if (st + 2 < ntile) look(even);
+        if (st + 1 >= ntile || !put(odd, st + 1)) break;
+        if (st + 3 < ntile) look(odd);
       }
       // never leave the CTA with copies in flight
       for (int st = (issued > kStages ? issued - kStages : 0); st < issued; ++st)
@@ -317,36 +370,49 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV8>::kCtas)
   bool ok = pool_ok;
   if (!pool_ok && threadIdx.x == 0) atomicOr(a.status, (uint32_t)ptx::kStatusCheck);
 
-  // pairs that see nothing (a slot without a sequence): zeros and -inf, by one CTA each
-  for (int i = c; i < n_items; i += gridDim.x) {
-    const Pair s = pair_of(a, i);
-    if (s.n) continue;
-    const size_t h0 = (size_t)s.b * a.Hkv * grp + (size_t)s.g * grp;
-    for (int x = threadIdx.x; x < grp * D; x += kWarps * 32)
-      reinterpret_cast<__nv_bfloat16*>(a.o)[h0 * D + x] = __float2bfloat16_rn(0.f);
-    if (a.lse && (int)threadIdx.x < grp) a.lse[h0 + threadIdx.x] = -INFINITY;
+  // slots without a sequence see nothing: zeros and -inf, by one CTA each
+  for (int i = c; i < a.B; i += gridDim.x) {
+    if (a.pos[i] >= 0) continue;
+    const size_t h0 = (size_t)i * a.Hkv * grp;
+    for (int x = threadIdx.x; x < a.Hkv * grp * (D / 8); x += kWarps * 32)
+      reinterpret_cast<uint4*>(a.o)[h0 * (D / 8) + x] = make_uint4(0, 0, 0, 0);
+    if (a.lse)
+      for (int x = threadIdx.x; x < a.Hkv * grp; x += kWarps * 32) a.lse[h0 + x] = -INFINITY;
   }
 
   int4 rec = make_int4(-1, 0, 0, 0);
   int st = 0;
-  int item = first_item, off = first_off;
-  for (long long w = w0; w < w1;) {
-    const Pair s = pair_of(a, item);
-    const int take = (int)(w1 - w < s.n - off ? w1 - w : s.n - off);
-    if (take > 0) {
-      // Q^T fragments: columns are the heads of the group (those past it are zero)
-      uint32_t qf[KS][2];
-      const uint32_t* q = reinterpret_cast<const uint32_t*>(
-          reinterpret_cast<const __nv_bfloat16*>(a.q_t) + ((size_t)s.b * a.Hkv * grp + (size_t)s.g * grp + imin(gr, grp - 1)) * D);
+  // Q^T fragments as they stand in memory: columns are the heads of the group
+  uint32_t qn[KS][2];
+  auto load_q = [&](int it) {
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(
+        reinterpret_cast<const __nv_bfloat16*>(a.q_t) + ((size_t)it * grp + imin(gr, grp - 1)) * D);
 #pragma unroll
-      for (int kk = 0; kk < KS; ++kk) {
-        // E4M3: the head dimension is visited in another order, so that a thread's bytes of a key row are
-        // contiguous: chunk kk of thread tq is d = 32 tq + 4 kk .. + 3
-        const uint32_t x = KV8 ? q[16 * tq + 2 * kk] : q[8 * kk + tq];
-        const uint32_t y = KV8 ? q[16 * tq + 2 * kk + 1] : q[8 * kk + 4 + tq];
-        qf[kk][0] = gr < grp ? (KV8 ? bf16x2_to_f16x2(x) : x) : 0u;
-        qf[kk][1] = gr < grp ? (KV8 ? bf16x2_to_f16x2(y) : y) : 0u;
-      }
+    for (int kk = 0; kk < KS; ++kk) {
+      // E4M3: the head dimension is visited in another order, so that a thread's bytes of a key row are
+      // contiguous: chunk kk of thread tq is d = 32 tq + 4 kk .. + 3
+      qn[kk][0] = KV8 ? q[16 * tq + 2 * kk] : q[8 * kk + tq];
+      qn[kk][1] = KV8 ? q[16 * tq + 2 * kk + 1] : q[8 * kk + 4 + tq];
+    }
+  };
+  Counts counts;
+  int item = 0, off = 0, n = 0;  // n: tiles of the pair at hand, of which `off` are not this CTA's
+  if (w0 < w1) {
+    item = first_item;
+    off = first_off;
+    load_q(item);
+    counts.fill(a, item, n_items);
+    n = counts.get(a, item, n_items);
+  }
+  for (int w = w0; w < w1;) {
+    const int take = imin(w1 - w, n - off), h0 = item * grp;
+    {
+      uint32_t qf[KS][2];
+#pragma unroll
+      for (int kk = 0; kk < KS; ++kk)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)  // (columns past the group are zero)
+          qf[kk][h] = gr < grp ? (KV8 ? bf16x2_to_f16x2(qn[kk][h]) : qn[kk][h]) : 0u;
       State<D> z;
       z.clear();
       for (int i = 0; ok && i < take; ++i, ++st) {
@@ -443,6 +509,16 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV8>::kCtas)
           if (lane == 0) ptx::mbar_arrive(&empty_bar[sl]);
         }
       }
+      // ---- the next segment's pair and query rows, while the warps are joined
+      const bool begins = off == 0, ends = off + take == n;
+      if (begins && !ends) rec = make_int4(item, sh.of(w + n - 1), 0, 0);  // the CTA that holds its last tile
+      w += take;
+      off = 0;
+      if (w < w1) {
+        do n = counts.get(a, ++item, n_items);
+        while (n == 0);
+        load_q(item);
+      }
       // ---- join the warps
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) {
@@ -465,9 +541,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV8>::kCtas)
         }
       }
       asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
-      const bool begins = off == 0, ends = off + take == s.n;
       if (ok && !abort_flag) {
-        const size_t h0 = (size_t)s.b * a.Hkv * grp + (size_t)s.g * grp;
         float* part = a.part + ((size_t)2 * c + (begins ? 1 : 0)) * grp * (D + 2);
         for (int x = threadIdx.x; x < grp * D; x += kWarps * 32) {
           const int hd = x / D, d = x - hd * D;
@@ -484,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV8>::kCtas)
           }
           if (KV8) o *= a.v_scale;
           if (begins && ends) {  // the pair is finished here
-            reinterpret_cast<__nv_bfloat16*>(a.o)[(h0 + hd) * D + d] = __float2bfloat16_rn(m == -INFINITY ? 0.f : o / l);
+            reinterpret_cast<__nv_bfloat16*>(a.o)[(size_t)(h0 + hd) * D + d] = __float2bfloat16_rn(m == -INFINITY ? 0.f : o / l);
             if (a.lse && d == 0) a.lse[h0 + hd] = m == -INFINITY ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
           } else {
             part[hd * (D + 2) + 2 + d] = o;
@@ -492,16 +566,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV8>::kCtas)
           }
         }
       }
-      if (begins && !ends) {  // the pair's other tiles: CTAs c + 1 .. last
-        const long long end = w + s.n;
-        int last = c + 1;
-        while (share(W, G, last + 1) < end) ++last;
-        rec = make_int4(s.b, s.g, last, 0);
-      }
-      w += take;
     }
-    ++item;
-    off = 0;
   }
   if (threadIdx.x == 0) a.rec[c] = rec;
 }
@@ -516,7 +581,7 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
   if (rec.x < 0) return;
   constexpr int E = D / 32;
   __shared__ float sm[4], sl[4], so[4][D];
-  const int n = rec.z - c + 1;
+  const int n = rec.y - c + 1;
   const size_t slot = (size_t)a.grp * (D + 2);
   // piece 0 is CTA c's last segment, piece i CTA c + i's first
   auto piece = [&](int i) { return a.part + (i == 0 ? 2 * (size_t)c + 1 : 2 * ((size_t)c + i)) * slot + hd * (D + 2); };
@@ -544,7 +609,7 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
   const int d = threadIdx.x;
   l = sl[0] + sl[1] + sl[2] + sl[3];
   const float o = so[0][d] + so[1][d] + so[2][d] + so[3][d];
-  const size_t h = (size_t)rec.x * a.Hkv * a.grp + (size_t)rec.y * a.grp + hd;
+  const size_t h = (size_t)rec.x * a.grp + hd;
   reinterpret_cast<__nv_bfloat16*>(a.o)[h * D + d] = __float2bfloat16_rn(m == -INFINITY ? 0.f : o / l);
   if (a.lse && d == 0) a.lse[h] = m == -INFINITY ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
 }
@@ -554,31 +619,37 @@ cudaError_t launch_paged_t(const PagedDecodeArgs& a, cudaStream_t s) {
   const int bytes = Geo<D, KV8>::smem(a.grp);
   cudaError_t e = cudaFuncSetAttribute(paged_split_kernel<D, KV8>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  paged_split_kernel<D, KV8><<<a.grid, kThreads, bytes, s>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.grid, a.grp);
-  cfg.blockDim = dim3(128);
-  cfg.stream = s;
+  // both kernels are set up while the one before them runs, and wait for its results themselves
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = s;
   cfg.attrs = at;
   cfg.numAttrs = 1;
+  if ((e = cudaLaunchKernelEx(&cfg, paged_split_kernel<D, KV8>, a)) != cudaSuccess) return e;
+  cfg.gridDim = dim3(a.grid, a.grp);
+  cfg.blockDim = dim3(128);
+  cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, paged_join_kernel<D>, a);
 }
 
 }  // namespace
 
-// CTAs of a paged decode: as many as the GPU holds at once, and no more than there can be tiles.
+// CTAs of a paged decode: as many as the GPU holds at once, and no more than there can be tiles (0:
+// more tiles than the kernels can count).
 int paged_decode_grid(const Pat& p, int B, int Hq, int Hkv, int d, bool kv8, int max_pages, int page_size) {
   const int grp = Hq / Hkv;
   const int most = 148 * (kv8 ? Geo<128, true>::ctas(grp) : (d == 128 ? Geo<128, false>::ctas(grp) : Geo<64, false>::ctas(grp)));
   const int64_t cap = (int64_t)max_pages * page_size, R = (int64_t)p.T - p.S;
   const int64_t wide = R > 0 ? (R + p.H - 1) / p.H : 0;
   auto tiles = [&](int64_t n) { return n > 0 ? ((n < cap ? n : cap) + kTok - 1) / kTok + 1 : 0; };
-  const int64_t n = (tiles(p.S) + tiles(wide) + tiles(p.L)) * B * Hkv;
-  return (int)(n < most ? n : most);
+  const int64_t n = tiles(p.S) + tiles(wide) + tiles(p.L);
+  if (n > 0x7fffffff / ((int64_t)B * Hkv)) return 0;  // the kernels count tiles in 32 bits
+  return (int)(n * B * Hkv < most ? n * B * Hkv : most);
 }
 
 size_t paged_decode_bytes(int grid, int grp, int d) {

@@ -27,17 +27,18 @@ constexpr int kThreads = 256;
 constexpr int kMaxTok = 8;  // tokens per block, at most
 
 // How a row is cut into units of work:
-//   kSplit  8 pairs (i, i + r/2): two 16-byte pieces     (r/2 a multiple of 8)
-//   kInter  4 pairs (2i, 2i + 1): one 16-byte piece      (r a multiple of 8; also no rotation at all)
+//   kSplit  8 pairs (i, i + r/2): two 16-byte pieces r/2 elements apart   (r/2 a multiple of 8)
+//   kInter  8 pairs (2i, 2i + 1): two 16-byte pieces side by side          (r a multiple of 8; also no
+//           rotation at all); with r = 8 mod 16 the last unit's second piece passes through
 //   kAny    one 16-byte piece, its partners wherever they are, through shared memory
 enum { kSplit, kInter, kAny };
 // What becomes of the rows: rotated copies; bf16 pages; pages of E4M3 codes
 enum { kTurn, kPagesBf16, kPagesE4m3 };
 
-// bytes of a block's fp32 cos and sin tables, and of all its shared memory
-__host__ __device__ inline size_t table_bytes(int entries) { return ((size_t)entries * 8 + 15) / 16 * 16; }
+// bytes of a block's fp32 cos and sin tables (whole units of 8 pairs), and of all its shared memory
+__host__ __device__ inline size_t table_bytes(int tok, int half) { return (size_t)tok * ((half + 7) / 8) * 64; }
 inline size_t smem_bytes(int mode, int tok, int half, int Hk) {
-  return table_bytes(tok * half) + (mode == kPagesE4m3 ? (size_t)tok * half * 16 : 0) + (mode == kTurn ? 0 : (size_t)tok * Hk * 16);
+  return table_bytes(tok, half) + (mode == kPagesE4m3 ? (size_t)tok * half * 16 : 0) + (mode == kTurn ? 0 : (size_t)tok * Hk * 16);
 }
 
 struct Row {
@@ -71,14 +72,14 @@ __device__ __forceinline__ uint2 codes8(const float* x, float inv) {
 }
 
 template <int MODE, int CUT>
-__global__ void __launch_bounds__(kThreads) turn_kernel(const __grid_constant__ RopeArgs a, int tok_per_block) {
-  // cos and sin of the block's tokens.  Vector cuts: [token][piece][unit] of float4, the pieces being
-  // the unit's cosines (2 or 1 float4) and then its sines, so that neighbouring units are neighbours
-  // in memory.  kAny: [token][pair] of (cos, sin).
+__global__ void __launch_bounds__(kThreads, 4) turn_kernel(const __grid_constant__ RopeArgs a, int tok_per_block) {
+  // cos and sin of the block's tokens.  kSplit and kInter: [token][piece][unit] of float4, the pieces
+  // being the unit's 8 cosines and then its 8 sines, so that neighbouring units are neighbours in
+  // memory.  kAny: [token][pair] of (cos, sin).
   extern __shared__ __align__(16) unsigned char smem[];
   float* tab = reinterpret_cast<float*>(smem);
   // E4M3 keys: cos and sin in 64 bits, [token][pair]
-  double2* tab64 = reinterpret_cast<double2*>(smem + table_bytes(tok_per_block * a.half));
+  double2* tab64 = reinterpret_cast<double2*>(smem + table_bytes(tok_per_block, a.half));
   // element offset of each (token, KV head)'s key and value row in the pools, -1 for none
   longlong2* dst = reinterpret_cast<longlong2*>(tab64 + (MODE == kPagesE4m3 ? tok_per_block * a.half : 0));
   __shared__ int live[kMaxTok];
@@ -89,18 +90,19 @@ __global__ void __launch_bounds__(kThreads) turn_kernel(const __grid_constant__ 
   const int nt = (int)(a.M - m0 < tok_per_block ? a.M - m0 : tok_per_block);
   const int b0 = MODE == kTurn ? (int)(m0 / a.N) : 0, t0 = (int)(m0 - (long long)b0 * a.N);  // of the first token
   const int half = a.half, rd = 2 * half;
-  constexpr int P = CUT == kSplit ? 8 : 4;  // pairs per unit
-  const int rot_units = CUT == kSplit ? half / 8 : (CUT == kInter ? rd / 8 : 0);
-  const int units = CUT == kSplit ? rot_units + (a.d - rd) / 8 : a.d / 8;
+  const int rot_units = CUT == kAny ? 0 : (half + 7) / 8;
+  const int units = CUT == kSplit ? rot_units + (a.d - rd) / 8 : (CUT == kInter ? a.d / 16 : a.d / 8);
   const int lanes = kThreads / units;  // rows in flight
   const int heads = a.Hq + a.Hk + (MODE == kTurn ? 0 : a.Hk);
   const int u = tid % units;
   const bool active = tid < lanes * units;
 
-  // The block's rows in order of (token, head); a thread's next one is `lanes` further on.
+  // The block's rows in order of (token, head); a thread's next one is `lanes` further on.  (b, t): the
+  // token's place in its tensors; an append has one axis of tokens, and needs neither.
   struct At {
     int tok, head, b, t;
   };
+  auto t_of = [&](const At& x) -> int64_t { return MODE == kTurn ? x.t : t0 + x.tok; };
   const int step_tok = lanes / heads, step_head = lanes % heads;
   At at{(tid / units) / heads, (tid / units) % heads, b0, t0};
   at.t += at.tok;
@@ -114,19 +116,26 @@ __global__ void __launch_bounds__(kThreads) turn_kernel(const __grid_constant__ 
     x.head += step_head;
     if (x.head >= heads) { x.head -= heads; ++n; }
     x.tok += n;
-    x.t += n;
-    wrap(x);
+    if (MODE == kTurn) {
+      x.t += n;
+      wrap(x);
+    }
   };
   auto fetch = [&](const At& x) -> Row {
     const __nv_bfloat16* p;
-    if (x.head < a.Hq) p = a.q + x.b * a.q_sb + x.t * a.q_st + x.head * a.q_sh;
-    else if (MODE == kTurn || x.head < a.Hq + a.Hk) p = a.k + x.b * a.k_sb + x.t * a.k_st + (x.head - a.Hq) * a.k_sh;
-    else p = a.v + x.t * a.v_st + (x.head - a.Hq - a.Hk) * a.v_sh;
+    const int64_t t = t_of(x);
+    if (x.head < a.Hq) p = a.q + (MODE == kTurn ? x.b * a.q_sb : 0) + t * a.q_st + x.head * a.q_sh;
+    else if (MODE == kTurn) p = a.k + x.b * a.k_sb + t * a.k_st + (x.head - a.Hq) * a.k_sh;
+    else if (x.head < a.Hq + a.Hk) p = a.k + t * a.k_st + (x.head - a.Hq) * a.k_sh;
+    else p = a.v + t * a.v_st + (x.head - a.Hq - a.Hk) * a.v_sh;
     Row r;
     r.hi = make_uint4(0, 0, 0, 0);
     if (CUT == kSplit && u < rot_units) {
       r.lo = *reinterpret_cast<const uint4*>(p + 8 * u);
       r.hi = *reinterpret_cast<const uint4*>(p + half + 8 * u);
+    } else if (CUT == kInter) {
+      r.lo = *reinterpret_cast<const uint4*>(p + 16 * u);
+      r.hi = *reinterpret_cast<const uint4*>(p + 16 * u + 8);
     } else {
       r.lo = *reinterpret_cast<const uint4*>(p + (CUT == kSplit ? rd + 8 * (u - rot_units) : 8 * u));
     }
@@ -134,7 +143,7 @@ __global__ void __launch_bounds__(kThreads) turn_kernel(const __grid_constant__ 
   };
   // the rows at hand, fetched before the angles are computed; kRows of them, so that enough bytes
   // are on their way
-  constexpr int kRows = CUT == kSplit ? 1 : 2;
+  constexpr int kRows = CUT == kAny ? 2 : 1;
   Row cur[kRows];
   At where[kRows];
   auto refill = [&]() {
@@ -181,10 +190,10 @@ __global__ void __launch_bounds__(kThreads) turn_kernel(const __grid_constant__ 
     if (CUT == kAny) {
       reinterpret_cast<float2*>(tab)[x] = make_float2(c, s);
     } else {
-      const int un = i / P, j = i % P;
-      float* base = tab + (size_t)tk * rd + 4 * un + (j & 3);
+      const int un = i / 8, j = i % 8;
+      float* base = tab + (size_t)tk * 16 * rot_units + 4 * un + (j & 3);
       base[(j >> 2) * 4 * rot_units] = c;
-      base[((P / 4) + (j >> 2)) * 4 * rot_units] = s;
+      base[(2 + (j >> 2)) * 4 * rot_units] = s;
     }
   }
   if (MODE != kTurn) {
@@ -220,7 +229,7 @@ __global__ void __launch_bounds__(kThreads) turn_kernel(const __grid_constant__ 
     const bool is_q = x.head < a.Hq, is_v = MODE != kTurn && x.head >= a.Hq + a.Hk;
     float lo[8], hi[8];
     widen8(r.lo, lo);
-    if (CUT == kSplit) widen8(r.hi, hi);
+    if (CUT != kAny) widen8(r.hi, hi);
     const bool exact = MODE == kPagesE4m3 && !is_q;
     if (!is_v) {
       if (CUT == kAny) {
@@ -243,28 +252,30 @@ __global__ void __launch_bounds__(kThreads) turn_kernel(const __grid_constant__ 
         }
       } else if (u < rot_units) {
         if (exact) {
-          const double2* cs = tab64 + x.tok * half + P * u;
+          const double2* cs = tab64 + x.tok * half + 8 * u;
 #pragma unroll
-          for (int j = 0; j < P; ++j) {
-            float& ea = CUT == kSplit ? lo[j] : lo[2 * j];
-            float& eb = CUT == kSplit ? hi[j] : lo[2 * j + 1];
+          for (int j = 0; j < 8; ++j) {
+            if (CUT == kInter && j >= 4 && 8 * u + j >= half) break;
+            float& ea = CUT == kSplit ? lo[j] : (j < 4 ? lo[2 * j] : hi[2 * j - 8]);
+            float& eb = CUT == kSplit ? hi[j] : (j < 4 ? lo[2 * j + 1] : hi[2 * j - 7]);
             const double xa = ea, xb = eb, c = cs[j].x, s = cs[j].y;
             ea = (float)fma(xa, c, -(xb * s));
             eb = (float)fma(xb, c, xa * s);
           }
         } else {
-          const float4* cs = reinterpret_cast<const float4*>(tab + (size_t)x.tok * rd) + u;
-          float c[P], s[P];
+          const float4* cs = reinterpret_cast<const float4*>(tab + (size_t)x.tok * 16 * rot_units) + u;
+          float c[8], s[8];
 #pragma unroll
-          for (int w = 0; w < P / 4; ++w) {
-            const float4 cw = cs[w * rot_units], sw = cs[(P / 4 + w) * rot_units];
+          for (int w = 0; w < 2; ++w) {
+            const float4 cw = cs[w * rot_units], sw = cs[(2 + w) * rot_units];
             c[4 * w] = cw.x; c[4 * w + 1] = cw.y; c[4 * w + 2] = cw.z; c[4 * w + 3] = cw.w;
             s[4 * w] = sw.x; s[4 * w + 1] = sw.y; s[4 * w + 2] = sw.z; s[4 * w + 3] = sw.w;
           }
 #pragma unroll
-          for (int j = 0; j < P; ++j) {
-            float& ea = CUT == kSplit ? lo[j] : lo[2 * j];
-            float& eb = CUT == kSplit ? hi[j] : lo[2 * j + 1];
+          for (int j = 0; j < 8; ++j) {
+            if (CUT == kInter && j >= 4 && 8 * u + j >= half) break;
+            float& ea = CUT == kSplit ? lo[j] : (j < 4 ? lo[2 * j] : hi[2 * j - 8]);
+            float& eb = CUT == kSplit ? hi[j] : (j < 4 ? lo[2 * j + 1] : hi[2 * j - 7]);
             const float xa = ea, xb = eb;
             ea = fmaf(xa, c[j], -(xb * s[j]));
             eb = fmaf(xb, c[j], xa * s[j]);
@@ -272,13 +283,15 @@ __global__ void __launch_bounds__(kThreads) turn_kernel(const __grid_constant__ 
         }
       }
     }
-    // elements [e1, e1 + 8) and, for a rotated kSplit unit, [e2, e2 + 8)
-    const bool two = CUT == kSplit && u < rot_units;
-    const int e1 = CUT == kSplit && !two ? rd + 8 * (u - rot_units) : 8 * u, e2 = half + 8 * u;
+    // elements [e1, e1 + 8) and, where the unit has two pieces, [e2, e2 + 8)
+    const bool two = CUT == kInter || (CUT == kSplit && u < rot_units);
+    const int e1 = CUT == kSplit && !two ? rd + 8 * (u - rot_units) : (CUT == kInter ? 16 * u : 8 * u);
+    const int e2 = CUT == kInter ? e1 + 8 : half + 8 * u;
     if (MODE == kTurn || is_q) {
       if (MODE != kTurn && !live[x.tok]) return;
-      __nv_bfloat16* o = is_q ? a.qo + x.b * a.qo_sb + x.t * a.qo_st + x.head * a.qo_sh
-                              : a.ko + x.b * a.ko_sb + x.t * a.ko_st + (x.head - a.Hq) * a.ko_sh;
+      const int64_t t = t_of(x);
+      __nv_bfloat16* o = is_q ? a.qo + (MODE == kTurn ? x.b * a.qo_sb : 0) + t * a.qo_st + x.head * a.qo_sh
+                              : a.ko + x.b * a.ko_sb + t * a.ko_st + (x.head - a.Hq) * a.ko_sh;
       *reinterpret_cast<uint4*>(o + e1) = narrow8(lo);
       if (two) *reinterpret_cast<uint4*>(o + e2) = narrow8(hi);
     } else {
@@ -318,7 +331,7 @@ cudaError_t launch_turn(const RopeArgs& a, cudaStream_t s) {
   const int cut = a.half == 0 || (a.interleaved && rd % 8 == 0) ? kInter
                   : !a.interleaved && a.half % 8 == 0           ? kSplit
                                                                 : kAny;
-  const int units = cut == kSplit ? a.half / 8 + (a.d - rd) / 8 : a.d / 8;
+  const int units = cut == kSplit ? a.half / 8 + (a.d - rd) / 8 : (cut == kInter ? a.d / 16 : a.d / 8);
   const int heads = a.Hq + (MODE == kTurn ? 1 : 2) * a.Hk;
   const int lanes = kThreads / units;
   // tokens per block: enough rows to fill its threads, but no fewer blocks than the SMs can hold

@@ -66,7 +66,7 @@ def test_append_refusals(status, change):
     (1, dict(o=None)), (3, dict(q=0x10004)), (3, dict(o=0x10008)), (3, dict(lse=0x10002)), (3, dict(pos=0x9002)),
     (1, dict(kp=T(None))), (3, dict(vp=T(sb=12))), (1, dict(tab=table(page=20))), (1, dict(tab=table(n_pages=0))),
     (1, dict(tab=table(ptr=None))), (1, dict(tab=table(per_head=1, sh=0))), (4, dict(ws=None)), (4, dict(ws=0x40080)),
-    (4, dict(less=1)), (1, dict(pat=cw.Pattern(10, 4, 5, 1))), (1, dict(ks=-1.0)), (1, dict(B=2**30)),
+    (4, dict(less=1)), (1, dict(pat=cw.Pattern(10, 4, 5, 1))), (1, dict(ks=-1.0)), (2, dict(B=2**30)),
 ])
 def test_decode_refusals(status, change):
     a = dict(pat=cw.Pattern(64, 100, 1024, 4), B=3, Hq=8, Hkv=4, d=128, q=0x10000, kp=T(), vp=T(), tab=table(),
