@@ -9,7 +9,7 @@
 //   * The work is the list of 64-position tiles of all (sequence, KV head) pairs, in that order.
 //     Lengths are known on the device only, and differ from 1 to the whole cache, so every CTA adds up
 //     the tile counts itself (integer arithmetic on pos) and takes an equal, contiguous share of the
-//     list.  A pair that lies inside one CTA's share is finished there; one that several CTAs share
+//     list, in which every pair counts kSegment tiles more than it has.  A pair that lies inside one CTA's share is finished there; one that several CTAs share
 //     leaves fp32 partials (at most two per CTA), which a second kernel joins in order.
 //   * A producer warp looks up the pages (one lane per box of 8 to 64 rows, two tiles ahead of the
 //     copies) and streams K and V tiles into a shared-memory ring with TMA; boxes that hold no
@@ -38,6 +38,10 @@ constexpr int kThreads = (kWarps + 1) * 32;    // + the producer
 constexpr int kTok = 64;                       // positions per tile
 constexpr int kBoxBytes = kTok * 128;          // 64 rows x 128 bytes
 constexpr float kRescale = 8.0f;               // lazy-rescale threshold, log2 units
+// What a segment costs besides its tiles (query rows, join of the warps, a start of the pipeline), in
+// tiles: 37 sequences of 1 to 32K positions, E4M3, took 2.0 us a segment and 1.0 us a tile, and the CTAs
+// that held nine segments of one tile each twice as long as the others.
+constexpr int kSegment = 2;
 // E4M3: P is rounded to f16, whose smallest normal number is 2^-14; relative to a running maximum
 // lifted by 2^6 (P at most 2^14) it covers P down to 2^-20 of the largest at full precision.
 template <bool KV8>
@@ -209,15 +213,18 @@ struct State {
   }
 };
 
-// W tiles in G shares: the first `more` shares hold one tile more than the `each` of the others.
+// W places in G shares: the first `more` shares hold one place more than the `each` of the others.  A
+// pair of n > 0 tiles takes kSegment places and then one per tile.
 struct Shares {
   int each, more;
   __device__ __forceinline__ int begin(int c) const { return c * each + imin(c, more); }
-  __device__ __forceinline__ int of(int w) const {  // the share that holds tile w
+  __device__ __forceinline__ int of(int w) const {  // the share that holds place w
     const int big = more * (each + 1);
     return w < big ? w / (each + 1) : more + (w - big) / each;
   }
 };
+
+__device__ __forceinline__ int places(int n) { return n > 0 ? n + kSegment : 0; }
 
 template <int D, bool KV8>
 __global__ void __launch_bounds__(kThreads, Geo<D, KV8>::kCtas)
@@ -232,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV8>::kCtas)
   int* warp_sum = reinterpret_cast<int*>(full_bar + 16);  // [5]
   volatile int& abort_flag = *reinterpret_cast<volatile int*>(full_bar + 24);
   int& first_item = *reinterpret_cast<int*>(full_bar + 25);
-  int& first_off = *reinterpret_cast<int*>(full_bar + 26);
+  int& first_place = *reinterpret_cast<int*>(full_bar + 26);  // of that pair
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c = blockIdx.x;
@@ -253,11 +260,11 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV8>::kCtas)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // ---- this CTA's share: tiles [w0, w1) of the list
+  // ---- this CTA's share: places [w0, w1) of the list
   const int per = (n_items + kThreads - 1) / kThreads;
   const int i0 = imin(n_items, (int)threadIdx.x * per), i1 = imin(n_items, i0 + per);
   int mine = 0;
-  for (int i = i0; i < i1; ++i) mine += pair_of(a, i).n;
+  for (int i = i0; i < i1; ++i) mine += places(pair_of(a, i).n);
   int incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -272,15 +279,15 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV8>::kCtas)
     if (w < warp) before += warp_sum[w];
     W += warp_sum[w];
   }
-  // no share is empty: with fewer tiles than CTAs the last CTAs have none
+  // no share is empty: with fewer places than CTAs the last CTAs have none
   const int G = W < (int)gridDim.x ? W : (int)gridDim.x;
   const Shares sh{G ? W / G : 0, G ? W % G : 0};
   const int w0 = c < G ? sh.begin(c) : W, w1 = c < G ? sh.begin(c + 1) : W;
   if (w0 < w1 && before <= w0 && w0 < before + mine) {
     int p = before;
     for (int i = i0; i < i1; ++i) {
-      const int n = per == 1 ? mine : pair_of(a, i).n;
-      if (w0 < p + n) { first_item = i; first_off = w0 - p; break; }
+      const int n = per == 1 ? mine : places(pair_of(a, i).n);
+      if (w0 < p + n) { first_item = i; first_place = p; break; }
       p += n;
     }
   }
@@ -291,19 +298,26 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV8>::kCtas)
     // ------------------------------------------------------------------ producer
     if (w0 < w1 && pool_ok) {
       const int nbox = kTok / a.box_rows;
-      const int ntile = w1 - w0;
       Window win;
       win.fill(a, first_item, n_items);
-      int item = first_item, off = first_off;
+      int item = first_item, place = first_place;
       Pair s = win.get(a, item, n_items);
+      // this CTA's tiles of the pair at hand: [off, lim)
+      int off = imax(0, w0 - place - kSegment), lim = imin(s.n, w1 - place - kSegment);
       // Box `lane` of a tile: the page it lies in.  The load is unconditional, at a clamped place, and
       // what it gave is looked at when the tile's turn comes, two tiles later.
       struct Look {
         int base, lo, hi, g, slot, page;
         bool want;
       };
-      auto look = [&](Look& k) {
-        while (off >= s.n) { s = win.get(a, ++item, n_items); off = 0; }
+      auto look = [&](Look& k) -> bool {
+        while (off >= lim) {
+          place += places(s.n);
+          if (place >= w1) return false;
+          s = win.get(a, ++item, n_items);
+          off = 0;
+          lim = imin(s.n, w1 - place - kSegment);
+        }
         s.tile(off++, k.base, k.lo, k.hi);
         k.g = item - s.b * a.Hkv;
         const int p = k.base + (lane & (nbox - 1)) * a.box_rows;
@@ -311,6 +325,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV8>::kCtas)
         const int i = a.page_shift >= 0 ? p >> a.page_shift : p / a.tab.page_size;
         k.slot = p - i * a.tab.page_size;
         k.page = a.tab.ptr[s.b * a.tab.sb + k.g * a.tab.sh + imin(i, a.tab.max_pages - 1)];
+        return true;
       };
       int issued = 0;
       auto put = [&](const Look& k, int st) -> bool {
@@ -346,13 +361,12 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV8>::kCtas)
         return true;
       };
       Look even, odd;
-      look(even);
-      if (ntile > 1) look(odd);
-      for (int st = 0; st < ntile; st += 2) {  // by twos, so that nothing has to be moved between the two
+      bool more_even = look(even), more_odd = more_even && look(odd);
+      for (int st = 0; more_even; st += 2) {  // by twos, so that nothing has to be moved between the two
         if (!put(even, st)) break;
-        if (st + 2 < ntile) look(even);
-        if (st + 1 >= ntile || !put(odd, st + 1)) break;
-        if (st + 3 < ntile) look(odd);
+        more_even = more_odd && look(even);
+        if (!more_odd || !put(odd, st + 1)) break;
+        more_odd = more_even && look(odd);
       }
       // never leave the CTA with copies in flight
       for (int st = (issued > kStages ? issued - kStages : 0); st < issued; ++st)
@@ -396,16 +410,31 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV8>::kCtas)
     }
   };
   Counts counts;
-  int item = 0, off = 0, n = 0;  // n: tiles of the pair at hand, of which `off` are not this CTA's
+  // the pair at hand: its place, its tiles, and this CTA's share of them [off, lim)
+  int item = 0, place = 0, n = 0, off = 0, lim = 0;
+  auto step = [&]() -> bool {  // the next pair of which this CTA has tiles
+    do {
+      place += places(n);
+      if (place >= w1) return false;
+      n = counts.get(a, ++item, n_items);
+      off = 0;
+      lim = imin(n, w1 - place - kSegment);
+    } while (off >= lim);
+    return true;
+  };
+  bool more = false;
   if (w0 < w1) {
     item = first_item;
-    off = first_off;
-    load_q(item);
+    place = first_place;
     counts.fill(a, item, n_items);
     n = counts.get(a, item, n_items);
+    off = imax(0, w0 - place - kSegment);
+    lim = imin(n, w1 - place - kSegment);
+    more = off < lim || step();
+    if (more) load_q(item);
   }
-  for (int w = w0; w < w1;) {
-    const int take = imin(w1 - w, n - off), h0 = item * grp;
+  while (more) {
+    const int take = lim - off, h0 = item * grp;
     {
       uint32_t qf[KS][2];
 #pragma unroll
@@ -510,15 +539,10 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV8>::kCtas)
         }
       }
       // ---- the next segment's pair and query rows, while the warps are joined
-      const bool begins = off == 0, ends = off + take == n;
-      if (begins && !ends) rec = make_int4(item, sh.of(w + n - 1), 0, 0);  // the CTA that holds its last tile
-      w += take;
-      off = 0;
-      if (w < w1) {
-        do n = counts.get(a, ++item, n_items);
-        while (n == 0);
-        load_q(item);
-      }
+      const bool begins = off == 0, ends = lim == n;
+      if (begins && !ends) rec = make_int4(item, sh.of(place + kSegment + n - 1), 0, 0);  // the CTA with its last tile
+      more = step();
+      if (more) load_q(item);
       // ---- join the warps
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) {
@@ -647,7 +671,7 @@ int paged_decode_grid(const Pat& p, int B, int Hq, int Hkv, int d, bool kv8, int
   const int64_t cap = (int64_t)max_pages * page_size, R = (int64_t)p.T - p.S;
   const int64_t wide = R > 0 ? (R + p.H - 1) / p.H : 0;
   auto tiles = [&](int64_t n) { return n > 0 ? ((n < cap ? n : cap) + kTok - 1) / kTok + 1 : 0; };
-  const int64_t n = tiles(p.S) + tiles(wide) + tiles(p.L);
+  const int64_t n = tiles(p.S) + tiles(wide) + tiles(p.L) + kSegment;
   if (n > 0x7fffffff / ((int64_t)B * Hkv)) return 0;  // the kernels count tiles in 32 bits
   return (int)(n * B * Hkv < most ? n * B * Hkv : most);
 }
