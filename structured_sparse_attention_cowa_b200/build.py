@@ -5,7 +5,9 @@
 Compiles every csrc/*.cu to an object in _build/ and links them into
 structured_sparse_attention_cowa_b200/libcowa.so (static CUDA runtime; the
 driver API is reached through cudaGetDriverEntryPoint, so no -lcuda).
-Objects are rebuilt only when a source or header is newer.
+csrc/binding.cpp, the part of the Python binding that is compiled, becomes
+_binding.so beside it (against the installed torch; it finds either library's
+entry points at run time).  Objects are rebuilt only when a source or header is newer.
 
 --debug builds libcowa_debug.so with COWA_DEBUG=1: the kernels check every planned tile and
 cache row against the call's tensors before loading it, and a failed check is reported as
@@ -27,6 +29,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libcowa.so")
 LIB_DEBUG = os.path.join(PKG, "libcowa_debug.so")
+BINDING = os.path.join(PKG, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O3", "--expt-relaxed-constexpr",
@@ -44,6 +47,31 @@ def _newest_header() -> float:
     hdrs = glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + \
         glob.glob(os.path.join(ROOT, "include", "*.h"))
     return max((os.path.getmtime(h) for h in hdrs), default=0.0)
+
+
+def build_binding(verbose: bool = False) -> str:
+    """Compile csrc/binding.cpp against the installed torch into _binding.so, if it is out of date."""
+    src = os.path.join(CSRC, "binding.cpp")
+    hdr = os.path.join(ROOT, "include", "cowa.h")
+    if os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(os.path.getmtime(src), os.path.getmtime(hdr)):
+        return BINDING
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension as ext
+
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))) if os.path.isabs(_nvcc()) else "/usr/local/cuda"
+    inc = [*ext.include_paths(), os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *("-isystem" + i for i in inc), src, "-o", BINDING, *("-L" + p for p in ext.library_paths()), "-lc10",
+           "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError("g++ failed on binding.cpp")
+    return BINDING
 
 
 def build(debug: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
@@ -81,6 +109,7 @@ def build(debug: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             sys.stderr.write(r.stdout + r.stderr)
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed on {os.path.basename(src)}")
+    build_binding(verbose)
     out = LIB_DEBUG if debug else LIB
     lib_t = os.path.getmtime(out) if os.path.exists(out) else -1
     if lib_t < max(os.path.getmtime(o) for o in objs):

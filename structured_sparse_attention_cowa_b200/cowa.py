@@ -3,8 +3,8 @@
 Every step of the computation runs in the library's CUDA kernels; this module
 turns torch tensors into the C ABI's pointers and strides, allocates the
 caller-owned outputs and workspace with torch, and raises on any non-OK
-status.  There is no fallback: if libcowa.so is missing or fails to load,
-every call raises.
+status.  There is no fallback: if libcowa.so (or, for the calls of a serving step, the compiled
+part of the binding, _binding.so) is missing or fails to load, every call raises.
 
 Calls are asynchronous on the stream, as in the C ABI.  A kernel whose bounded wait
 runs out records COWA_ERR_TIMEOUT in its workspace's status word instead of hanging;
@@ -22,7 +22,6 @@ paged_append_fp8, cowa_decode_paged_fp8, cowa_fwd_paged and pages_needed), plus 
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import dataclasses
 import os
@@ -615,79 +614,34 @@ def cowa_decode_fp8_compact(q_t, kc, vc, pos, pattern: Pattern, k_scale: float, 
 
 
 # ---------------------------------------------------------------------------- rotary positions, paged cache
-# A step of one token makes these calls in a few microseconds of GPU time, so their checks are kept
-# short: one comparison per property, device indices instead of device objects.
-def _device_of(x, *others) -> int:
-    """Index of x's CUDA device, which must be that of the others (None: not given) too."""
-    dev = x.get_device()
-    for y in others:
-        if y is not None and y.get_device() != dev:
-            raise ValueError(f"tensors are on different devices: {x.device} and {y.device}")
-    return dev
+# These calls belong to a serving step, of which there are several per layer and microseconds each, so
+# their arguments are checked and packed by compiled code (csrc/binding.cpp).
+_binding = None
+_binding_of = None
 
 
-def _launch_on(dev: int, stream):
-    """Context in which device `dev` is current and allocations and launches go to `stream` (the
-    device's current stream if None): what a call allocates then belongs to the stream that uses it."""
+def _native():
+    """The compiled part of this binding, calling the library that lib() has loaded."""
+    global _binding, _binding_of
+    L = lib()
+    if _binding_of is not L:
+        import torch  # noqa: F401  (the extension needs its libraries)
+
+        from . import _binding as b
+
+        b.use(L._handle)
+        _binding, _binding_of = b, L
+    return _binding
+
+
+def _on(x, stream):
+    """Context in which allocations and launches go to `stream`, which must be on x's device: what a call
+    allocates then belongs to the stream that uses it."""
     import torch
 
-    if stream is not None:
-        if stream.device.index != dev:
-            raise ValueError("stream and tensors are on different devices")
-        return torch.cuda.stream(stream)
-    if torch.cuda.current_device() != dev:
-        return torch.cuda.device(dev)
-    return _HERE_ALREADY
-
-
-_HERE_ALREADY = contextlib.nullcontext()
-_raw_stream = None
-
-
-def _stream_of(dev: int) -> int:
-    """Handle of device dev's current stream."""
-    global _raw_stream
-    if _raw_stream is None:
-        import torch
-
-        # torch's own accessor of the handle, without a Stream object (20 times cheaper) where it has one
-        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
-                              lambda d: torch.cuda.current_stream(d).cuda_stream)
-    return _raw_stream(dev)
-
-
-def _int32(name, x, shape):
-    import torch
-
-    if x.dtype is not torch.int32 or not x.is_cuda:
-        raise TypeError(f"{name} must be a CUDA int32 tensor")
-    if x.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(x.shape)}, expected {shape}")
-    if x.stride(-1) != 1 and shape[-1] > 1:
-        raise ValueError(f"{name} must be contiguous along its last dimension")
-    return x.data_ptr()
-
-
-def _bf16(name, x, shape):
-    import torch
-
-    if x.dtype is not torch.bfloat16 or not x.is_cuda:
-        raise TypeError(f"{name} must be a CUDA bfloat16 tensor")
-    if x.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(x.shape)}, expected {shape}")
-
-
-def _rows(name, x) -> c_tensor:
-    """[B, N, H, d] or packed [total, H, d] tensor (d contiguous) -> cowa_tensor."""
-    s = x.stride()
-    if s[-1] != 1:
-        raise ValueError(f"the last dimension of {name} must be contiguous")
-    if len(s) == 3:
-        return c_tensor(x.data_ptr(), s[0] * max(1, x.shape[0]), s[0], s[1])
-    return c_tensor(x.data_ptr(), s[0], s[1], s[2])
-
-
-_NO_TENSOR = c_tensor(None, 0, 0, 0)
+    if stream.device != x.device:
+        raise ValueError("stream and tensors are on different devices")
+    return torch.cuda.stream(stream)
 
 
 def rope_frequencies(rotary_dim: int, base: float = 10000.0, device="cuda"):
@@ -701,7 +655,7 @@ class Rope:
     """Rotary positions of a layer (cowa_rotary in include/cowa.h): inv_freq, a CUDA float32 tensor of
     rotary_dim / 2 frequencies; `sections`, how many pairs turn with each position axis (1 to 4 axes,
     adding up to rotary_dim / 2; default one axis); `interleaved`, pairs (2i, 2i+1) instead of
-    (i, i + rotary_dim/2); `scale`, a factor of cos and sin."""
+    (i, i + rotary_dim/2); `scale`, a factor of cos and sin (0 means 1)."""
 
     def __init__(self, inv_freq, sections=(), interleaved: bool = False, scale: float = 1.0):
         import torch
@@ -713,59 +667,37 @@ class Rope:
         if len(sections) > 4 or min(sections) < 0 or sum(sections) != inv_freq.numel():
             raise ValueError("sections: 1 to 4 counts of pairs that add up to the number of frequencies")
         self.inv_freq, self.sections, self.n_axes = inv_freq, sections, len(sections)
+        self.interleaved, self.scale = bool(interleaved), float(scale)
         self._c = c_rotary(inv_freq.data_ptr(), 2 * inv_freq.numel(), len(sections),
-                           (ctypes.c_int32 * 4)(*sections), int(bool(interleaved)), float(scale))
+                           (ctypes.c_int32 * 4)(*sections), int(self.interleaved), self.scale)
+        self._address = ctypes.addressof(self._c)
 
     def c(self) -> c_rotary:
         return self._c
 
+    def __reduce__(self):  # (the C structure holds addresses of this process)
+        return Rope, (self.inv_freq, self.sections, self.interleaved, self.scale)
 
-def _rope(fn, q, k, rope, positions, q_out, k_out, stream):
-    import torch
 
-    x = q if q is not None else k
-    if x is None:
-        raise ValueError("q or k is needed")
-    if x.dim() != 4:
-        raise ValueError("q and k are [B, N, H, d]")
-    B, N, _, d = x.shape
-    heads = [0, 0]
-    for i, (name, y, y_out) in enumerate((("q", q, q_out), ("k", k, k_out))):
-        if y is not None:
-            heads[i] = y.shape[2] if y.dim() == 4 else -1
-            _bf16(name, y, (B, N, heads[i], d))
-            if y_out is not None:
-                _bf16(name + "_out", y_out, y.shape)
-        elif y_out is not None:
-            raise ValueError(f"{name}_out without {name}")
-    dev = _device_of(x, k, positions, q_out, k_out, rope.inv_freq)
-    pos, sa, sb = None, 0, 0
-    if positions is not None:
-        if positions.dim() == 2 and rope.n_axes == 1:
-            pos, sb = _int32("positions", positions, (B, N)), positions.stride(0)
-        else:
-            pos = _int32("positions", positions, (rope.n_axes, B, N))
-            sa, sb, _ = positions.stride()
-    with _launch_on(dev, stream):
-        if q is not None and q_out is None:
-            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        if k is not None and k_out is None:
-            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
-        t = lambda name, y: _NO_TENSOR if y is None else _rows(name, y)
-        _check(fn, getattr(lib(), fn)(ctypes.byref(rope._c), B, N, *heads, d, t("q", q), t("k", k), t("q_out", q_out),
-                                      t("k_out", k_out), pos, sa, sb, _stream_of(dev)))
+def _rope(bwd, q, k, rope, positions, q_out, k_out, stream):
+    if stream is not None:
+        with _on(q if q is not None else k, stream):
+            return _rope(bwd, q, k, rope, positions, q_out, k_out, None)
+    status, q_out, k_out = _native().rope(bwd, q, k, rope._address, rope.inv_freq, positions, q_out, k_out)
+    if status:
+        _check("cowa_rope_bwd" if bwd else "cowa_rope", status)
     return q_out, k_out
 
 
 def cowa_rope(q, k, rope: Rope, positions=None, q_out=None, k_out=None, stream=None):
     """Rotated (q, k), both [B, N, H, d] bf16 (either may be None): positions CUDA int32 [n_axes, B, N]
     ([B, N] for one axis; default: t).  q_out, k_out may be q, k."""
-    return _rope("cowa_rope", q, k, rope, positions, q_out, k_out, stream)
+    return _rope(False, q, k, rope, positions, q_out, k_out, stream)
 
 
 def cowa_rope_bwd(dq, dk, rope: Rope, positions=None, dq_out=None, dk_out=None, stream=None):
     """Gradients of q and k from those of the rotated q and k (the transpose of cowa_rope)."""
-    return _rope("cowa_rope_bwd", dq, dk, rope, positions, dq_out, dk_out, stream)
+    return _rope(True, dq, dk, rope, positions, dq_out, dk_out, stream)
 
 
 def pages_needed(pattern: Pattern, h_kv: int, page_size: int, n_pages: int, pos: int) -> np.ndarray:
@@ -777,71 +709,16 @@ def pages_needed(pattern: Pattern, h_kv: int, page_size: int, n_pages: int, pos:
     return out.astype(bool)
 
 
-def _pages(k_pages, v_pages, page_table, layout, d, h_kv=None):
-    """(H_kv, k and v as cowa_tensor, cowa_page_table) of pools [n_pages, page_size, H, d] ("bthd") or
-    [n_pages, H, page_size, d] ("bhtd"), H = H_kv or, with a table [n_seq, H_kv, max_pages], 1."""
-    import torch
-
-    if layout == "bthd":
-        t, h = 1, 2
-    elif layout == "bhtd":
-        t, h = 2, 1
-    else:
-        raise ValueError("layout must be 'bhtd' or 'bthd'")
-    if page_table.dtype is not torch.int32 or not page_table.is_cuda:
-        raise TypeError("page_table must be a CUDA int32 tensor")
-    ts, shape, dims = page_table.stride(), k_pages.shape, page_table.dim()
-    if not 2 <= dims <= 3 or (ts[-1] != 1 and page_table.shape[-1] > 1):
-        raise ValueError("page_table is [n_seq, max_pages] or [n_seq, H_kv, max_pages], contiguous along the last dimension")
-    if len(shape) != 4 or shape != v_pages.shape or shape[3] != d:
-        raise ValueError("k_pages and v_pages must be 4-D pools of the same shape and head dimension")
-    heads = page_table.shape[1] if dims == 3 else shape[h]
-    if (h_kv is not None and heads != h_kv) or (dims == 3 and shape[h] != 1):
-        raise ValueError("the pools hold all KV heads, or one, if the table has entries for each")
-    ks, vs = k_pages.stride(), v_pages.stride()
-    if ks[3] != 1 or vs[3] != 1:
-        raise ValueError("the last dimension of the pools must be contiguous")
-    return (heads, c_tensor(k_pages.data_ptr(), ks[0], ks[t], ks[h]), c_tensor(v_pages.data_ptr(), vs[0], vs[t], vs[h]),
-            c_page_table(page_table.data_ptr(), ts[0], ts[1] if dims == 3 else 0, page_table.shape[-1], shape[t],
-                         shape[0], dims == 3))
-
-
-def _paged_append(fn, q, k, v, pos, k_pages, v_pages, page_table, rope, seq, rope_pos, q_out, layout, scales, stream):
-    import torch
-
-    if k.dim() != 3 or (q is not None and q.dim() != 3):
-        raise ValueError("q is [total, H_q, d], k and v are [total, H_kv, d]")
-    total, Hkv, d = shape = k.shape
-    _bf16("k", k, shape)
-    _bf16("v", v, shape)
-    Hq = 0
-    if q is not None:
-        Hq = q.shape[1]
-        _bf16("q", q, (total, Hq, d))
-        if q_out is not None:
-            _bf16("q_out", q_out, q.shape)
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    pos_p, seq_p, rp, rs = _int32("pos", pos, (total,)), None, None, 0
-    if seq is not None:
-        seq_p = _int32("seq", seq, (total,))
-    if rope_pos is not None:
-        if rope is None:
-            raise ValueError("rope_pos without rope")
-        if rope_pos.dim() == 1 and rope.n_axes == 1:
-            rp = _int32("rope_pos", rope_pos, (total,))
-        else:
-            rp, rs = _int32("rope_pos", rope_pos, (rope.n_axes, total)), rope_pos.stride(0)
-    _, kp, vp, tab = _pages(k_pages, v_pages, page_table, layout, d, Hkv)
-    dev = _device_of(k, q, v, pos, seq, rope_pos, q_out, k_pages, v_pages, page_table,
-                     None if rope is None else rope.inv_freq)
-    with _launch_on(dev, stream):
-        if q is not None and q_out is None:
-            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        _check(fn, getattr(lib(), fn)(None if rope is None else ctypes.byref(rope._c), total, page_table.shape[0], Hq, Hkv,
-                                      d, _NO_TENSOR if q is None else _rows("q", q), _rows("k", k), _rows("v", v),
-                                      _NO_TENSOR if q is None else _rows("q_out", q_out), pos_p, seq_p, rp, rs, kp, vp,
-                                      *scales, tab, _stream_of(dev)))
+def _paged_append(q, k, v, pos, k_pages, v_pages, page_table, rope, seq, rope_pos, q_out, layout, scales, stream):
+    if stream is not None:
+        with _on(k, stream):
+            return _paged_append(q, k, v, pos, k_pages, v_pages, page_table, rope, seq, rope_pos, q_out, layout,
+                                 scales, None)
+    address, freq = (None, None) if rope is None else (rope._address, rope.inv_freq)
+    status, q_out = _native().append(q, k, v, pos, k_pages, v_pages, page_table, address, freq, seq, rope_pos, q_out,
+                                     layout, scales)
+    if status:
+        _check("cowa_paged_append" if scales is None else "cowa_paged_append_fp8", status)
     return q_out
 
 
@@ -855,60 +732,26 @@ def paged_append(q, k, v, pos, k_pages, v_pages, page_table, rope: Rope = None, 
     ("bhtd") with page_table [n_seq, max_pages], or one head per page (H_kv replaced by 1) with
     page_table [n_seq, H_kv, max_pages].  Rows with pos < 0 are left out (q_out too); keys and values
     without a page are dropped."""
-    for n_, x_ in (("k_pages", k_pages), ("v_pages", v_pages)):
-        _bf16_cuda(n_, x_)
-    return _paged_append("cowa_paged_append", q, k, v, pos, k_pages, v_pages, page_table, rope, seq, rope_pos, q_out,
-                         layout, (), stream)
+    return _paged_append(q, k, v, pos, k_pages, v_pages, page_table, rope, seq, rope_pos, q_out, layout, None, stream)
 
 
 def paged_append_fp8(q, k, v, pos, k_pages, v_pages, page_table, k_scale: float, v_scale: float, rope: Rope = None,
                      seq=None, rope_pos=None, q_out=None, layout: str = "bthd", stream=None):
     """paged_append into pages of E4M3 codes (uint8, d = 128), quantised as by quantize_e4m3."""
-    _u8_cuda("k_pages", k_pages)
-    _u8_cuda("v_pages", v_pages)
-    return _paged_append("cowa_paged_append_fp8", q, k, v, pos, k_pages, v_pages, page_table, rope, seq, rope_pos,
-                         q_out, layout, (float(k_scale), float(v_scale)), stream)
+    return _paged_append(q, k, v, pos, k_pages, v_pages, page_table, rope, seq, rope_pos, q_out, layout,
+                         (float(k_scale), float(v_scale)), stream)
 
 
-def _lse(lse, shape):
-    import torch
-
-    if lse.dtype is not torch.float32 or lse.shape != shape or not lse.is_contiguous():
-        raise ValueError(f"lse must be a contiguous float32 tensor of shape {shape}")
-
-
-def _decode_paged(fn, q_t, k_pages, v_pages, page_table, pos, pattern, scales, layout, out, lse, workspace, stream,
+def _decode_paged(q_t, k_pages, v_pages, page_table, pos, pattern, scales, layout, out, lse, workspace, stream,
                   want_lse):
-    import torch
-
-    B, Hq, d = shape = q_t.shape
-    _bf16("q_t", q_t, shape)
-    if not q_t.is_contiguous():
-        raise ValueError("q_t must be contiguous [B, H_q, d]")
-    Hkv, kp, vp, tab = _pages(k_pages, v_pages, page_table, layout, d)
-    pos_p = _int32("pos", pos, (B,))
-    if page_table.shape[0] != B:
-        raise ValueError(f"page_table has {page_table.shape[0]} sequences, expected {B}")
-    if out is not None:
-        _bf16("out", out, shape)
-        if not out.is_contiguous():
-            raise ValueError("out must be contiguous [B, H_q, d]")
-    if lse is not None:
-        _lse(lse, (B, Hq))
-    dev = _device_of(q_t, k_pages, v_pages, page_table, pos, out, lse, workspace)
-    pat = ctypes.byref(pattern.c())
-    L = lib()
-    with _launch_on(dev, stream):
-        if out is None:
-            out = torch.empty_like(q_t)
-        if lse is None and want_lse:
-            lse = torch.empty((B, Hq), dtype=torch.float32, device=q_t.device)
-        if workspace is None:
-            workspace = _workspace(getattr(L, fn + "_workspace_size")(pat, B, Hq, Hkv, d, tab.max_pages, tab.page_size),
-                                   q_t.device)
-        _check(fn, getattr(L, fn)(pat, B, Hq, Hkv, d, q_t.data_ptr(), kp, vp, *scales, tab, pos_p, out.data_ptr(),
-                                  lse.data_ptr() if lse is not None else None, workspace.data_ptr(), workspace.nbytes,
-                                  _stream_of(dev)))
+    if stream is not None:
+        with _on(q_t, stream):
+            return _decode_paged(q_t, k_pages, v_pages, page_table, pos, pattern, scales, layout, out, lse, workspace,
+                                 None, want_lse)
+    status, out, lse = _native().decode(q_t, k_pages, v_pages, page_table, pos, pattern, scales, layout, out, lse,
+                                        workspace, want_lse)
+    if status:
+        _check("cowa_decode_paged" if scales is None else "cowa_decode_paged_fp8", status)
     return out, lse
 
 
@@ -916,10 +759,8 @@ def cowa_decode_paged(q_t, k_pages, v_pages, page_table, pos, pattern: Pattern, 
                       lse=None, workspace=None, stream=None, want_lse: bool = True):
     """o [B, H_q, d] bf16 (and lse [B, H_q] fp32) for one new token per sequence at pos[b] over a paged
     cache (pools and page_table as for paged_append).  pos[b] < 0: no sequence, o = 0 and lse = -inf."""
-    for n_, x_ in (("k_pages", k_pages), ("v_pages", v_pages)):
-        _bf16_cuda(n_, x_)
-    return _decode_paged("cowa_decode_paged", q_t, k_pages, v_pages, page_table, pos, pattern, (), layout, out, lse,
-                         workspace, stream, want_lse)
+    return _decode_paged(q_t, k_pages, v_pages, page_table, pos, pattern, None, layout, out, lse, workspace, stream,
+                         want_lse)
 
 
 def cowa_decode_paged_fp8(q_t, k_pages, v_pages, page_table, pos, pattern: Pattern, k_scale: float, v_scale: float,
@@ -927,10 +768,8 @@ def cowa_decode_paged_fp8(q_t, k_pages, v_pages, page_table, pos, pattern: Patte
                           want_lse: bool = True):
     """cowa_decode_paged over pages of E4M3 codes (uint8, d = 128): keys k_scale * e4m3(code), values
     v_scale * e4m3(code)."""
-    _u8_cuda("k_pages", k_pages)
-    _u8_cuda("v_pages", v_pages)
-    return _decode_paged("cowa_decode_paged_fp8", q_t, k_pages, v_pages, page_table, pos, pattern,
-                         (float(k_scale), float(v_scale)), layout, out, lse, workspace, stream, want_lse)
+    return _decode_paged(q_t, k_pages, v_pages, page_table, pos, pattern, (float(k_scale), float(v_scale)), layout,
+                         out, lse, workspace, stream, want_lse)
 
 
 def cowa_fwd_paged(q, k_pages, v_pages, page_table, cu_seqlens, q_start, pattern: Pattern, layout: str = "bthd",
@@ -939,32 +778,14 @@ def cowa_fwd_paged(q, k_pages, v_pages, page_table, cu_seqlens, q_start, pattern
     cu_seqlens CUDA int32 [n_seq + 1], q_start CUDA int32 [n_seq] the position of each chunk's first row;
     pools and page_table as for paged_append (bf16).  Returns o [total, H_q, d] bf16 and lse [H_q, total]
     fp32."""
-    import torch
-
-    for n_, x_ in (("k_pages", k_pages), ("v_pages", v_pages)):
-        _bf16_cuda(n_, x_)
-    total, Hq, d = shape = q.shape
-    _bf16("q", q, shape)
-    Hkv, kp, vp, tab = _pages(k_pages, v_pages, page_table, layout, d)
-    n_seq = page_table.shape[0]
-    cu_p, start_p = _int32("cu_seqlens", cu_seqlens, (n_seq + 1,)), _int32("q_start", q_start, (n_seq,))
-    if out is not None:
-        _bf16("out", out, shape)
-    if lse is not None:
-        _lse(lse, (Hq, total))
-    dev = _device_of(q, k_pages, v_pages, page_table, cu_seqlens, q_start, out, lse, workspace)
-    pat = ctypes.byref(pattern.c())
-    L = lib()
-    with _launch_on(dev, stream):
-        if out is None:
-            out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        if lse is None:
-            lse = torch.empty((Hq, total), dtype=torch.float32, device=q.device)
-        if workspace is None:
-            workspace = _workspace(L.cowa_fwd_paged_workspace_size(pat, n_seq, total, Hq, Hkv, d), q.device)
-        _check("cowa_fwd_paged", L.cowa_fwd_paged(pat, n_seq, total, Hq, Hkv, d, cu_p, start_p, _rows("q", q), kp, vp, tab,
-                                                  _rows("out", out), lse.data_ptr(), workspace.data_ptr(),
-                                                  workspace.nbytes, _stream_of(dev)))
+    if stream is not None:
+        with _on(q, stream):
+            return cowa_fwd_paged(q, k_pages, v_pages, page_table, cu_seqlens, q_start, pattern, layout, out, lse,
+                                  workspace)
+    status, out, lse = _native().fwd(q, k_pages, v_pages, page_table, cu_seqlens, q_start, pattern, layout, out, lse,
+                                     workspace)
+    if status:
+        _check("cowa_fwd_paged", status)
     return out, lse
 
 

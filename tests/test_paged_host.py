@@ -147,7 +147,8 @@ def test_binding_refuses_cpu_tensors_and_wrong_types():
     with pytest.raises(TypeError):
         cw.Rope(torch.ones(32))
     fake = object.__new__(cw.Rope)
-    fake.inv_freq, fake.sections, fake.n_axes = torch.ones(32), (32,), 1
+    fake.inv_freq, fake._c = torch.ones(32), rotary(r=64)
+    fake._address = ctypes.addressof(fake._c)
     with pytest.raises(TypeError):
         cw.cowa_rope(q, None, fake)
     with pytest.raises(ValueError):
