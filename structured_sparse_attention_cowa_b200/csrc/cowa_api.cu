@@ -789,7 +789,7 @@ size_t paged_workspace(const cowa_pattern* pat, int B, int Hq, int Hkv, int d, b
   if (check_pattern(pat, Hkv, &p) != COWA_OK || check_heads(B, 1, Hq, Hkv, d) != COWA_OK || (e4m3 && d != 128) ||
       max_pages < 1 || page_size < 8 || page_size % 8 != 0 || (int64_t)max_pages * page_size > (1 << 30))
     return 0;
-  const int grid = paged_decode_grid(p, B, Hq, Hkv, d, e4m3, max_pages, page_size);
+  const int grid = paged_decode_plan(p, B, Hq, Hkv, d, e4m3, max_pages, page_size).grid;
   return grid > 0 ? kWsHeader + paged_decode_bytes(grid, Hq / Hkv, d) : 0;
 }
 
@@ -811,7 +811,8 @@ cowa_status decode_paged(const cowa_pattern* pat, int B, int Hq, int Hkv, int d,
   if (!aligned16(q_t) || !aligned16(o) || (reinterpret_cast<uintptr_t>(pos) & 3u) ||
       (reinterpret_cast<uintptr_t>(lse) & 3u))
     return COWA_ERR_ALIGNMENT;
-  a.grid = paged_decode_grid(p, B, Hq, Hkv, d, e4m3, table.max_pages, table.page_size);
+  const PagedPlan plan = paged_decode_plan(p, B, Hq, Hkv, d, e4m3, table.max_pages, table.page_size);
+  a.grid = plan.grid; a.cluster = plan.cluster;
   if (a.grid == 0 || (int64_t)B * Hq > 0x7fffffff) return COWA_ERR_UNSUPPORTED;
   COWA_TRY(check_ws(ws, ws_bytes, kWsHeader + paged_decode_bytes(a.grid, Hq / Hkv, d)));
   a.pat = p; a.B = B; a.Hkv = Hkv; a.grp = Hq / Hkv;

@@ -88,12 +88,15 @@ struct PagedDecodeArgs {
   int4* rec;         // [grid]: {pair, last CTA} of the (b, g) that begins in CTA c and does not end there; x = -1: none
   float* part;       // [2 grid][grp][d + 2] fp32 partials: m, l, o
   float scale_log2, v_scale;
-  int grid;
+  int grid, cluster; // see paged_decode_plan
   int box_rows;      // rows per TMA box: the largest power of two up to 64 that divides the page size
   int page_shift;    // log2 of the page size, -1 if it is not a power of two
   CUtensorMap tm_k, tm_v;
 };
-int paged_decode_grid(const Pat& p, int B, int Hq, int Hkv, int d, bool kv8, int max_pages, int page_size);
+struct PagedPlan {
+  int grid, cluster;
+};
+PagedPlan paged_decode_plan(const Pat& p, int B, int Hq, int Hkv, int d, bool kv8, int max_pages, int page_size);
 size_t paged_decode_bytes(int grid, int grp, int d);
 cudaError_t launch_paged_decode(const PagedDecodeArgs& a, int d, bool kv8, cudaStream_t s);
 

@@ -11,6 +11,9 @@
 //     the tile counts itself (integer arithmetic on pos) and takes an equal, contiguous share of the
 //     list, in which every pair counts kSegment tiles more than it has.  A pair that lies inside one CTA's share is finished there; one that several CTAs share
 //     leaves fp32 partials (at most two per CTA), which a second kernel joins in order.
+//   * Where no CTA gets more than a few tiles anyway (one user, short caches), latency counts instead:
+//     a cluster of CTAs takes one pair, shares its tiles out evenly and joins its results through
+//     distributed shared memory, so there is no list to add up and no second kernel.
 //   * A producer warp looks up the pages (one lane per box of 8 to 64 rows, two tiles ahead of the
 //     copies) and streams K and V tiles into a shared-memory ring with TMA; boxes that hold no
 //     visible key are not fetched.
@@ -42,6 +45,8 @@ constexpr float kRescale = 8.0f;               // lazy-rescale threshold, log2 u
 // tiles: 37 sequences of 1 to 32K positions, E4M3, took 2.0 us a segment and 1.0 us a tile, and the CTAs
 // that held nine segments of one tile each twice as long as the others.
 constexpr int kSegment = 2;
+// Up to how many tiles a CTA may have for the cluster form.
+constexpr int kClusterTiles = 8;
 // E4M3: P is rounded to f16, whose smallest normal number is 2^-14; relative to a running maximum
 // lifted by 2^6 (P at most 2^14) it covers P down to 2^-20 of the largest at full precision.
 template <bool KV8>
@@ -226,7 +231,20 @@ struct Shares {
 
 __device__ __forceinline__ int places(int n) { return n > 0 ? n + kSegment : 0; }
 
-template <int D, bool KV8>
+// ---- thread-block cluster: barriers of all its threads, and the other CTAs' shared memory
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float cluster_ld(const float* own, int rank) {  // the word at the same place in CTA `rank`
+  uint32_t addr;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(ptx::smem_u32(own)), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// CL: CTAs c, c + 1, .. of a cluster of a.cluster share one pair; else every CTA has its share of the list.
+template <int D, bool KV8, bool CL>
 __global__ void __launch_bounds__(kThreads, Geo<D, KV8>::kCtas)
     paged_split_kernel(const __grid_constant__ PagedDecodeArgs a) {
   using G_ = Geo<D, KV8>;
@@ -238,8 +256,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV8>::kCtas)
   volatile uint64_t* seen = empty_bar + kStages;  // per stage: the tile's visible positions
   int* warp_sum = reinterpret_cast<int*>(full_bar + 16);  // [5]
   volatile int& abort_flag = *reinterpret_cast<volatile int*>(full_bar + 24);
-  int& first_item = *reinterpret_cast<int*>(full_bar + 25);
-  int& first_place = *reinterpret_cast<int*>(full_bar + 26);  // of that pair
+  int* first_of = reinterpret_cast<int*>(full_bar + 25);  // [2]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c = blockIdx.x;
@@ -260,38 +277,53 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV8>::kCtas)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // ---- this CTA's share: places [w0, w1) of the list
-  const int per = (n_items + kThreads - 1) / kThreads;
-  const int i0 = imin(n_items, (int)threadIdx.x * per), i1 = imin(n_items, i0 + per);
-  int mine = 0;
-  for (int i = i0; i < i1; ++i) mine += places(pair_of(a, i).n);
-  int incl = mine;
+  // ---- this CTA's share: places [w0, w1) of the list, the first pair of it and that pair's place
+  int w0, w1, first_item, first_place;
+  Shares sh{0, 0};
+  if constexpr (CL) {
+    first_item = c / a.cluster;
+    const int rank = c - first_item * a.cluster, n = pair_of(a, first_item).n;
+    // (in 64 bits: a pair may have 2^24 tiles)
+    w0 = (int)((int64_t)n * rank / a.cluster);
+    w1 = (int)((int64_t)n * (rank + 1) / a.cluster);
+    first_place = -kSegment;  // place w is tile w
+    __syncthreads();
+  } else {
+    const int per = (n_items + kThreads - 1) / kThreads;
+    const int i0 = imin(n_items, (int)threadIdx.x * per), i1 = imin(n_items, i0 + per);
+    int mine = 0;
+    for (int i = i0; i < i1; ++i) mine += places(pair_of(a, i).n);
+    int incl = mine;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
-  }
-  if (lane == 31) warp_sum[warp] = incl;
-  __syncthreads();
-  int before = incl - mine, W = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before += warp_sum[w];
-    W += warp_sum[w];
-  }
-  // no share is empty: with fewer places than CTAs the last CTAs have none
-  const int G = W < (int)gridDim.x ? W : (int)gridDim.x;
-  const Shares sh{G ? W / G : 0, G ? W % G : 0};
-  const int w0 = c < G ? sh.begin(c) : W, w1 = c < G ? sh.begin(c + 1) : W;
-  if (w0 < w1 && before <= w0 && w0 < before + mine) {
-    int p = before;
-    for (int i = i0; i < i1; ++i) {
-      const int n = per == 1 ? mine : places(pair_of(a, i).n);
-      if (w0 < p + n) { first_item = i; first_place = p; break; }
-      p += n;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
     }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    int before = incl - mine, W = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += warp_sum[w];
+      W += warp_sum[w];
+    }
+    // no share is empty: with fewer places than CTAs the last CTAs have none
+    const int G = W < (int)gridDim.x ? W : (int)gridDim.x;
+    sh = Shares{G ? W / G : 0, G ? W % G : 0};
+    w0 = c < G ? sh.begin(c) : W;
+    w1 = c < G ? sh.begin(c + 1) : W;
+    if (w0 < w1 && before <= w0 && w0 < before + mine) {
+      int p = before;
+      for (int i = i0; i < i1; ++i) {
+        const int n = per == 1 ? mine : places(pair_of(a, i).n);
+        if (w0 < p + n) { first_of[0] = i; first_of[1] = p; break; }
+        p += n;
+      }
+    }
+    __syncthreads();
+    first_item = first_of[0];
+    first_place = first_of[1];
   }
-  __syncthreads();
   const bool pool_ok = (ptx::smem_u32(smem) & 1023u) == 0;  // the swizzle pattern assumes it
 
   if (warp == kWarps) {
@@ -372,6 +404,11 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV8>::kCtas)
       for (int st = (issued > kStages ? issued - kStages : 0); st < issued; ++st)
         ptx::mbar_wait(&full_bar[st % kStages], (st / kStages) & 1, nullptr, a.status);
     }
+    if constexpr (CL) {
+      __syncwarp();
+      cluster_sync();
+      cluster_sync();
+    }
     return;
   }
 
@@ -385,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV8>::kCtas)
   if (!pool_ok && threadIdx.x == 0) atomicOr(a.status, (uint32_t)ptx::kStatusCheck);
 
   // slots without a sequence see nothing: zeros and -inf, by one CTA each
-  for (int i = c; i < a.B; i += gridDim.x) {
+  for (int i = c; !CL && i < a.B; i += gridDim.x) {
     if (a.pos[i] >= 0) continue;
     const size_t h0 = (size_t)i * a.Hkv * grp;
     for (int x = threadIdx.x; x < a.Hkv * grp * (D / 8); x += kWarps * 32)
@@ -430,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV8>::kCtas)
     n = counts.get(a, item, n_items);
     off = imax(0, w0 - place - kSegment);
     lim = imin(n, w1 - place - kSegment);
-    more = off < lim || step();
+    more = off < lim || (!CL && step());
     if (more) load_q(item);
   }
   while (more) {
@@ -540,8 +577,8 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV8>::kCtas)
       }
       // ---- the next segment's pair and query rows, while the warps are joined
       const bool begins = off == 0, ends = lim == n;
-      if (begins && !ends) rec = make_int4(item, sh.of(place + kSegment + n - 1), 0, 0);  // the CTA with its last tile
-      more = step();
+      if (!CL && begins && !ends) rec = make_int4(item, sh.of(place + kSegment + n - 1), 0, 0);  // the CTA with its last tile
+      more = !CL && step();
       if (more) load_q(item);
       // ---- join the warps
 #pragma unroll
@@ -566,7 +603,8 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV8>::kCtas)
       }
       asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
       if (ok && !abort_flag) {
-        float* part = a.part + ((size_t)2 * c + (begins ? 1 : 0)) * grp * (D + 2);
+        float* part = CL ? reinterpret_cast<float*>(smem)  // (the ring is drained)
+                         : a.part + ((size_t)2 * c + (begins ? 1 : 0)) * grp * (D + 2);
         for (int x = threadIdx.x; x < grp * D; x += kWarps * 32) {
           const int hd = x / D, d = x - hd * D;
           float m = -INFINITY;
@@ -581,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV8>::kCtas)
             l += f * r[1];
           }
           if (KV8) o *= a.v_scale;
-          if (begins && ends) {  // the pair is finished here
+          if (!CL && begins && ends) {  // the pair is finished here
             reinterpret_cast<__nv_bfloat16*>(a.o)[(size_t)(h0 + hd) * D + d] = __float2bfloat16_rn(m == -INFINITY ? 0.f : o / l);
             if (a.lse && d == 0) a.lse[h0 + hd] = m == -INFINITY ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
           } else {
@@ -592,7 +630,39 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV8>::kCtas)
       }
     }
   }
-  if (threadIdx.x == 0) a.rec[c] = rec;
+  if constexpr (!CL) {
+    if (threadIdx.x == 0) a.rec[c] = rec;
+  } else {
+    // ---- join the cluster's CTAs: each writes its part of the pair's outputs
+    float* part = reinterpret_cast<float*>(smem);
+    if (w0 >= w1 && (int)threadIdx.x < grp) {
+      part[threadIdx.x * (D + 2)] = -INFINITY;
+      part[threadIdx.x * (D + 2) + 1] = 0.f;
+    }
+    __syncwarp();
+    cluster_sync();
+    const int k = a.cluster, rank = c % k, each = (grp * D + k - 1) / k;
+    for (int x = rank * each + threadIdx.x; x < imin(grp * D, (rank + 1) * each); x += kWarps * 32) {
+      const int hd = x / D, d = x - hd * D;
+      const float* p = part + hd * (D + 2);
+      float m = -INFINITY;
+      for (int r = 0; r < k; ++r) m = fmaxf(m, cluster_ld(p, r));
+      float o = 0.f, l = 0.f;
+#pragma unroll 4
+      for (int r = 0; r < k; ++r) {
+        const float mr = cluster_ld(p, r);
+        if (mr == -INFINITY) continue;  // (its outputs were not written)
+        const float f = ptx::ex2(mr - m);
+        l += f * cluster_ld(p + 1, r);
+        o += f * cluster_ld(p + 2 + d, r);
+      }
+      const size_t h = (size_t)first_item * grp + hd;
+      reinterpret_cast<__nv_bfloat16*>(a.o)[h * D + d] = __float2bfloat16_rn(m == -INFINITY ? 0.f : o / l);
+      if (a.lse && d == 0) a.lse[h] = m == -INFINITY ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
+    }
+    __syncwarp();
+    cluster_sync();  // no CTA leaves while another still reads from it
+  }
 }
 
 // Joins the pieces of the pair that begins in CTA c and goes on in later ones; one block per
@@ -641,20 +711,34 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
 template <int D, bool KV8>
 cudaError_t launch_paged_t(const PagedDecodeArgs& a, cudaStream_t s) {
   const int bytes = Geo<D, KV8>::smem(a.grp);
-  cudaError_t e = cudaFuncSetAttribute(paged_split_kernel<D, KV8>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e != cudaSuccess) return e;
-  // both kernels are set up while the one before them runs, and wait for its results themselves
-  cudaLaunchAttribute at[1];
+  // the kernels are set up while the one before them runs, and wait for its results themselves
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.grid);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = s;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  if ((e = cudaLaunchKernelEx(&cfg, paged_split_kernel<D, KV8>, a)) != cudaSuccess) return e;
+  cudaError_t e;
+  if (a.cluster > 0) {
+    auto kern = paged_split_kernel<D, KV8, true>;
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
+    if (a.cluster > 8 &&
+        (e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
+      return e;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = a.cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+    cfg.gridDim = dim3((unsigned)(a.B * a.Hkv * a.cluster));
+    return cudaLaunchKernelEx(&cfg, kern, a);
+  }
+  auto kern = paged_split_kernel<D, KV8, false>;
+  if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
+  cfg.gridDim = dim3(a.grid);
+  if ((e = cudaLaunchKernelEx(&cfg, kern, a)) != cudaSuccess) return e;
   cfg.gridDim = dim3(a.grid, a.grp);
   cfg.blockDim = dim3(128);
   cfg.dynamicSmemBytes = 0;
@@ -663,17 +747,26 @@ cudaError_t launch_paged_t(const PagedDecodeArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-// CTAs of a paged decode: as many as the GPU holds at once, and no more than there can be tiles (0:
-// more tiles than the kernels can count).
-int paged_decode_grid(const Pat& p, int B, int Hq, int Hkv, int d, bool kv8, int max_pages, int page_size) {
+// How a paged decode is laid out.  grid: CTAs that share the list of all tiles, as many as the GPU holds at
+// once, and no more than there can be tiles (0: more tiles than the kernels can count).  cluster > 0:
+// instead, a cluster of so many CTAs per pair, the largest power of two up to 16 with which all fit the
+// GPU at once, if then no CTA can have more than kClusterTiles tiles.
+PagedPlan paged_decode_plan(const Pat& p, int B, int Hq, int Hkv, int d, bool kv8, int max_pages, int page_size) {
   const int grp = Hq / Hkv;
   const int most = 148 * (kv8 ? Geo<128, true>::ctas(grp) : (d == 128 ? Geo<128, false>::ctas(grp) : Geo<64, false>::ctas(grp)));
-  const int64_t cap = (int64_t)max_pages * page_size, R = (int64_t)p.T - p.S;
+  const int64_t cap = (int64_t)max_pages * page_size, R = (int64_t)p.T - p.S, pairs = (int64_t)B * Hkv;
   const int64_t wide = R > 0 ? (R + p.H - 1) / p.H : 0;
   auto tiles = [&](int64_t n) { return n > 0 ? ((n < cap ? n : cap) + kTok - 1) / kTok + 1 : 0; };
-  const int64_t n = tiles(p.S) + tiles(wide) + tiles(p.L) + kSegment;
-  if (n > 0x7fffffff / ((int64_t)B * Hkv)) return 0;  // the kernels count tiles in 32 bits
-  return (int)(n * B * Hkv < most ? n * B * Hkv : most);
+  int64_t n = tiles(p.S) + tiles(wide) + tiles(p.L);
+  const int64_t all = (cap + kTok - 1) / kTok + 2;  // (the ranges lie in the cache, and do not overlap)
+  n = n < all ? n : all;
+  PagedPlan plan{0, 0};
+  if (n + kSegment > 0x7fffffff / pairs) return plan;  // the kernels count tiles in 32 bits
+  plan.grid = (int)((n + kSegment) * pairs < most ? (n + kSegment) * pairs : most);
+  int k = 16;
+  while (k > 1 && pairs * k > most) k /= 2;
+  if ((n + k - 1) / k <= kClusterTiles) plan.cluster = k;
+  return plan;
 }
 
 size_t paged_decode_bytes(int grid, int grp, int d) {

@@ -8,6 +8,7 @@ less than 2^-13, as are the 32-bit sums of P and O together, so 2^-12 A more.  l
 error and a few roundings of a number below 32: 2e-4."""
 
 import ctypes
+import dataclasses
 
 import numpy as np
 import pytest
@@ -61,6 +62,16 @@ def make_table(rng, B, n, spare=2, heads=None):
     return t.reshape((B, heads, n) if heads else (B, n)), want + spare
 
 
+def widened(pat, tab, ps):
+    """The pattern with a far longer declared span (head 0's interval then holds everything behind the
+    sink) and the table with unmapped pages up to 25,000 positions: a call that could have long pairs,
+    whose work is shared out over the whole list of tiles and joined by a second kernel; the small
+    caches of these tests otherwise take the cluster form."""
+    more = -(-25000 // ps) - tab.shape[-1]
+    return dataclasses.replace(pat, T=pat.S + 400000), np.concatenate(
+        [tab, np.full((*tab.shape[:-1], more), -1, np.int32)], axis=-1)
+
+
 def ws_for(fn, pat, B, Hq, Hkv, d, n, ps, dev):
     size = getattr(cw.lib(), fn + "_workspace_size")(ctypes.byref(pat.c()), B, Hq, Hkv, d, n, ps)
     return torch.zeros(size, dtype=torch.uint8, device=dev)
@@ -83,11 +94,17 @@ DECODE = [
 
 @pytest.mark.parametrize("Hq,Hkv,d,pat,ps,n,per_head,layout,pos", DECODE)
 @pytest.mark.parametrize("e4m3", [False, True])
-def test_decode_matches_oracle(cuda_device, Hq, Hkv, d, pat, ps, n, per_head, layout, pos, e4m3):
+@pytest.mark.parametrize("wide", [False, True])
+def test_decode_matches_oracle(cuda_device, Hq, Hkv, d, pat, ps, n, per_head, layout, pos, e4m3, wide):
     if e4m3 and d != 128:
         pytest.skip("E4M3 pages need d = 128")
     B, rng = len(pos), np.random.default_rng(ps * n)
     tab, n_pages = make_table(rng, B, n, heads=Hkv if per_head else None)
+    cap = n * ps
+    if wide:
+        pat, tab = widened(pat, tab, ps)
+        pos = [min(p, cap - 1) for p in pos]
+        n = tab.shape[-1]
     shape = (n_pages, ps, 1 if per_head else Hkv, d)
     if e4m3:
         kc, vc = (f8.f64_to_e4m3(rng.standard_normal(shape) * 3) for _ in range(2))
@@ -104,8 +121,8 @@ def test_decode_matches_oracle(cuda_device, Hq, Hkv, d, pat, ps, n, per_head, la
                              torch.tensor(pos, dtype=torch.int32, device=cuda_device), pat,
                              *((0.4, 0.25) if e4m3 else ()), layout=layout, workspace=ws)
     assert cw.workspace_status(ws) == 0
-    k, _ = orp.gather_pages(k64, tab, n * ps)
-    v, _ = orp.gather_pages(v64, tab, n * ps)
+    k, _ = orp.gather_pages(k64, tab, cap)
+    v, _ = orp.gather_pages(v64, tab, cap)
     assert_decoded(o, lse, q64, k, v, pos, pat, 2.0 ** -11 if e4m3 else 2.0 ** -8)
 
 
@@ -126,13 +143,17 @@ def test_decode_equals_the_contiguous_decode(cuda_device):
 
 @pytest.mark.parametrize("e4m3", [False, True])
 @pytest.mark.parametrize("ps,layout", [(16, "bthd"), (64, "bhtd"), (24, "bthd")])
-def test_unseen_rows_may_hold_anything(cuda_device, e4m3, ps, layout):
+@pytest.mark.parametrize("wide", [False, True])
+def test_unseen_rows_may_hold_anything(cuda_device, e4m3, ps, layout, wide):
     """NaN and infinities in every row that no head sees, and pages of their own for each head, of which
     only the needed ones are mapped: the same result, to the bit, as over clean pages."""
     Hq, Hkv, d, n = 10, 2, 128, 512 // ps
     pat, pos = cw.Pattern(20, 70, 500, 2), [500, 130, 60, 21, 0]
     B, rng = len(pos), np.random.default_rng(74)
     tab, n_pages = make_table(rng, B, n, heads=Hkv)
+    if wide:
+        pat, tab = widened(pat, tab, ps)
+        n = tab.shape[-1]
     clean = tab.copy()
     shape = (n_pages, ps, 1, d)
     if e4m3:
@@ -145,7 +166,7 @@ def test_unseen_rows_may_hold_anything(cuda_device, e4m3, ps, layout):
     for b in range(B):
         for g in range(Hkv):
             see = orc.visible_mask(np.array([pos[b]]), n * ps, oracle_pattern(pat), g, Hkv)[0]
-            for s in np.flatnonzero(~see):
+            for s in np.flatnonzero(~see[:512 // ps * ps]):
                 for i, p in enumerate(dirty):
                     p[int(tab[b, g, s // ps]), int(s % ps), 0] = junk[(i + int(s)) % 2]
             tab[b, g, ~see.reshape(n, ps).any(1)] = [-1, 2**31 - 1, n_pages][g + 0 if b % 2 else 2]
@@ -167,7 +188,8 @@ def test_unseen_rows_may_hold_anything(cuda_device, e4m3, ps, layout):
 
 
 @pytest.mark.parametrize("e4m3", [False, True])
-def test_bad_entries_are_left_out_and_reported(cuda_device, e4m3):
+@pytest.mark.parametrize("wide", [False, True])
+def test_bad_entries_are_left_out_and_reported(cuda_device, e4m3, wide):
     """Entries outside the pool on pages with visible keys: their keys are left out, the status says so
     once, and a sequence whose every page is bad gives zeros and -inf."""
     B, Hq, Hkv, d, ps, n = 4, 8, 2, 128, 16, 20
@@ -177,6 +199,9 @@ def test_bad_entries_are_left_out_and_reported(cuda_device, e4m3):
     tab[0, [1, 17]] = -1, n_pages
     tab[1, 15] = 2**31 - 1
     tab[3, :] = -2**31
+    if wide:
+        pat, tab = widened(pat, tab, ps)
+        n = tab.shape[-1]
     shape = (n_pages, ps, Hkv, d)
     if e4m3:
         kc, vc = (f8.f64_to_e4m3(rng.standard_normal(shape) * 3) for _ in range(2))
@@ -192,8 +217,8 @@ def test_bad_entries_are_left_out_and_reported(cuda_device, e4m3):
                              *((1.0, 1.0) if e4m3 else ()), workspace=ws)
     assert cw.workspace_status(ws) == 8
     assert cw.workspace_status(ws) == 0
-    k, has = orp.gather_pages(k64, tab, n * ps)
-    v, _ = orp.gather_pages(v64, tab, n * ps)
+    k, has = orp.gather_pages(k64, tab, 320)
+    v, _ = orp.gather_pages(v64, tab, 320)
     assert_decoded(o, lse, q64, k, v, pos, pat, 2.0 ** -11 if e4m3 else 2.0 ** -8, has=has)
 
 
