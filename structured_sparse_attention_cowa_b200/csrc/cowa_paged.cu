@@ -47,6 +47,7 @@ constexpr float kRescale = 8.0f;               // lazy-rescale threshold, log2 u
 constexpr int kSegment = 2;
 // Up to how many tiles a CTA may have for the cluster form.
 constexpr int kClusterTiles = 8;
+constexpr int kMaxCluster = 16;
 // E4M3: P is rounded to f16, whose smallest normal number is 2^-14; relative to a running maximum
 // lifted by 2^6 (P at most 2^14) it covers P down to 2^-20 of the largest at full precision.
 template <bool KV8>
@@ -645,16 +646,27 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV8>::kCtas)
     for (int x = rank * each + threadIdx.x; x < imin(grp * D, (rank + 1) * each); x += kWarps * 32) {
       const int hd = x / D, d = x - hd * D;
       const float* p = part + hd * (D + 2);
-      float m = -INFINITY;
-      for (int r = 0; r < k; ++r) m = fmaxf(m, cluster_ld(p, r));
-      float o = 0.f, l = 0.f;
-#pragma unroll 4
-      for (int r = 0; r < k; ++r) {
-        const float mr = cluster_ld(p, r);
-        if (mr == -INFINITY) continue;  // (its outputs were not written)
-        const float f = ptx::ex2(mr - m);
-        l += f * cluster_ld(p + 1, r);
-        o += f * cluster_ld(p + 2 + d, r);
+      // (all loads of a kind are on their way before the first is used)
+      float mr[kMaxCluster], lr[kMaxCluster], om[kMaxCluster], m = -INFINITY, o = 0.f, l = 0.f;
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) {
+        mr[r] = -INFINITY;
+        if (r < k) mr[r] = cluster_ld(p, r);
+      }
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r)
+        if (r < k) {
+          lr[r] = cluster_ld(p + 1, r);
+          om[r] = cluster_ld(p + 2 + d, r);
+        }
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) m = fmaxf(m, mr[r]);
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) {
+        if (mr[r] == -INFINITY) continue;  // (no such CTA, or its outputs were not written)
+        const float f = ptx::ex2(mr[r] - m);
+        l += f * lr[r];
+        o += f * om[r];
       }
       const size_t h = (size_t)first_item * grp + hd;
       reinterpret_cast<__nv_bfloat16*>(a.o)[h * D + d] = __float2bfloat16_rn(m == -INFINITY ? 0.f : o / l);
@@ -763,7 +775,7 @@ PagedPlan paged_decode_plan(const Pat& p, int B, int Hq, int Hkv, int d, bool kv
   PagedPlan plan{0, 0};
   if (n + kSegment > 0x7fffffff / pairs) return plan;  // the kernels count tiles in 32 bits
   plan.grid = (int)((n + kSegment) * pairs < most ? (n + kSegment) * pairs : most);
-  int k = 16;
+  int k = kMaxCluster;
   while (k > 1 && pairs * k > most) k /= 2;
   if ((n + k - 1) / k <= kClusterTiles) plan.cluster = k;
   return plan;
