@@ -812,7 +812,7 @@ cowa_status decode_paged(const cowa_pattern* pat, int B, int Hq, int Hkv, int d,
       (reinterpret_cast<uintptr_t>(lse) & 3u))
     return COWA_ERR_ALIGNMENT;
   const PagedPlan plan = paged_decode_plan(p, B, Hq, Hkv, d, e4m3, table.max_pages, table.page_size);
-  a.grid = plan.grid; a.cluster = plan.cluster;
+  a.grid = plan.grid; a.cluster = plan.cluster; a.by_pair = (int64_t)B * Hkv <= plan.grid;
   if (a.grid == 0 || (int64_t)B * Hq > 0x7fffffff) return COWA_ERR_UNSUPPORTED;
   COWA_TRY(check_ws(ws, ws_bytes, kWsHeader + paged_decode_bytes(a.grid, Hq / Hkv, d)));
   a.pat = p; a.B = B; a.Hkv = Hkv; a.grp = Hq / Hkv;

@@ -85,7 +85,10 @@ struct PagedDecodeArgs {
   void* o;
   float* lse;        // may be null
   uint32_t* status;  // word 3: a visible page's entry was outside the pool
-  int4* rec;         // [grid]: {pair, last CTA} of the (b, g) that begins in CTA c and does not end there; x = -1: none
+  // [pairs] (by_pair) or [grid], whichever is less: {pair, first CTA, last CTA} of the (b, g), or of the one
+  // that begins in the CTA and does not end there; x = -1: nothing to join
+  int4* rec;
+  int by_pair;
   float* part;       // [2 grid][grp][d + 2] fp32 partials: m, l, o
   float scale_log2, v_scale;
   int grid, cluster; // see paged_decode_plan

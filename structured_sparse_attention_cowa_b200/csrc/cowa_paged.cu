@@ -45,9 +45,11 @@ constexpr float kRescale = 8.0f;               // lazy-rescale threshold, log2 u
 // tiles: 37 sequences of 1 to 32K positions, E4M3, took 2.0 us a segment and 1.0 us a tile, and the CTAs
 // that held nine segments of one tile each twice as long as the others.
 constexpr int kSegment = 2;
-// Up to how many tiles a CTA may have for the cluster form.
-constexpr int kClusterTiles = 8;
+// Up to how many tiles a CTA may have for the cluster form: with 9.5 (8 sequences of 8K) it took 12.0 us
+// against the list's 13.8, with 12.6 (two of 32K) 14.1 against 13.2.
+constexpr int kClusterTiles = 10;
 constexpr int kMaxCluster = 16;
+constexpr int kJoinWarps = 16;  // of a joining block, at most
 // E4M3: P is rounded to f16, whose smallest normal number is 2^-14; relative to a running maximum
 // lifted by 2^6 (P at most 2^14) it covers P down to 2^-20 of the largest at full precision.
 template <bool KV8>
@@ -430,6 +432,8 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV8>::kCtas)
       reinterpret_cast<uint4*>(a.o)[h0 * (D / 8) + x] = make_uint4(0, 0, 0, 0);
     if (a.lse)
       for (int x = threadIdx.x; x < a.Hkv * grp; x += kWarps * 32) a.lse[h0 + x] = -INFINITY;
+    if (a.by_pair)
+      for (int x = threadIdx.x; x < a.Hkv; x += kWarps * 32) a.rec[i * a.Hkv + x].x = -1;
   }
 
   int4 rec = make_int4(-1, 0, 0, 0);
@@ -578,7 +582,14 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV8>::kCtas)
       }
       // ---- the next segment's pair and query rows, while the warps are joined
       const bool begins = off == 0, ends = lim == n;
-      if (!CL && begins && !ends) rec = make_int4(item, sh.of(place + kSegment + n - 1), 0, 0);  // the CTA with its last tile
+      if (!CL && begins) {  // whether the pair goes on, and to which CTA
+        const int4 r = make_int4(ends ? -1 : item, c, sh.of(place + kSegment + n - 1), 0);
+        if (a.by_pair) {
+          if (threadIdx.x == 0) a.rec[item] = r;
+        } else if (!ends) {
+          rec = r;
+        }
+      }
       more = !CL && step();
       if (more) load_q(item);
       // ---- join the warps
@@ -632,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV8>::kCtas)
     }
   }
   if constexpr (!CL) {
-    if (threadIdx.x == 0) a.rec[c] = rec;
+    if (!a.by_pair && threadIdx.x == 0) a.rec[c] = rec;
   } else {
     // ---- join the cluster's CTAs: each writes its part of the pair's outputs
     float* part = reinterpret_cast<float*>(smem);
@@ -677,30 +688,31 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV8>::kCtas)
   }
 }
 
-// Joins the pieces of the pair that begins in CTA c and goes on in later ones; one block per
-// (c, head of the group).  Each warp takes every fourth piece; the pieces' order is fixed.
+// Joins the pieces of a pair that several CTAs share; one block per (record, head of the group).  Warp w
+// takes pieces w, w + warps, ..; the pieces' order is fixed.
 template <int D>
-__global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ PagedDecodeArgs a) {
+__global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const __grid_constant__ PagedDecodeArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int c = blockIdx.x, hd = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int4 rec = a.rec[c];
+  const int hd = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  const int4 rec = a.rec[blockIdx.x];
   if (rec.x < 0) return;
   constexpr int E = D / 32;
-  __shared__ float sm[4], sl[4], so[4][D];
-  const int n = rec.y - c + 1;
+  __shared__ float sm[kJoinWarps], sl[kJoinWarps], so[kJoinWarps][D];
+  const int c = rec.y, n = rec.z - c + 1;
   const size_t slot = (size_t)a.grp * (D + 2);
   // piece 0 is CTA c's last segment, piece i CTA c + i's first
   auto piece = [&](int i) { return a.part + (i == 0 ? 2 * (size_t)c + 1 : 2 * ((size_t)c + i)) * slot + hd * (D + 2); };
   float m = -INFINITY;
-  for (int i = warp * 32 + lane; i < n; i += 128) m = fmaxf(m, piece(i)[0]);
+  for (int i = threadIdx.x; i < n; i += blockDim.x) m = fmaxf(m, piece(i)[0]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   if (lane == 0) sm[warp] = m;
   __syncthreads();
-  m = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
+  m = sm[0];
+  for (int w = 1; w < warps; ++w) m = fmaxf(m, sm[w]);
   float acc[E] = {}, l = 0.f;
-#pragma unroll 4
-  for (int i = warp; i < n; i += 4) {
+#pragma unroll 8
+  for (int i = warp; i < n; i += warps) {
     const float* p = piece(i);
     const float f = p[0] == -INFINITY ? 0.f : ptx::ex2(p[0] - m);
     l += f * p[1];
@@ -713,8 +725,9 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
   __syncthreads();
   if (threadIdx.x >= D) return;
   const int d = threadIdx.x;
-  l = sl[0] + sl[1] + sl[2] + sl[3];
-  const float o = so[0][d] + so[1][d] + so[2][d] + so[3][d];
+  l = sl[0];
+  float o = so[0][d];
+  for (int w = 1; w < warps; ++w) { l += sl[w]; o += so[w][d]; }
   const size_t h = (size_t)rec.x * a.grp + hd;
   reinterpret_cast<__nv_bfloat16*>(a.o)[h * D + d] = __float2bfloat16_rn(m == -INFINITY ? 0.f : o / l);
   if (a.lse && d == 0) a.lse[h] = m == -INFINITY ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
@@ -751,8 +764,9 @@ cudaError_t launch_paged_t(const PagedDecodeArgs& a, cudaStream_t s) {
   if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
   cfg.gridDim = dim3(a.grid);
   if ((e = cudaLaunchKernelEx(&cfg, kern, a)) != cudaSuccess) return e;
-  cfg.gridDim = dim3(a.grid, a.grp);
-  cfg.blockDim = dim3(128);
+  // a pair in many pieces is one of few: more warps for it
+  cfg.gridDim = dim3(a.by_pair ? a.B * a.Hkv : a.grid, a.grp);
+  cfg.blockDim = dim3(a.grid >= 8 * a.B * a.Hkv ? kJoinWarps * 32 : 128);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, paged_join_kernel<D>, a);
 }
@@ -761,8 +775,10 @@ cudaError_t launch_paged_t(const PagedDecodeArgs& a, cudaStream_t s) {
 
 // How a paged decode is laid out.  grid: CTAs that share the list of all tiles, as many as the GPU holds at
 // once, and no more than there can be tiles (0: more tiles than the kernels can count).  cluster > 0:
-// instead, a cluster of so many CTAs per pair, the largest power of two up to 16 with which all fit the
-// GPU at once, if then no CTA can have more than kClusterTiles tiles.
+// instead, a cluster of so many CTAs per pair: 16 if all fit one CTA an SM (16 at two an SM are slower
+// than 8: 18.8 against 14.0 us for 16 pairs of 6,200 keys), else 8 or 4 with which all fit the GPU at
+// once, if then no CTA can have more than kClusterTiles tiles.  With fewer than 4 the list is as fast or
+// faster (296 pairs of up to 680 keys in the cluster form: 21.6 us full, 18.8 ragged; 22.4 and 13.6 as a list).
 PagedPlan paged_decode_plan(const Pat& p, int B, int Hq, int Hkv, int d, bool kv8, int max_pages, int page_size) {
   const int grp = Hq / Hkv;
   const int most = 148 * (kv8 ? Geo<128, true>::ctas(grp) : (d == 128 ? Geo<128, false>::ctas(grp) : Geo<64, false>::ctas(grp)));
@@ -775,9 +791,8 @@ PagedPlan paged_decode_plan(const Pat& p, int B, int Hq, int Hkv, int d, bool kv
   PagedPlan plan{0, 0};
   if (n + kSegment > 0x7fffffff / pairs) return plan;  // the kernels count tiles in 32 bits
   plan.grid = (int)((n + kSegment) * pairs < most ? (n + kSegment) * pairs : most);
-  int k = kMaxCluster;
-  while (k > 1 && pairs * k > most) k /= 2;
-  if ((n + k - 1) / k <= kClusterTiles) plan.cluster = k;
+  const int k = pairs * 16 <= 148 ? 16 : (pairs * 8 <= most ? 8 : 4);
+  if (pairs * k <= most && (n + k - 1) / k <= kClusterTiles) plan.cluster = k;
   return plan;
 }
 
