@@ -421,8 +421,7 @@ cowa_status cowa_decode_paged_fp8(const cowa_pattern* pat, int B, int H_q, int H
  * cu_seqlens[s] .. cu_seqlens[s+1]-1 of q [total, H_q, d], the first at position q_start[s], against its
  * keys at positions 0 .. q_start[s] + len_s - 1, the chunk's own among them (cowa_paged_append first).
  * Outputs o [total, H_q, d] and lse fp32 [H_q, total] as cowa_fwd_varlen, whose rules hold for
- * cu_seqlens (device int32 [n_seq + 1]), strides and workspace; rows behind the last sequence are left
- * as they are.  q_start: device int32 [n_seq], clamped into [0, capacity - len_s] (rows of a sequence
+ * cu_seqlens (device int32 [n_seq + 1]) and strides; rows behind the last sequence are left as they are.  q_start: device int32 [n_seq], clamped into [0, capacity - len_s] (rows of a sequence
  * longer than the capacity see the keys there are); a row that sees nothing has o 0 and lse -inf.
  * Where an entry of a page with a key that some row of a query tile (128 rows of a sequence) sees lies
  * outside [0, n_pages), the tile's rows of that KV head's group are left empty (o 0, lse -inf) and

@@ -838,7 +838,9 @@ cowa_status decode_paged(const cowa_pattern* pat, int B, int Hq, int Hkv, int d,
 }  // namespace
 
 size_t cowa_fwd_paged_workspace_size(const cowa_pattern* pat, int n_seq, int total, int H_q, int H_kv, int d) {
-  return cowa_fwd_varlen_workspace_size(pat, n_seq, total, H_q, H_kv, d);
+  Pat p;
+  if (n_seq < 1 || check_pattern(pat, H_kv, &p) != COWA_OK || check_heads(1, total, H_q, H_kv, d) != COWA_OK) return 0;
+  return kWsHeader;
 }
 
 cowa_status cowa_fwd_paged(const cowa_pattern* pat, int n_seq, int total, int Hq, int Hkv, int d,
@@ -859,7 +861,6 @@ cowa_status cowa_fwd_paged(const cowa_pattern* pat, int n_seq, int total, int Hq
   a.pat = p; a.B = 1; a.Hq = Hq; a.Hkv = Hkv; a.d = d;
   a.Nq = total; a.Nk = total;
   a.varlen = 1; a.n_seq = n_seq; a.total = total; a.cu_seqlens = cu_seqlens;
-  a.seq_tab = reinterpret_cast<int32_t*>(reinterpret_cast<char*>(ws) + kWsHeader);
   a.paged = 1;
   a.q_start = q_start;
   a.box_rows = page_box_rows(table.page_size, 128);

@@ -17,7 +17,9 @@
 // PAGED: a packed batch of query chunks against a paged cache.  The K/V tiles keep their places
 // (128 positions each); the producer warp looks up the pages of a tile, one lane per TMA box of 8 to
 // 128 rows, and fetches the boxes that some row of the query tile sees.  V rows that are not fetched,
-// or lie past the last key, are zeroed (their P is 0, but 0 times what memory holds may be NaN).
+// or lie past the last key, are zeroed (their P is 0, but 0 times what memory holds may be NaN).  The
+// CTAs come heaviest first over all sequences (see find_chunk), and those with a single head, of an
+// odd group, last.
 // Registers: the kernel is compiled for 168 per thread (384 * 168 = 64512 at launch); the two
 // softmax warpgroups then raise theirs to 216 and the third lowers to 72
 // (2*128*216 + 128*72 = 64512), so a whole 128-column score row stays in registers.  The
@@ -75,6 +77,85 @@ struct FwdGeom {
   static constexpr int kColO = 256;
 };
 
+// PAGED: query tile `rank` of the packed chunks; one warp.  Up to 64 sequences: the tiles in descending
+// order of the position they begin at (in steps of a tile), which is about that of their work, found
+// by a binary search over that position with the sequences in the lanes' registers.  More: sequence by
+// sequence.  The offsets are clamped as in the sequence table of kernel_common.cuh.
+struct Chunk {
+  int seq, tile, row0, len, start;  // seq -1: there are no more tiles
+};
+__device__ __forceinline__ Chunk find_chunk(const FwdArgs& a, int rank) {
+  constexpr unsigned kAll = 0xffffffffu;
+  const int lane = threadIdx.x & 31, cap = a.tab.max_pages * a.tab.page_size;
+  struct Seq {
+    int row0, len, start, tiles;
+  };
+  int end = imin(imax(a.cu_seqlens[0], 0), a.total);  // of the sequences before
+  auto load = [&](int first) {  // sequences first .. first + 31, one per lane
+    const int s = first + lane;
+    int e = s < a.n_seq ? a.cu_seqlens[s + 1] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(kAll, e, o);
+      if (lane >= o) e = imax(e, y);
+    }
+    e = imin(imax(e, end), a.total);
+    const int before = __shfl_up_sync(kAll, e, 1);
+    Seq q;
+    q.row0 = lane == 0 ? end : before;
+    q.len = e - q.row0;
+    q.start = s < a.n_seq ? imax(0, imin(a.q_start[s], cap - q.len)) : 0;
+    q.tiles = (q.len + kBM - 1) / kBM;
+    end = __shfl_sync(kAll, e, 31);
+    return q;
+  };
+  auto hand = [&](const Seq& q, int src, int first, int tile) {
+    return Chunk{first + src, __shfl_sync(kAll, tile, src), __shfl_sync(kAll, q.row0, src), __shfl_sync(kAll, q.len, src),
+                 __shfl_sync(kAll, q.start, src)};
+  };
+  if (a.n_seq <= 64) {
+    const Seq q0 = load(0);
+    Seq q1 = {0, 0, 0, 0};
+    if (a.n_seq > 32) q1 = load(32);
+    const int k0 = q0.start / kBM, k1 = q1.start / kBM;  // place of a sequence's first tile
+    auto from = [&](int x) {  // tiles at place x or later
+      return (int)__reduce_add_sync(kAll, (unsigned)(imax(0, imin(q0.tiles, k0 + q0.tiles - x)) +
+                                                     imax(0, imin(q1.tiles, k1 + q1.tiles - x))));
+    };
+    if (from(0) <= rank) return Chunk{-1, 0, 0, 0, 0};
+    int lo = 0, hi = (int)__reduce_max_sync(kAll, (unsigned)imax(k0 + q0.tiles, k1 + q1.tiles));
+    while (lo < hi) {  // the last place with more than `rank` tiles at it or later
+      const int mid = (lo + hi + 1) >> 1;
+      if (from(mid) > rank) lo = mid; else hi = mid - 1;
+    }
+    const int nth = rank - from(lo + 1);
+    const unsigned in0 = __ballot_sync(kAll, k0 <= lo && lo < k0 + q0.tiles), in1 = __ballot_sync(kAll, k1 <= lo && lo < k1 + q1.tiles);
+    const int n0 = __popc(in0);
+    return nth < n0 ? hand(q0, __fns(in0, 0, nth + 1), 0, lo - k0) : hand(q1, __fns(in1, 0, nth - n0 + 1), 32, lo - k1);
+  }
+  for (int first = 0, done = 0; first < a.n_seq; first += 32) {
+    const Seq q = load(first);
+    int incl = q.tiles;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(kAll, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const int before = done + incl - q.tiles;
+    const unsigned in = __ballot_sync(kAll, rank >= before && rank < before + q.tiles);
+    if (in) return hand(q, __ffs(in) - 1, first, q.tiles - 1 - (rank - before));
+    done += __shfl_sync(kAll, incl, 31);
+  }
+  return Chunk{-1, 0, 0, 0, 0};
+}
+
+// bits lo .. hi - 1 of a word (either may lie outside it)
+__device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
+  lo = imax(lo, 0);
+  hi = imin(hi, 32);
+  return hi > lo ? (0xffffffffu >> (32 - (hi - lo))) << lo : 0u;
+}
+
 template <int D, bool PAGED>
 __global__ void __launch_bounds__(kFwdThreads, 1) cowa_fwd_kernel(const __grid_constant__ FwdArgs a) {
   using Geo = FwdGeom<D>;
@@ -102,29 +183,51 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cowa_fwd_kernel(const __grid_c
   const int per_i = a.B * a.Hkv * npair;
   int i, row0 = 0, Nq = a.Nq, Nk = a.Nk, q_off = a.q_off;  // row0: first row of the sequence
   int pg_seq = 0;
-  if (!a.varlen) {
-    i = (a.Nq + kBM - 1) / kBM - 1 - (int)(blockIdx.x / per_i);
-  } else {
-    // the grid is an upper bound on the q-tiles of the packed batch: find this CTA's sequence
-    const int tiles = a.seq_tab[a.n_seq];
-    const int tg = tiles - 1 - (int)(blockIdx.x / per_i);
-    if (tg < 0) return;  // whole CTA, before any barrier or TMEM use
-    const int sq = seq_of_tile(a.seq_tab, a.n_seq, tg);
-    i = tg - a.seq_tab[sq];
-    row0 = a.seq_tab[a.n_seq + 1 + sq];
-    Nq = Nk = a.seq_tab[2 * a.n_seq + 1 + sq];
-    q_off = 0;
-    if constexpr (PAGED) {
-      const int cap = a.tab.max_pages * a.tab.page_size;
-      pg_seq = sq;
-      q_off = imax(0, imin(a.q_start[sq], cap - Nq));
-      Nk = imin(q_off + Nq, cap);
+  int pair, g, b = 0;
+  if constexpr (PAGED) {
+    // (set up while the kernel before it in the stream ran; waits for that one's results here)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    __shared__ Chunk chunk;
+    const int whole = grp >> 1, bound = (int)packed_tiles_bound(a.total, a.n_seq), n_whole = bound * a.Hkv * whole;
+    int rank = blockIdx.x;
+    if (rank < n_whole) {
+      pair = rank % whole; rank /= whole;
+    } else {  // the odd heads, half as much work each
+      rank -= n_whole;
+      pair = whole;
     }
+    g = rank % a.Hkv; rank /= a.Hkv;
+    if (warp == 0) {
+      const Chunk c = find_chunk(a, rank);
+      if (lane == 0) chunk = c;
+    }
+    __syncthreads();
+    if (chunk.seq < 0) return;  // whole CTA, before any barrier or TMEM use
+    pg_seq = chunk.seq;
+    i = chunk.tile;
+    row0 = chunk.row0;
+    Nq = chunk.len;
+    q_off = chunk.start;
+    Nk = imin(q_off + Nq, a.tab.max_pages * a.tab.page_size);
+  } else {
+    if (!a.varlen) {
+      i = (a.Nq + kBM - 1) / kBM - 1 - (int)(blockIdx.x / per_i);
+    } else {
+      // the grid is an upper bound on the q-tiles of the packed batch: find this CTA's sequence
+      const int tiles = a.seq_tab[a.n_seq];
+      const int tg = tiles - 1 - (int)(blockIdx.x / per_i);
+      if (tg < 0) return;  // whole CTA, before any barrier or TMEM use
+      const int sq = seq_of_tile(a.seq_tab, a.n_seq, tg);
+      i = tg - a.seq_tab[sq];
+      row0 = a.seq_tab[a.n_seq + 1 + sq];
+      Nq = Nk = a.seq_tab[2 * a.n_seq + 1 + sq];
+      q_off = 0;
+    }
+    int rem = blockIdx.x % per_i;
+    pair = rem % npair; rem /= npair;
+    g = rem % a.Hkv;
+    b = rem / a.Hkv;
   }
-  int rem = blockIdx.x % per_i;
-  const int pair = rem % npair; rem /= npair;
-  const int g = rem % a.Hkv;
-  const int b = rem / a.Hkv;
   const int h0 = g * grp + 2 * pair;
   const bool has1 = (2 * pair + 1) < grp;
   // query rows of the tile: local q rows [i*BM, ...), absolute positions [t0, t1)
@@ -447,7 +550,18 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cowa_fwd_kernel(const __grid_c
 #pragma unroll
         for (int q = 0; q < 4; ++q) ptx::tmem_ld32(s_tm + q * 32, xr + q * 32);
         ptx::tmem_wait_ld();
-        if (need_mask) {
+        if (PAGED && need_mask) {
+          // the visible columns as bits (a chunk of a few hundred rows is mostly partial tiles)
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const int o = 32 * w;
+            const uint32_t vis = bit_range(-o, sink_end - o) | bit_range(band_lo - o, diag_end - o) |
+                                 bit_range(lr_lo - o, lr_hi - o);
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (!((vis >> c) & 1)) xr[o + c] = 0xff800000u;  // -inf: gives exactly 0
+          }
+        } else if (need_mask) {
 #pragma unroll
           for (int c = 0; c < 128; ++c) {
             const bool vis = (c < sink_end) || (c >= band_lo && c < diag_end) || (c >= lr_lo && c < lr_hi);
@@ -665,6 +779,19 @@ cudaError_t launch_fwd_d(const FwdArgs& a, cudaStream_t s) {
     regs_ok = fa.numRegs == kRegsLaunch ? 1 : 0;
   }
   if (!regs_ok) return cudaErrorInvalidConfiguration;
+  if (PAGED) {
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)nblk);
+    cfg.blockDim = dim3(kFwdThreads);
+    cfg.dynamicSmemBytes = Geo::kSmem;
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, a);
+  }
   if (a.varlen) {
     if ((e = launch_seq_table(a.cu_seqlens, a.n_seq, a.total, a.seq_tab, s)) != cudaSuccess) return e;
   }

@@ -161,7 +161,7 @@ cudaError_t launch_fwd(const FwdArgs& a, cudaStream_t s);
 inline size_t seq_table_bytes(int n_seq) { return align_up((size_t)(3 * n_seq + 1) * sizeof(int32_t), 256); }
 cudaError_t launch_seq_table(const int32_t* cu_seqlens, int n_seq, int total, int32_t* tab, cudaStream_t s);
 // upper bound on the 128-row tiles of a packed batch: sum of ceil(len / 128) <= total / 128 + n_seq
-inline long long packed_tiles_bound(int total, int n_seq) { return (long long)total / 128 + n_seq; }
+__host__ __device__ inline long long packed_tiles_bound(int total, int n_seq) { return (long long)total / 128 + n_seq; }
 
 // ---- backward ----
 struct BwdArgs {

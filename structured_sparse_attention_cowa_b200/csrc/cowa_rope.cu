@@ -85,6 +85,10 @@ __global__ void __launch_bounds__(kThreads, 4) turn_kernel(const __grid_constant
   __shared__ int live[kMaxTok];
   __shared__ __align__(16) __nv_bfloat16 stage[CUT == kAny ? kThreads * 8 : 8];
 
+  // set up while the kernel before it in the stream ran (it waits for that one's results here), as the
+  // one after it may be
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x;
   const long long m0 = (long long)blockIdx.x * tok_per_block;
   const int nt = (int)(a.M - m0 < tok_per_block ? a.M - m0 : tok_per_block);
@@ -342,10 +346,18 @@ cudaError_t launch_turn(const RopeArgs& a, cudaStream_t s) {
   const long long blocks = (a.M + tok - 1) / tok;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   const size_t smem = smem_bytes(MODE, tok, a.half, a.Hk);
-  if (cut == kSplit) turn_kernel<MODE, kSplit><<<(unsigned)blocks, kThreads, smem, s>>>(a, tok);
-  else if (cut == kInter) turn_kernel<MODE, kInter><<<(unsigned)blocks, kThreads, smem, s>>>(a, tok);
-  else turn_kernel<MODE, kAny><<<(unsigned)blocks, kThreads, smem, s>>>(a, tok);
-  return cudaGetLastError();
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  auto kern = cut == kSplit ? turn_kernel<MODE, kSplit> : (cut == kInter ? turn_kernel<MODE, kInter> : turn_kernel<MODE, kAny>);
+  return cudaLaunchKernelEx(&cfg, kern, a, tok);
 }
 
 }  // namespace

@@ -667,4 +667,4 @@ def test_chunk_graph_stream_and_refusals(cuda_device):
         with pytest.raises(TypeError):
             run(**bad)
     with pytest.raises(cw.CowaError):
-        run(workspace=torch.zeros(256, dtype=torch.uint8, device=cuda_device))
+        run(workspace=torch.zeros(128, dtype=torch.uint8, device=cuda_device))
