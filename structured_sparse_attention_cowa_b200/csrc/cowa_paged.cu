@@ -93,11 +93,10 @@ struct Pair {
   }
 };
 
-__device__ __forceinline__ Pair pair_of(const PagedDecodeArgs& a, int item) {
+// pair (b, g) at position t = pos[b]
+__device__ __forceinline__ Pair pair_at(const PagedDecodeArgs& a, int b, int g, int t) {
   Pair s;
-  s.b = item / a.Hkv;
-  const int g = item - s.b * a.Hkv;
-  int t = a.pos[s.b];
+  s.b = b;
   const int cap = a.tab.max_pages * a.tab.page_size;
   if (t >= cap) t = cap - 1;
   const Range iv = a.Hkv <= kPagedIv ? a.iv[g] : interval_of(a.pat, g);
@@ -111,6 +110,10 @@ __device__ __forceinline__ Pair pair_of(const PagedDecodeArgs& a, int item) {
   s.lo0 = r[0].lo; s.hi0 = r[0].hi; s.lo1 = r[1].lo; s.hi1 = r[1].hi; s.lo2 = r[2].lo; s.hi2 = r[2].hi;
   s.n = Pair::tiles_of(s.lo0, s.hi0) + Pair::tiles_of(s.lo1, s.hi1) + Pair::tiles_of(s.lo2, s.hi2);
   return s;
+}
+__device__ __forceinline__ Pair pair_of(const PagedDecodeArgs& a, int item) {
+  const int b = item / a.Hkv;
+  return pair_at(a, b, item - b * a.Hkv, a.pos[b]);
 }
 
 // 32 pairs, one per lane, handed to the whole warp one at a time (all lanes call with the same item,
@@ -292,10 +295,27 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV8>::kCtas)
     first_place = -kSegment;  // place w is tile w
     __syncthreads();
   } else {
+    // thread i adds up the pairs i0 .. i1 - 1; up to kKept of them stay at hand
+    constexpr int kKept = 4;
     const int per = (n_items + kThreads - 1) / kThreads;
     const int i0 = imin(n_items, (int)threadIdx.x * per), i1 = imin(n_items, i0 + per);
-    int mine = 0;
-    for (int i = i0; i < i1; ++i) mine += places(pair_of(a, i).n);
+    int mine = 0, kept[kKept];
+    if (per <= kKept) {
+      int b[kKept], g[kKept], t[kKept];
+#pragma unroll
+      for (int j = 0; j < kKept; ++j) {
+        b[j] = (i0 + j) / a.Hkv;
+        g[j] = i0 + j - b[j] * a.Hkv;
+        t[j] = i0 + j < i1 ? a.pos[b[j]] : -1;
+      }
+#pragma unroll
+      for (int j = 0; j < kKept; ++j) {
+        kept[j] = j < per ? places(pair_at(a, b[j], g[j], t[j]).n) : 0;
+        mine += kept[j];
+      }
+    } else {
+      for (int i = i0; i < i1; ++i) mine += places(pair_of(a, i).n);
+    }
     int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -317,10 +337,18 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV8>::kCtas)
     w1 = c < G ? sh.begin(c + 1) : W;
     if (w0 < w1 && before <= w0 && w0 < before + mine) {
       int p = before;
-      for (int i = i0; i < i1; ++i) {
-        const int n = per == 1 ? mine : places(pair_of(a, i).n);
-        if (w0 < p + n) { first_of[0] = i; first_of[1] = p; break; }
-        p += n;
+      if (per <= kKept) {
+#pragma unroll
+        for (int j = 0; j < kKept; ++j) {
+          if (w0 >= p && w0 < p + kept[j]) { first_of[0] = i0 + j; first_of[1] = p; }
+          p += kept[j];
+        }
+      } else {
+        for (int i = i0; i < i1; ++i) {
+          const int n = places(pair_of(a, i).n);
+          if (w0 < p + n) { first_of[0] = i; first_of[1] = p; break; }
+          p += n;
+        }
       }
     }
     __syncthreads();

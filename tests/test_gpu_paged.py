@@ -636,6 +636,48 @@ def test_chunk_bad_entries_and_overlong_sequences(cuda_device, Hq, ps):
     assert empty == [True, ps == 64, True] + [False] * (len(empty) - 3)
 
 
+@pytest.mark.parametrize("n_seq", [33, 64, 65, 150])
+def test_chunks_of_many_sequences(cuda_device, n_seq):
+    """However many sequences a call has (their tiles are dealt out in other orders then), each gets the
+    bits of a call of its own; some are empty, some a single row."""
+    Hq, Hkv, d, ps, n = 3, 1, 64, 16, 40
+    pat = cw.Pattern(30, 100, 640, 1)
+    rng = np.random.default_rng(n_seq)
+    lens = [int(x) for x in rng.choice([0, 0, 1, 2, 17, 128, 129, 300], n_seq)]
+    starts = [int(rng.integers(0, n * ps - x + 1)) for x in lens]
+    kp, vp = (synth.cuda_normal_bf16((500, ps, Hkv, d), synth.seed_of(x, 96), cuda_device) for x in ("k", "v"))
+    tab = torch.from_numpy(rng.integers(0, 500, (n_seq, n)).astype(np.int32)).to(cuda_device)
+    total = max(1, sum(lens))
+    q = synth.cuda_normal_bf16((total, Hq, d), synth.seed_of("q", 96), cuda_device)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=cuda_device)
+    cu = np.cumsum([0] + lens)
+    ws = torch.zeros(256, dtype=torch.uint8, device=cuda_device)
+    o, lse = cw.cowa_fwd_paged(q, kp, vp, tab, i32(cu.tolist()), i32(starts), pat, workspace=ws)
+    assert cw.workspace_status(ws) == 0
+    for s in range(n_seq):
+        if lens[s] == 0:
+            continue
+        r = slice(cu[s], cu[s + 1])
+        wo, wl = cw.cowa_fwd_paged(q[r], kp, vp, tab[s:s + 1], i32([0, lens[s]]), i32([starts[s]]), pat)
+        assert torch.equal(o[r], wo) and torch.equal(lse[:, r], wl), s
+
+
+def test_chunk_offsets_are_clamped(cuda_device):
+    """A malformed cu_seqlens: sequences in order, disjoint and inside the rows, as for cowa_fwd_varlen."""
+    Hq, Hkv, d, ps, n = 2, 1, 64, 16, 20
+    pat = cw.Pattern(8, 30, 320, 1)
+    kp, vp = (synth.cuda_normal_bf16((60, ps, Hkv, d), synth.seed_of(x, 97), cuda_device) for x in ("k", "v"))
+    q = synth.cuda_normal_bf16((100, Hq, d), synth.seed_of("q", 97), cuda_device)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=cuda_device)
+    tab = torch.arange(80, device=cuda_device).int().view(4, n) % 60
+    start = i32([10, 20, 30, 40])
+    run = lambda cu: cw.cowa_fwd_paged(q, kp, vp, tab, i32(cu), start, pat, out=torch.zeros_like(q),
+                                       lse=torch.zeros((Hq, 100), device=cuda_device))
+    for bad, good in (([-5, 30, 20, 70, 500], [0, 30, 30, 70, 100]), ([200, 1, 2, 3, 4], [100] * 5)):
+        (o, lse), (wo, wl) = run(bad), run(good)
+        assert torch.equal(o, wo) and torch.equal(lse, wl)
+
+
 def test_chunk_graph_stream_and_refusals(cuda_device):
     Hq, Hkv, d, ps, n = 4, 2, 64, 32, 16
     pat = cw.Pattern(16, 60, 512, 2)
