@@ -9,7 +9,7 @@
 //   * The work is the list of 64-position tiles of all (sequence, KV head) pairs, in that order.
 //     Lengths are known on the device only, and differ from 1 to the whole cache, so every CTA adds up
 //     the tile counts itself (integer arithmetic on pos) and takes an equal, contiguous share of the
-//     list, in which every pair counts kSegment tiles more than it has.  A pair that lies inside one CTA's share is finished there; one that several CTAs share
+//     list, in which every pair counts a few tiles more than it has (kSegmentOf).  A pair that lies inside one CTA's share is finished there; one that several CTAs share
 //     leaves fp32 partials (at most two per CTA), which a second kernel joins in order.
 //   * Where no CTA gets more than a few tiles anyway (one user, short caches), latency counts instead:
 //     a cluster of CTAs takes one pair, shares its tiles out evenly and joins its results through
@@ -42,9 +42,11 @@ constexpr int kTok = 64;                       // positions per tile
 constexpr int kBoxBytes = kTok * 128;          // 64 rows x 128 bytes
 constexpr float kRescale = 8.0f;               // lazy-rescale threshold, log2 units
 // What a segment costs besides its tiles (query rows, join of the warps, a start of the pipeline), in
-// tiles: 37 sequences of 1 to 32K positions, E4M3, took 2.0 us a segment and 1.0 us a tile, and the CTAs
-// that held nine segments of one tile each twice as long as the others.
-constexpr int kSegment = 2;
+// tiles: about 2.8 us beside 1.0 us a tile with E4M3 pages, whose tiles are half the bytes (37 sequences
+// of 1 to 32K positions: 22.7 us with 3, 24.4 with 2, 36 with 0), and 2 tiles with bf16 (37 of up to 1K:
+// 13.3 us with 2, 14.4 with 3).
+template <bool KV8>
+constexpr int kSegmentOf = KV8 ? 3 : 2;
 // Up to how many tiles a CTA may have for the cluster form: with 9.5 (8 sequences of 8K) it took 12.0 us
 // against the list's 13.8, with 12.6 (two of 32K) 14.1 against 13.2.
 constexpr int kClusterTiles = 10;
@@ -225,7 +227,7 @@ struct State {
 };
 
 // W places in G shares: the first `more` shares hold one place more than the `each` of the others.  A
-// pair of n > 0 tiles takes kSegment places and then one per tile.
+// pair of n > 0 tiles takes kSegmentOf places and then one per tile.
 struct Shares {
   int each, more;
   __device__ __forceinline__ int begin(int c) const { return c * each + imin(c, more); }
@@ -234,8 +236,6 @@ struct Shares {
     return w < big ? w / (each + 1) : more + (w - big) / each;
   }
 };
-
-__device__ __forceinline__ int places(int n) { return n > 0 ? n + kSegment : 0; }
 
 // ---- thread-block cluster: barriers of all its threads, and the other CTAs' shared memory
 __device__ __forceinline__ void cluster_sync() {
@@ -256,6 +256,8 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV8>::kCtas)
   using G_ = Geo<D, KV8>;
   constexpr int KS = D / 16;
   constexpr int kStages = G_::kStages;
+  constexpr int kSegment = kSegmentOf<KV8>;
+  auto places = [](int n) { return n > 0 ? n + kSegmentOf<KV8> : 0; };
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + G_::kOffBar);
   uint64_t* empty_bar = full_bar + kStages;
@@ -817,6 +819,7 @@ PagedPlan paged_decode_plan(const Pat& p, int B, int Hq, int Hkv, int d, bool kv
   const int64_t all = (cap + kTok - 1) / kTok + 2;  // (the ranges lie in the cache, and do not overlap)
   n = n < all ? n : all;
   PagedPlan plan{0, 0};
+  const int kSegment = kv8 ? kSegmentOf<true> : kSegmentOf<false>;
   if (n + kSegment > 0x7fffffff / pairs) return plan;  // the kernels count tiles in 32 bits
   plan.grid = (int)((n + kSegment) * pairs < most ? (n + kSegment) * pairs : most);
   const int k = pairs * 16 <= 148 ? 16 : (pairs * 8 <= most ? 8 : 4);
