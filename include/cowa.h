@@ -428,7 +428,8 @@ cowa_status cowa_decode_paged_fp8(const cowa_pattern* pat, int B, int H_q, int H
  * COWA_ERR_PAGE is reported as for cowa_decode_paged; other entries may hold anything.  Keys and values
  * below q_start[s] + len_s on mapped pages must be finite where they share a tile of 128 positions with
  * visible ones; what stands behind them is never used.  bf16 pages only.  The workspace's first 256 bytes must be zero before its first call. */
-size_t cowa_fwd_paged_workspace_size(const cowa_pattern* pat, int n_seq, int total, int H_q, int H_kv, int d);
+size_t cowa_fwd_paged_workspace_size(const cowa_pattern* pat, int n_seq, int total, int H_q, int H_kv, int d,
+                                     int max_pages, int page_size);
 cowa_status cowa_fwd_paged(const cowa_pattern* pat, int n_seq, int total, int H_q, int H_kv, int d,
                            const int32_t* cu_seqlens, const int32_t* q_start, cowa_tensor q, cowa_tensor k_pages,
                            cowa_tensor v_pages, cowa_page_table table, cowa_tensor o, float* lse, void* ws,

@@ -171,7 +171,7 @@ def lib() -> ctypes.CDLL:
     L.cowa_decode_paged_fp8_workspace_size.restype = sz
     L.cowa_decode_paged_fp8.argtypes = [P, i, i, i, i, vp, T, T, f, f, PT, vp, vp, vp, vp, sz, vp]
     L.cowa_decode_paged_fp8.restype = i
-    L.cowa_fwd_paged_workspace_size.argtypes = [P, i, i, i, i, i]
+    L.cowa_fwd_paged_workspace_size.argtypes = [P, i, i, i, i, i, i, i]
     L.cowa_fwd_paged_workspace_size.restype = sz
     L.cowa_fwd_paged.argtypes = [P, i, i, i, i, i, vp, vp, T, T, T, PT, T, vp, vp, sz, vp]
     L.cowa_fwd_paged.restype = i

@@ -400,7 +400,7 @@ PyObject* fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!lse) lse = &(ml = at::empty({Hq, total}, q.options().dtype(at::kFloat)));
     const int t = to_int(total), hq = to_int(Hq), di = to_int(d);
     if (!ws) {
-      const size_t bytes = lib.fwd_size(&pat, p.n_seq, t, hq, p.Hkv, di);
+      const size_t bytes = lib.fwd_size(&pat, p.n_seq, t, hq, p.Hkv, di, p.table.max_pages, p.table.page_size);
       ws = &(mw = at::zeros({(int64_t)std::max<size_t>(256, bytes)}, q.options().dtype(at::kByte)));
     }
     const int status = lib.fwd(&pat, p.n_seq, t, hq, p.Hkv, di, cu_p, start_p, rows(q, "q"), p.k, p.v, p.table,

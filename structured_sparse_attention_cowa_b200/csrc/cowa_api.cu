@@ -837,10 +837,13 @@ cowa_status decode_paged(const cowa_pattern* pat, int B, int Hq, int Hkv, int d,
 }
 }  // namespace
 
-size_t cowa_fwd_paged_workspace_size(const cowa_pattern* pat, int n_seq, int total, int H_q, int H_kv, int d) {
+size_t cowa_fwd_paged_workspace_size(const cowa_pattern* pat, int n_seq, int total, int H_q, int H_kv, int d,
+                                     int max_pages, int page_size) {
   Pat p;
-  if (n_seq < 1 || check_pattern(pat, H_kv, &p) != COWA_OK || check_heads(1, total, H_q, H_kv, d) != COWA_OK) return 0;
-  return kWsHeader;
+  if (n_seq < 1 || check_pattern(pat, H_kv, &p) != COWA_OK || check_heads(1, total, H_q, H_kv, d) != COWA_OK ||
+      max_pages < 1 || page_size < 8 || page_size % 8 != 0 || (int64_t)max_pages * page_size > (1 << 30))
+    return 0;
+  return kWsHeader + fwd_paged_bytes(fwd_paged_parts(p, n_seq, total, H_q, H_kv, d, max_pages, page_size), total, H_q, d);
 }
 
 cowa_status cowa_fwd_paged(const cowa_pattern* pat, int n_seq, int total, int Hq, int Hkv, int d,
@@ -857,7 +860,13 @@ cowa_status cowa_fwd_paged(const cowa_pattern* pat, int n_seq, int total, int Hq
   FwdArgs a;
   memset(&a, 0, sizeof(a));
   COWA_TRY(check_page_table(table, n_seq, &a.tab));
-  COWA_TRY(check_ws(ws, ws_bytes, cowa_fwd_paged_workspace_size(pat, n_seq, total, Hq, Hkv, d)));
+  a.parts = fwd_paged_parts(p, n_seq, total, Hq, Hkv, d, table.max_pages, table.page_size);
+  COWA_TRY(check_ws(ws, ws_bytes, kWsHeader + fwd_paged_bytes(a.parts, total, Hq, d)));
+  if (a.parts > 1) {
+    a.part_ml = reinterpret_cast<float2*>(reinterpret_cast<char*>(ws) + kWsHeader);
+    a.part_o = reinterpret_cast<float*>(reinterpret_cast<char*>(a.part_ml) +
+                                        align_up((size_t)a.parts * Hq * total * sizeof(float2), 256));
+  }
   a.pat = p; a.B = 1; a.Hq = Hq; a.Hkv = Hkv; a.d = d;
   a.Nq = total; a.Nk = total;
   a.varlen = 1; a.n_seq = n_seq; a.total = total; a.cu_seqlens = cu_seqlens;

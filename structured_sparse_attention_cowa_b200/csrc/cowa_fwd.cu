@@ -19,7 +19,8 @@
 // 128 rows, and fetches the boxes that some row of the query tile sees.  V rows that are not fetched,
 // or lie past the last key, are zeroed (their P is 0, but 0 times what memory holds may be NaN).  The
 // CTAs come heaviest first over all sequences (see find_chunk), and those with a single head, of an
-// odd group, last.
+// odd group, last.  Where there are too few CTAs for the GPU (a short chunk behind a long prefix),
+// several share the key tiles of one (a.parts) and leave fp32 results that a second kernel joins.
 // Registers: the kernel is compiled for 168 per thread (384 * 168 = 64512 at launch); the two
 // softmax warpgroups then raise theirs to 216 and the third lowers to 72
 // (2*128*216 + 128*72 = 64512), so a whole 128-column score row stays in registers.  The
@@ -149,6 +150,25 @@ __device__ __forceinline__ Chunk find_chunk(const FwdArgs& a, int rank) {
   return Chunk{-1, 0, 0, 0, 0};
 }
 
+// Part `part` of `parts` of a tile list, in order (parts differ by at most one tile; some may be empty).
+__device__ __forceinline__ Tiles part_of(const Tiles& all, int part, int parts) {
+  if (parts == 1) return all;
+  const int first = (int)((int64_t)all.count * part / parts), last = (int)((int64_t)all.count * (part + 1) / parts);
+  Range r[3];
+  int before = 0;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const int len = all.r[i].hi - all.r[i].lo;
+    const int lo = imax(first - before, 0), hi = imin(last - before, len);
+    r[i] = hi > lo ? Range{all.r[i].lo + lo, all.r[i].lo + hi} : Range{0, 0};
+    before += len;
+  }
+  Tiles T;
+  T.n = merge3(r[0], r[1], r[2], T.r);
+  T.count = (T.r[0].hi - T.r[0].lo) + (T.r[1].hi - T.r[1].lo) + (T.r[2].hi - T.r[2].lo);
+  return T;
+}
+
 // bits lo .. hi - 1 of a word (either may lie outside it)
 __device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
   lo = imax(lo, 0);
@@ -182,14 +202,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cowa_fwd_kernel(const __grid_c
   const int npair = (grp + 1) >> 1;
   const int per_i = a.B * a.Hkv * npair;
   int i, row0 = 0, Nq = a.Nq, Nk = a.Nk, q_off = a.q_off;  // row0: first row of the sequence
-  int pg_seq = 0;
+  int pg_seq = 0, part = 0;
   int pair, g, b = 0;
   if constexpr (PAGED) {
     // (set up while the kernel before it in the stream ran; waits for that one's results here)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     __shared__ Chunk chunk;
     const int whole = grp >> 1, bound = (int)packed_tiles_bound(a.total, a.n_seq), n_whole = bound * a.Hkv * whole;
-    int rank = blockIdx.x;
+    int rank = blockIdx.x / a.parts;
+    part = blockIdx.x % a.parts;
     if (rank < n_whole) {
       pair = rank % whole; rank /= whole;
     } else {  // the odd heads, half as much work each
@@ -234,7 +255,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cowa_fwd_kernel(const __grid_c
   const int t0 = q_off + i * kBM, t1 = imin(q_off + Nq, t0 + kBM);
   const Range iv = interval_of(a.pat, g);
   // (a paged sequence longer than its cache: its last rows see the keys that there are)
-  const Tiles T = plan_tiles(a.pat, iv, t0, PAGED ? imin(t1, Nk) : t1);
+  const Tiles T = PAGED ? part_of(plan_tiles(a.pat, iv, t0, imin(t1, Nk)), part, a.parts) : plan_tiles(a.pat, iv, t0, t1);
 
   uint8_t* sQ = smem + Geo::kOffQ;
   uint8_t* sRing = smem + Geo::kOffRing;
@@ -643,12 +664,26 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cowa_fwd_kernel(const __grid_c
       const float l = la + lb;
       // ---- epilogue
       if constexpr (PAGED) {
-        if (ntiles == 0 && t < t1 && k < (has1 ? 2 : 1)) {  // a query tile whose band begins past the cache
-          __nv_bfloat16* z = reinterpret_cast<__nv_bfloat16*>(a.o) + (size_t)(row0 + t - q_off) * a.o_st + (size_t)(h0 + k) * a.o_sh;
-          for (int c = 0; c < D / 8; ++c) reinterpret_cast<uint4*>(z)[c] = make_uint4(0, 0, 0, 0);
-          a.lse[(size_t)(h0 + k) * a.total + row0 + t - q_off] = -INFINITY;
+        if (ntiles == 0 && t < t1 && k < (has1 ? 2 : 1)) {  // no keys: an empty part, or past the cache and its band
+          const size_t row = (size_t)(h0 + k) * a.total + row0 + t - q_off;
+          if (a.parts > 1) {
+            a.part_ml[(size_t)part * a.Hq * a.total + row] = make_float2(-INFINITY, 0.f);
+          } else {
+            __nv_bfloat16* z = reinterpret_cast<__nv_bfloat16*>(a.o) + (size_t)(row0 + t - q_off) * a.o_st + (size_t)(h0 + k) * a.o_sh;
+            for (int c = 0; c < D / 8; ++c) reinterpret_cast<uint4*>(z)[c] = make_uint4(0, 0, 0, 0);
+            a.lse[row] = -INFINITY;
+          }
         }
       }
+      // (a.parts > 1: the part's running max and sum, the sum -1 for a bad page, and its O as it stands)
+      auto part_row = [&](int h) { return ((size_t)part * a.Hq + h) * a.total + row0 + t - q_off; };
+      auto put_part = [&](int h, int c, const uint32_t* x) {  // 32 columns of O
+        float4* dst = reinterpret_cast<float4*>(a.part_o + part_row(h) * D + c * 32);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          dst[e] = make_float4(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 1]), __uint_as_float(x[4 * e + 2]),
+                               __uint_as_float(x[4 * e + 3]));
+      };
       const int rl = t - q_off;  // query row within the call's (or the sequence's) rows
       __nv_bfloat16* orow = reinterpret_cast<__nv_bfloat16*>(a.o) + (size_t)b * a.o_sb + (size_t)(row0 + rl) * a.o_st +
                             (size_t)h0 * a.o_sh;
@@ -659,16 +694,22 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cowa_fwd_kernel(const __grid_c
         if (ok && ntiles > 0 && ptx::mbar_wait_warp(&o_done[k], 0, &abort_flag, a.status)) {
           ptx::tc_fence_after();
           // (a paged row may see nothing, or its query tile a bad page)
-          const bool none = PAGED && (m_used == -INFINITY || *reinterpret_cast<volatile int*>(&bad_page));
+          const bool bad = PAGED && *reinterpret_cast<volatile int*>(&bad_page);
+          const bool none = PAGED && (m_used == -INFINITY || bad);
           const float inv = 1.f / l;
-          if (t < t1)
-            a.lse[lse_h0 + k * lse_step] = none ? -INFINITY : (m_used + log2f(l)) * 0.69314718055994530942f;
+          const bool partial = PAGED && a.parts > 1;
+          if (t < t1) {
+            if (partial) a.part_ml[part_row(h0 + k)] = make_float2(m_used, bad ? -1.f : l);
+            else a.lse[lse_h0 + k * lse_step] = none ? -INFINITY : (m_used + log2f(l)) * 0.69314718055994530942f;
+          }
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
             uint32_t ov[32];
             ptx::tmem_ld32(o_tm + c * 32, ov);  // warp-collective: every lane loads, valid rows store
             ptx::tmem_wait_ld();
-            if (t < t1) {
+            if (partial) {
+              if (t < t1) put_part(h0 + k, c, ov);
+            } else if (t < t1) {
 #pragma unroll
               for (int c8 = 0; c8 < 4; ++c8) {
                 uint32_t w[4];
@@ -700,10 +741,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cowa_fwd_kernel(const __grid_c
         const float f0 = m_used == -INFINITY ? 0.f : ptx::ex2(m_used - m);
         const float f1 = m1 == -INFINITY ? 0.f : ptx::ex2(m1 - m);
         const float lt = l * f0 + l1 * f1;
-        const bool none = PAGED && (m == -INFINITY || *reinterpret_cast<volatile int*>(&bad_page));
-        const float inv = 1.f / lt, g0 = f0 * inv, g1 = f1 * inv;
+        const bool bad = PAGED && *reinterpret_cast<volatile int*>(&bad_page);
+        const bool none = PAGED && (m == -INFINITY || bad), partial = PAGED && a.parts > 1;
+        const float inv = partial ? 1.f : 1.f / lt, g0 = f0 * inv, g1 = f1 * inv;
         const bool two = ntiles > 1;  // slot 1 has tiles (uniform over the CTA)
-        if (t < t1) a.lse[lse_h0] = none ? -INFINITY : (m + log2f(lt)) * 0.69314718055994530942f;
+        if (t < t1 && partial) a.part_ml[part_row(h0)] = make_float2(m, bad ? -1.f : lt);
+        else if (t < t1) a.lse[lse_h0] = none ? -INFINITY : (m + log2f(lt)) * 0.69314718055994530942f;
         const uint32_t o1_tm = lane_base + Geo::kColO + D;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
@@ -711,7 +754,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cowa_fwd_kernel(const __grid_c
           ptx::tmem_ld32(o_tm + c * 32, ov);  // warp-collective: every lane loads, valid rows store
           if (two) ptx::tmem_ld32(o1_tm + c * 32, ow);
           ptx::tmem_wait_ld();
-          if (t < t1) {
+          if (partial) {
+            if (t < t1) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                ov[e] = __float_as_uint(__uint_as_float(ov[e]) * g0 + (two ? __uint_as_float(ow[e]) * g1 : 0.f));
+              put_part(h0, c, ov);
+            }
+          } else if (t < t1) {
 #pragma unroll
             for (int c8 = 0; c8 < 4; ++c8) {
               uint32_t w[4];
@@ -759,6 +809,62 @@ __global__ void seq_table_kernel(const int32_t* cu, int n_seq, int total, int32_
   tab[n_seq] = off;
 }
 
+// Joins the parts of each query row: one warp per (row, head).  Rows outside the sequences stay as they are.
+template <int D>
+__global__ void __launch_bounds__(256) fwd_join_kernel(const __grid_constant__ FwdArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31;
+  // the sequences' rows: from the first offset to the largest (see find_chunk)
+  __shared__ int rows_end;
+  const int rows_begin = imin(imax(a.cu_seqlens[0], 0), a.total);
+  if (threadIdx.x == 0) rows_end = rows_begin;
+  __syncthreads();
+  int most = rows_begin;
+  for (int i = threadIdx.x; i <= a.n_seq; i += blockDim.x) most = imax(most, imin(a.cu_seqlens[i], a.total));
+  most = (int)__reduce_max_sync(0xffffffffu, (unsigned)most);
+  if (lane == 0) atomicMax(&rows_end, most);
+  __syncthreads();
+  const int64_t at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (at >= (int64_t)a.Hq * a.total) return;
+  const int h = (int)(at / a.total), row = (int)(at - (int64_t)h * a.total);
+  if (row < rows_begin || row >= rows_end) return;
+  const size_t step = (size_t)a.Hq * a.total;  // from part to part
+  float2 ml = lane < a.parts ? a.part_ml[lane * step + at] : make_float2(-INFINITY, 0.f);
+  const bool bad = __any_sync(0xffffffffu, ml.y < 0.f);
+  float m = ml.x;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float f = ml.x == -INFINITY ? 0.f : ptx::ex2(ml.x - m);
+  float l = f * ml.y, acc[E] = {};
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  const float* p = a.part_o + at * D + lane * E;
+#pragma unroll 4
+  for (int i = 0; i < a.parts; ++i) {
+    const float w = __shfl_sync(0xffffffffu, f, i);
+    if (w == 0.f) continue;  // (an empty part wrote no O)
+    float x[E];
+    if constexpr (E == 4) {
+      const float4 v = *reinterpret_cast<const float4*>(p + i * step * D);
+      x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+    } else {
+      const float2 v = *reinterpret_cast<const float2*>(p + i * step * D);
+      x[0] = v.x; x[1] = v.y;
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] += w * x[e];
+  }
+  const bool none = bad || m == -INFINITY;
+  uint32_t w[E / 2];
+#pragma unroll
+  for (int e = 0; e < E / 2; ++e) w[e] = none ? 0u : ptx::pack_bf16(acc[2 * e] / l, acc[2 * e + 1] / l);
+  __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(a.o) + row * a.o_st + h * a.o_sh + lane * E;
+  if constexpr (E == 4) *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[1]);
+  else *reinterpret_cast<uint32_t*>(o) = w[0];
+  if (lane == 0) a.lse[at] = none ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
+}
+
 template <int D, bool PAGED>
 cudaError_t launch_fwd_d(const FwdArgs& a, cudaStream_t s) {
   using Geo = FwdGeom<D>;
@@ -784,13 +890,17 @@ cudaError_t launch_fwd_d(const FwdArgs& a, cudaStream_t s) {
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)nblk);
+    cfg.gridDim = dim3((unsigned)(nblk * a.parts));
     cfg.blockDim = dim3(kFwdThreads);
     cfg.dynamicSmemBytes = Geo::kSmem;
     cfg.stream = s;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, a);
+    if ((e = cudaLaunchKernelEx(&cfg, kern, a)) != cudaSuccess || a.parts == 1) return e;
+    cfg.gridDim = dim3((unsigned)(((int64_t)a.Hq * a.total + 7) / 8));
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, fwd_join_kernel<D>, a);
   }
   if (a.varlen) {
     if ((e = launch_seq_table(a.cu_seqlens, a.n_seq, a.total, a.seq_tab, s)) != cudaSuccess) return e;
@@ -804,6 +914,32 @@ cudaError_t launch_fwd_d(const FwdArgs& a, cudaStream_t s) {
 cudaError_t launch_seq_table(const int32_t* cu_seqlens, int n_seq, int total, int32_t* tab, cudaStream_t s) {
   seq_table_kernel<<<1, 32, 0, s>>>(cu_seqlens, n_seq, total, tab);
   return cudaGetLastError();
+}
+
+// Parts that the key tiles of a paged call's CTAs are cut into: as many as leave each CTA two tiles or more
+// and all CTAs one SM each, with at most kPartBytes of partial results (which cost their writing and
+// reading).  1: no cut.
+int fwd_paged_parts(const Pat& p, int n_seq, int total, int Hq, int Hkv, int d, int max_pages, int page_size) {
+  constexpr int64_t kPartBytes = 8 << 20;
+  const int64_t cap = (int64_t)max_pages * page_size, R = (int64_t)p.T - p.S;
+  const int64_t wide = R > 0 ? (R + p.H - 1) / p.H : 0;
+  auto tiles = [&](int64_t n) { return n > 0 ? ((n < cap ? n : cap) + kBN - 1) / kBN + 1 : 0; };
+  int64_t n = tiles(p.S) + tiles(wide) + tiles((int64_t)p.L + kBM);
+  const int64_t all = (cap + kBN - 1) / kBN;
+  n = n < all ? n : all;
+  const int64_t ctas = packed_tiles_bound(total, n_seq) * Hkv * ((Hq / Hkv + 1) / 2);
+  int64_t parts = 148 / ctas;
+  if (parts > n / 2) parts = n / 2;
+  const int64_t bytes = (int64_t)Hq * total * (d + 2) * sizeof(float);
+  if (parts > kPartBytes / bytes) parts = kPartBytes / bytes;
+  if (parts > 32) parts = 32;  // (a lane each when they are joined)
+  return parts < 1 ? 1 : (int)parts;
+}
+
+size_t fwd_paged_bytes(int parts, int total, int Hq, int d) {
+  if (parts == 1) return 0;
+  const size_t rows = (size_t)parts * Hq * total;
+  return align_up(rows * sizeof(float2), 256) + rows * d * sizeof(float);
 }
 
 cudaError_t launch_fwd(const FwdArgs& a, cudaStream_t s) {

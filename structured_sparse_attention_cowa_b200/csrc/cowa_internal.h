@@ -144,6 +144,11 @@ struct FwdArgs {
   // paged != 0 (a packed batch): keys and values in pages (tm_k, tm_v over the pools), sequence s's
   // query rows at positions q_start[s]..
   int paged, box_rows;
+  // parts > 1: each CTA's key tiles are cut into so many parts, whose results go to part_ml (running max
+  // in log2 units and sum, [parts][Hq][total]) and part_o ([parts][Hq][total][d])
+  int parts;
+  float2* part_ml;
+  float* part_o;
   PageTab tab;
   const int32_t* q_start;
   void* o;
@@ -154,6 +159,8 @@ struct FwdArgs {
   CUtensorMap tm_q, tm_k, tm_v;
 };
 cudaError_t launch_fwd(const FwdArgs& a, cudaStream_t s);
+int fwd_paged_parts(const Pat& p, int n_seq, int total, int Hq, int Hkv, int d, int max_pages, int page_size);
+size_t fwd_paged_bytes(int parts, int total, int Hq, int d);
 
 // ---- packed variable-length batches ----
 // Bytes of the sequence table (3 n_seq + 1 int32, 256-aligned) and the kernel that writes it

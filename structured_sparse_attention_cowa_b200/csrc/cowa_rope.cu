@@ -23,7 +23,6 @@
 namespace cowa {
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kMaxTok = 8;  // tokens per block, at most
 
 // How a row is cut into units of work:
@@ -34,11 +33,16 @@ constexpr int kMaxTok = 8;  // tokens per block, at most
 enum { kSplit, kInter, kAny };
 // What becomes of the rows: rotated copies; bf16 pages; pages of E4M3 codes
 enum { kTurn, kPagesBf16, kPagesE4m3 };
+// Threads of a block.  (E4M3 pages, where the angles in 64 bits take long: smaller blocks wait for them
+// in smaller numbers, 41.4 us against 43.3 for 8K tokens; the others lose 2% that way.)
+template <int MODE>
+constexpr int kThreadsOf = MODE == kPagesE4m3 ? 128 : 256;
 
 // bytes of a block's fp32 cos and sin tables (whole units of 8 pairs), and of all its shared memory
-__host__ __device__ inline size_t table_bytes(int tok, int half) { return (size_t)tok * ((half + 7) / 8) * 64; }
+__host__ __device__ inline int whole_pairs(int half) { return (half + 7) / 8 * 8; }
+__host__ __device__ inline size_t table_bytes(int tok, int half) { return (size_t)tok * whole_pairs(half) * 8; }
 inline size_t smem_bytes(int mode, int tok, int half, int Hk) {
-  return table_bytes(tok, half) + (mode == kPagesE4m3 ? (size_t)tok * half * 16 : 0) + (mode == kTurn ? 0 : (size_t)tok * Hk * 16);
+  return table_bytes(tok, half) + (mode == kPagesE4m3 ? (size_t)tok * whole_pairs(half) * 16 : 0) + (mode == kTurn ? 0 : (size_t)tok * Hk * 16);
 }
 
 struct Row {
@@ -72,16 +76,18 @@ __device__ __forceinline__ uint2 codes8(const float* x, float inv) {
 }
 
 template <int MODE, int CUT>
-__global__ void __launch_bounds__(kThreads, 4) turn_kernel(const __grid_constant__ RopeArgs a, int tok_per_block) {
+__global__ void __launch_bounds__(kThreadsOf<MODE>, 1024 / kThreadsOf<MODE>)
+    turn_kernel(const __grid_constant__ RopeArgs a, int tok_per_block) {
+  constexpr int kThreads = kThreadsOf<MODE>;
   // cos and sin of the block's tokens.  kSplit and kInter: [token][piece][unit] of float4, the pieces
   // being the unit's 8 cosines and then its 8 sines, so that neighbouring units are neighbours in
   // memory.  kAny: [token][pair] of (cos, sin).
   extern __shared__ __align__(16) unsigned char smem[];
   float* tab = reinterpret_cast<float*>(smem);
-  // E4M3 keys: cos and sin in 64 bits, [token][pair]
+  // E4M3 keys: cos and sin in 64 bits, [token][pair of the unit][unit] (kAny: [token][pair])
   double2* tab64 = reinterpret_cast<double2*>(smem + table_bytes(tok_per_block, a.half));
   // element offset of each (token, KV head)'s key and value row in the pools, -1 for none
-  longlong2* dst = reinterpret_cast<longlong2*>(tab64 + (MODE == kPagesE4m3 ? tok_per_block * a.half : 0));
+  longlong2* dst = reinterpret_cast<longlong2*>(tab64 + (MODE == kPagesE4m3 ? tok_per_block * whole_pairs(a.half) : 0));
   __shared__ int live[kMaxTok];
   __shared__ __align__(16) __nv_bfloat16 stage[CUT == kAny ? kThreads * 8 : 8];
 
@@ -183,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 4) turn_kernel(const __grid_constant
       sincospi(2.0 * turns, &s64, &c64);
       s64 *= (double)a.sin_scale;
       c64 *= (double)a.scale;
-      tab64[x] = make_double2(c64, s64);
+      tab64[CUT == kAny ? x : (tk * 8 + i % 8) * rot_units + i / 8] = make_double2(c64, s64);
       s = (float)s64;
       c = (float)c64;
     } else {
@@ -256,13 +262,14 @@ __global__ void __launch_bounds__(kThreads, 4) turn_kernel(const __grid_constant
         }
       } else if (u < rot_units) {
         if (exact) {
-          const double2* cs = tab64 + x.tok * half + 8 * u;
+          const double2* cs = tab64 + x.tok * 8 * rot_units + u;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             if (CUT == kInter && j >= 4 && 8 * u + j >= half) break;
             float& ea = CUT == kSplit ? lo[j] : (j < 4 ? lo[2 * j] : hi[2 * j - 8]);
             float& eb = CUT == kSplit ? hi[j] : (j < 4 ? lo[2 * j + 1] : hi[2 * j - 7]);
-            const double xa = ea, xb = eb, c = cs[j].x, s = cs[j].y;
+            const double2 t = cs[j * rot_units];
+            const double xa = ea, xb = eb, c = t.x, s = t.y;
             ea = (float)fma(xa, c, -(xb * s));
             eb = (float)fma(xb, c, xa * s);
           }
@@ -337,7 +344,7 @@ cudaError_t launch_turn(const RopeArgs& a, cudaStream_t s) {
                                                                 : kAny;
   const int units = cut == kSplit ? a.half / 8 + (a.d - rd) / 8 : (cut == kInter ? a.d / 16 : a.d / 8);
   const int heads = a.Hq + (MODE == kTurn ? 1 : 2) * a.Hk;
-  const int lanes = kThreads / units;
+  const int lanes = kThreadsOf<MODE> / units;
   // tokens per block: enough rows to fill its threads, but no fewer blocks than the SMs can hold
   int tok = 1;
   while (tok < kMaxTok && (tok * heads < lanes || (a.M + 2 * tok - 1) / (2 * tok) >= 148 * 8) &&
@@ -351,7 +358,7 @@ cudaError_t launch_turn(const RopeArgs& a, cudaStream_t s) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kThreadsOf<MODE>);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = at;

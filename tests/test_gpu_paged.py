@@ -572,7 +572,7 @@ def test_chunks_match_oracle(cuda_device, Hq, Hkv, d, pat, ps, n, per_head, layo
     q64, q = host_and_device((total, Hq, d), "q", cuda_device, 92)
     i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=cuda_device)
     cu = np.cumsum([0] + lens)
-    ws = torch.zeros(cw.lib().cowa_fwd_paged_workspace_size(ctypes.byref(pat.c()), B, total, Hq, Hkv, d),
+    ws = torch.zeros(cw.lib().cowa_fwd_paged_workspace_size(ctypes.byref(pat.c()), B, total, Hq, Hkv, d, n, ps),
                      dtype=torch.uint8, device=cuda_device)
     out = torch.full((total, Hq, d), 3.0, dtype=torch.bfloat16, device=cuda_device)
     lse = torch.full((Hq, total), 5.0, device=cuda_device)
@@ -586,9 +586,10 @@ def test_chunks_match_oracle(cuda_device, Hq, Hkv, d, pat, ps, n, per_head, layo
 
 
 def test_chunks_equal_the_contiguous_forward(cuda_device):
-    """Over pages of 128 in order the tiles and their masks are those of cowa_fwd_chunk: the same bits."""
-    N, Hq, Hkv, d, start = 1100, 10, 2, 128, 640
-    pat = cw.Pattern(64, 300, 1100, 2)
+    """Over pages of 128 in order the tiles and their masks are those of cowa_fwd_chunk: the same bits
+    (with enough heads that the key tiles are not cut into parts)."""
+    N, Hq, Hkv, d, start = 1100, 40, 8, 128, 640
+    pat = cw.Pattern(64, 300, 1100, 8)
     k, v = (synth.cuda_normal_bf16((1, 1152, Hkv, d), synth.seed_of(x, 93), cuda_device) for x in ("k", "v"))
     q = synth.cuda_normal_bf16((1, N - start, Hq, d), synth.seed_of("q", 93), cuda_device)
     wo, wl = cw.cowa_fwd_chunk(q, k, v, pat, start, n_k=N)
@@ -617,7 +618,7 @@ def test_chunk_bad_entries_and_overlong_sequences(cuda_device, Hq, ps):
     cu = np.cumsum([0] + lens)
     q64, q = host_and_device((int(cu[-1]), Hq, d), "q", cuda_device, 94)
     i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=cuda_device)
-    ws = torch.zeros(4096, dtype=torch.uint8, device=cuda_device)
+    ws = torch.zeros(1 << 23, dtype=torch.uint8, device=cuda_device)
     o, lse = cw.cowa_fwd_paged(q, kd, vd, torch.from_numpy(tab).to(cuda_device), i32(cu.tolist()),
                                i32([s for s, _ in chunks]), pat, workspace=ws)
     assert cw.workspace_status(ws) == 8 and cw.workspace_status(ws) == 0
@@ -638,28 +639,64 @@ def test_chunk_bad_entries_and_overlong_sequences(cuda_device, Hq, ps):
 
 @pytest.mark.parametrize("n_seq", [33, 64, 65, 150])
 def test_chunks_of_many_sequences(cuda_device, n_seq):
-    """However many sequences a call has (their tiles are dealt out in other orders then), each gets the
-    bits of a call of its own; some are empty, some a single row."""
+    """However many sequences a call has (their tiles are dealt out in other orders then), some of them
+    empty, some a single row."""
     Hq, Hkv, d, ps, n = 3, 1, 64, 16, 40
     pat = cw.Pattern(30, 100, 640, 1)
     rng = np.random.default_rng(n_seq)
     lens = [int(x) for x in rng.choice([0, 0, 1, 2, 17, 128, 129, 300], n_seq)]
     starts = [int(rng.integers(0, n * ps - x + 1)) for x in lens]
-    kp, vp = (synth.cuda_normal_bf16((500, ps, Hkv, d), synth.seed_of(x, 96), cuda_device) for x in ("k", "v"))
-    tab = torch.from_numpy(rng.integers(0, 500, (n_seq, n)).astype(np.int32)).to(cuda_device)
+    (k64, kp), (v64, vp) = (host_and_device((500, ps, Hkv, d), x, cuda_device, 96) for x in ("k", "v"))
+    tabh = rng.integers(0, 500, (n_seq, n)).astype(np.int32)
+    tab = torch.from_numpy(tabh).to(cuda_device)
     total = max(1, sum(lens))
-    q = synth.cuda_normal_bf16((total, Hq, d), synth.seed_of("q", 96), cuda_device)
+    q64, q = host_and_device((total, Hq, d), "q", cuda_device, 96)
     i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=cuda_device)
     cu = np.cumsum([0] + lens)
-    ws = torch.zeros(256, dtype=torch.uint8, device=cuda_device)
+    ws = torch.zeros(1 << 23, dtype=torch.uint8, device=cuda_device)
     o, lse = cw.cowa_fwd_paged(q, kp, vp, tab, i32(cu.tolist()), i32(starts), pat, workspace=ws)
     assert cw.workspace_status(ws) == 0
     for s in range(n_seq):
         if lens[s] == 0:
             continue
         r = slice(cu[s], cu[s + 1])
-        wo, wl = cw.cowa_fwd_paged(q[r], kp, vp, tab[s:s + 1], i32([0, lens[s]]), i32([starts[s]]), pat)
-        assert torch.equal(o[r], wo) and torch.equal(lse[:, r], wl), s
+        k, _ = orp.gather_pages(k64, tabh[s:s + 1], starts[s] + lens[s])
+        v, _ = orp.gather_pages(v64, tabh[s:s + 1], starts[s] + lens[s])
+        assert_chunk(o[r], lse[:, r], q64[r], k[0], v[0], starts[s], pat)
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,rows", [(5, 1, 128, 3), (4, 2, 64, 130), (8, 1, 128, 1)])
+def test_short_chunks_behind_long_prefixes(cuda_device, Hq, Hkv, d, rows):
+    """A few rows against thousands of keys: the key tiles are cut into parts that several CTAs take."""
+    ps, n = 64, 100
+    pat = cw.Pattern(100, 900, 6400, Hkv)
+    rng = np.random.default_rng(98)
+    tab, n_pages = make_table(rng, 2, n)
+    (k64, kp), (v64, vp) = (host_and_device((n_pages, ps, Hkv, d), x, cuda_device, 98) for x in ("k", "v"))
+    starts, lens = [6000, 77], [rows, 2 * rows]
+    total = sum(lens) + 4
+    q64, q = host_and_device((total, Hq, d), "q", cuda_device, 98)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=cuda_device)
+    size = lambda pages: cw.lib().cowa_fwd_paged_workspace_size(ctypes.byref(pat.c()), 2, total, Hq, Hkv, d, pages, ps)
+    assert size(n) > 256 + 8 * total * Hq * d > size(2)  # (the cut needs room for its parts)
+    out, lse = torch.full_like(q, 3.0), torch.full((Hq, total), 5.0, device=cuda_device)
+    ws = torch.zeros(size(n), dtype=torch.uint8, device=cuda_device)
+    run = lambda: cw.cowa_fwd_paged(q, kp, vp, torch.from_numpy(tab).to(cuda_device), i32([2, 2 + rows, 2 + 3 * rows]),
+                                    i32(starts), pat, out=out, lse=lse, workspace=ws)
+    run()
+    assert cw.workspace_status(ws) == 0
+    first = out.clone(), lse.clone()
+    run()
+    assert torch.equal(first[0], out) and torch.equal(first[1], lse)
+    for r in (slice(0, 2), slice(2 + 3 * rows, total)):  # rows of no sequence
+        assert (out[r] == 3.0).all() and (lse[:, r] == 5.0).all()
+    row = 2
+    for b in range(2):
+        k, _ = orp.gather_pages(k64, tab[b:b + 1], starts[b] + lens[b])
+        v, _ = orp.gather_pages(v64, tab[b:b + 1], starts[b] + lens[b])
+        r = slice(row, row + lens[b])
+        assert_chunk(out[r], lse[:, r], q64[r], k[0], v[0], starts[b], pat)
+        row += lens[b]
 
 
 def test_chunk_offsets_are_clamped(cuda_device):
@@ -691,7 +728,7 @@ def test_chunk_graph_stream_and_refusals(cuda_device):
     o, lse = cw.cowa_fwd_paged(q, kp, vp, tab, cu, start, pat, stream=side)
     side.synchronize()
     assert torch.equal(o, wo) and torch.equal(lse, wl)
-    ws = torch.zeros(4096, dtype=torch.uint8, device=cuda_device)
+    ws = torch.zeros(1 << 23, dtype=torch.uint8, device=cuda_device)
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
         cw.cowa_fwd_paged(q, kp, vp, tab, cu, start, pat, out=o, lse=lse, workspace=ws)

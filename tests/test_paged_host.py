@@ -97,7 +97,7 @@ def test_chunk_refusals(status, change):
              kp=T(), vp=T(), tab=table(), o=T(), lse=0x30000, ws=0x40000, less=0)
     a.update(change)
     L = cw.lib()
-    n = L.cowa_fwd_paged_workspace_size(ctypes.byref(cw.Pattern(64, 100, 1024, 4).c()), 3, 500, 8, 4, 128)
+    n = L.cowa_fwd_paged_workspace_size(ctypes.byref(cw.Pattern(64, 100, 1024, 4).c()), 3, 500, 8, 4, 128, 64, 16)
     assert L.cowa_fwd_paged(ctypes.byref(a["pat"].c()), a["n_seq"], a["total"], a["Hq"], a["Hkv"], a["d"], a["cu"],
                             a["start"], a["q"], a["kp"], a["vp"], a["tab"], a["o"], a["lse"], a["ws"], n - a["less"],
                             None) == status
