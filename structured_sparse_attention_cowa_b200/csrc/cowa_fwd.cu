@@ -916,11 +916,12 @@ cudaError_t launch_seq_table(const int32_t* cu_seqlens, int n_seq, int total, in
   return cudaGetLastError();
 }
 
-// Parts that the key tiles of a paged call's CTAs are cut into: as many as leave each CTA two tiles or more
-// and all CTAs one SM each, with at most kPartBytes of partial results (which cost their writing and
-// reading).  1: no cut.
+// Parts that the key tiles of a paged call's CTAs are cut into: as many as leave every CTA a tile and an SM
+// of its own, with at most kPartBytes of partial results (which cost their writing and reading).  1: no cut.
+// 16 rows behind 32K keys (40/8 heads) 110 -> 32 us, 300 rows behind 4K (4/1 heads) 69 -> 24, 60 behind 1K
+// (2/2 heads, d = 64) 17.8 -> 12.4 (15.0 with three tiles a part at least).
 int fwd_paged_parts(const Pat& p, int n_seq, int total, int Hq, int Hkv, int d, int max_pages, int page_size) {
-  constexpr int64_t kPartBytes = 8 << 20;
+  constexpr int64_t kPartBytes = 12 << 20;
   const int64_t cap = (int64_t)max_pages * page_size, R = (int64_t)p.T - p.S;
   const int64_t wide = R > 0 ? (R + p.H - 1) / p.H : 0;
   auto tiles = [&](int64_t n) { return n > 0 ? ((n < cap ? n : cap) + kBN - 1) / kBN + 1 : 0; };
@@ -929,7 +930,7 @@ int fwd_paged_parts(const Pat& p, int n_seq, int total, int Hq, int Hkv, int d, 
   n = n < all ? n : all;
   const int64_t ctas = packed_tiles_bound(total, n_seq) * Hkv * ((Hq / Hkv + 1) / 2);
   int64_t parts = 148 / ctas;
-  if (parts > n / 2) parts = n / 2;
+  if (parts > n) parts = n;
   const int64_t bytes = (int64_t)Hq * total * (d + 2) * sizeof(float);
   if (parts > kPartBytes / bytes) parts = kPartBytes / bytes;
   if (parts > 32) parts = 32;  // (a lane each when they are joined)
