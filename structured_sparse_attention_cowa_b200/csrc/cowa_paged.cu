@@ -288,12 +288,14 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV8>::kCtas)
   // ---- this CTA's share: places [w0, w1) of the list, the first pair of it and that pair's place
   int w0, w1, first_item, first_place;
   Shares sh{0, 0};
+  Pair own;  // (CL) the one pair there is
   if constexpr (CL) {
     first_item = c / a.cluster;
-    const int rank = c - first_item * a.cluster, n = pair_of(a, first_item).n;
-    // (in 64 bits: a pair may have 2^24 tiles)
-    w0 = (int)((int64_t)n * rank / a.cluster);
-    w1 = (int)((int64_t)n * (rank + 1) / a.cluster);
+    const int rank = c - first_item * a.cluster;
+    own = pair_of(a, first_item);
+    // (a.cluster is 4, 8 or 16, and a pair has at most kClusterTiles tiles for each CTA)
+    w0 = own.n * rank / a.cluster;
+    w1 = own.n * (rank + 1) / a.cluster;
     first_place = -kSegment;  // place w is tile w
     __syncthreads();
   } else {
@@ -364,9 +366,12 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV8>::kCtas)
     if (w0 < w1 && pool_ok) {
       const int nbox = kTok / a.box_rows;
       Window win;
-      win.fill(a, first_item, n_items);
       int item = first_item, place = first_place;
-      Pair s = win.get(a, item, n_items);
+      Pair s = own;
+      if constexpr (!CL) {
+        win.fill(a, item, n_items);
+        s = win.get(a, item, n_items);
+      }
       // this CTA's tiles of the pair at hand: [off, lim)
       int off = imax(0, w0 - place - kSegment), lim = imin(s.n, w1 - place - kSegment);
       // Box `lane` of a tile: the page it lies in.  The load is unconditional, at a clamped place, and
@@ -378,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV8>::kCtas)
       auto look = [&](Look& k) -> bool {
         while (off >= lim) {
           place += places(s.n);
-          if (place >= w1) return false;
+          if (CL || place >= w1) return false;
           s = win.get(a, ++item, n_items);
           off = 0;
           lim = imin(s.n, w1 - place - kSegment);
@@ -498,8 +503,12 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV8>::kCtas)
   if (w0 < w1) {
     item = first_item;
     place = first_place;
-    counts.fill(a, item, n_items);
-    n = counts.get(a, item, n_items);
+    if constexpr (CL) {
+      n = own.n;
+    } else {
+      counts.fill(a, item, n_items);
+      n = counts.get(a, item, n_items);
+    }
     off = imax(0, w0 - place - kSegment);
     lim = imin(n, w1 - place - kSegment);
     more = off < lim || (!CL && step());

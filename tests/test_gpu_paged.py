@@ -747,3 +747,67 @@ def test_chunk_graph_stream_and_refusals(cuda_device):
             run(**bad)
     with pytest.raises(cw.CowaError):
         run(workspace=torch.zeros(128, dtype=torch.uint8, device=cuda_device))
+
+
+# ------------------------------------------------------------------------------------------ large pools, debug build
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_pools_past_32_bit_offsets(cuda_device, e4m3):
+    """Pages whose elements (and bytes) lie past 2^32: written, decoded, and read by a chunk."""
+    Hq, Hkv, d, ps = 4, 4, 128, 64
+    n_pages = (1 << 32) // (ps * Hkv * d) + 40  # 8.6 GB of bf16, 4.3 GB of codes
+    pat = cw.Pattern(8, 100, 200, 4)
+    dt = torch.uint8 if e4m3 else torch.bfloat16
+    kp, vp = (torch.empty((n_pages, ps, Hkv, d), dtype=dt, device=cuda_device) for _ in range(2))
+    tab = torch.tensor([[n_pages - 1, 0, n_pages - 7, n_pages - 30]], dtype=torch.int32, device=cuda_device)
+    N = 4 * ps
+    (k64, k), (v64, v) = (host_and_device((N, Hkv, d), x, cuda_device, 99) for x in ("k", "v"))
+    q64, q = host_and_device((1, Hq, d), "q", cuda_device, 99)
+    pos = torch.arange(N, dtype=torch.int32, device=cuda_device)
+    seq = torch.zeros(N, dtype=torch.int32, device=cuda_device)
+    one = torch.tensor([N - 1], dtype=torch.int32, device=cuda_device)
+    if e4m3:
+        cw.paged_append_fp8(None, k, v, pos, kp, vp, tab, 1 / 64, 1 / 64, seq=seq)
+        o, lse = cw.cowa_decode_paged_fp8(q, kp, vp, tab, one, pat, 1 / 64, 1 / 64)
+        k64, v64 = (f8.e4m3_to_f64(f8.quantize_e4m3_f32(x.astype(np.float32), 1 / 64)) / 64 for x in (k64, v64))
+    else:
+        cw.paged_append(None, k, v, pos, kp, vp, tab, seq=seq)
+        o, lse = cw.cowa_decode_paged(q, kp, vp, tab, one, pat)
+    assert_decoded(o, lse, q64, k64.transpose(1, 0, 2)[None], v64.transpose(1, 0, 2)[None], [N - 1], pat,
+                   2.0 ** -11 if e4m3 else 2.0 ** -8)
+    if not e4m3:
+        i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=cuda_device)
+        o, lse = cw.cowa_fwd_paged(q, kp, vp, tab, i32([0, 1]), i32([N - 1]), pat)
+        assert_chunk(o, lse, q64, k64.transpose(1, 0, 2), v64.transpose(1, 0, 2), N - 1, pat)
+
+
+def test_debug_build_gives_the_same_bits(cuda_device):
+    from structured_sparse_attention_cowa_b200 import build as cbuild
+
+    B, Hq, Hkv, d, ps, n = 3, 10, 2, 128, 24, 40
+    pat = cw.Pattern(20, 100, 900, 2)
+    rope = cw.Rope(cw.rope_frequencies(d, device=cuda_device))
+    tab = torch.randperm(B * n, device=cuda_device).int().view(B, n)
+    r = lambda s, nm: synth.cuda_normal_bf16(s, synth.seed_of(nm, 100), cuda_device)
+    q, k, v = r((B, Hq, d), "q"), r((B, Hkv, d), "k"), r((B, Hkv, d), "v")
+    pools = r((B * n, ps, Hkv, d), "k_cache"), r((B * n, ps, Hkv, d), "v_cache")
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=cuda_device)
+    pos = i32([900, 31, -1])
+
+    def step():
+        kp, vp = (p.clone() for p in pools)
+        ws = torch.zeros(1 << 23, dtype=torch.uint8, device=cuda_device)
+        qr = cw.paged_append(q, k, v, pos, kp, vp, tab, rope=rope, q_out=torch.zeros_like(q))
+        out = [qr, kp, vp, *cw.cowa_decode_paged(qr, kp, vp, tab, pos, pat, workspace=ws),
+               *cw.cowa_fwd_paged(qr, kp, vp, tab, i32([0, 1, 1, 3]), i32([900, 0, 5]), pat, workspace=ws)]
+        assert cw.workspace_status(ws) == 0
+        return out
+
+    want = step()
+    saved = cw._lib, cw.LIB_PATH
+    cw._lib, cw.LIB_PATH = None, cbuild.build(debug=True)
+    try:
+        got = step()
+    finally:
+        cw._lib, cw.LIB_PATH = saved
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
