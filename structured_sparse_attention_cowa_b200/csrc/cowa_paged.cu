@@ -57,13 +57,15 @@ constexpr int kJoinWarps = 16;  // of a joining block, at most
 template <bool KV8>
 constexpr float kLift = KV8 ? 6.0f : 0.0f;
 
-template <int D, bool KV8>
+// BIG: groups of more than 5 query heads, whose join takes more shared memory (with E4M3 pages a stage less
+// then keeps three CTAs on an SM)
+template <int D, bool KV8, bool BIG>
 struct Geo {
   static_assert(!KV8 || D == 128, "E4M3 rows are whole 128-byte rows");
   static constexpr int kBarBytes = 256;  // 3 words per stage, then a few of the block's own
   static constexpr int kUnits = KV8 ? 1 : D / 64;  // 128-byte columns of a row
   static constexpr int kTileBytes = kUnits * kBoxBytes;
-  static constexpr int kStages = KV8 ? 4 : (D == 128 ? 3 : 5);
+  static constexpr int kStages = KV8 ? (BIG ? 3 : 4) : (D == 128 ? 3 : 5);
   static constexpr int kCtas = KV8 ? 3 : 2;        // per SM, what the ring leaves room for
   static constexpr int kOffBar = kStages * 2 * kTileBytes;
   static_assert(3 * kStages <= 16, "the block's own words start at word 16");
@@ -250,10 +252,10 @@ __device__ __forceinline__ float cluster_ld(const float* own, int rank) {  // th
 }
 
 // CL: CTAs c, c + 1, .. of a cluster of a.cluster share one pair; else every CTA has its share of the list.
-template <int D, bool KV8, bool CL>
-__global__ void __launch_bounds__(kThreads, Geo<D, KV8>::kCtas)
+template <int D, bool KV8, bool CL, bool BIG>
+__global__ void __launch_bounds__(kThreads, Geo<D, KV8, BIG>::kCtas)
     paged_split_kernel(const __grid_constant__ PagedDecodeArgs a) {
-  using G_ = Geo<D, KV8>;
+  using G_ = Geo<D, KV8, BIG>;
   constexpr int KS = D / 16;
   constexpr int kStages = G_::kStages;
   constexpr int kSegment = kSegmentOf<KV8>;
@@ -772,9 +774,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const __gri
   if (a.lse && d == 0) a.lse[h] = m == -INFINITY ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
 }
 
-template <int D, bool KV8>
+template <int D, bool KV8, bool BIG>
 cudaError_t launch_paged_t(const PagedDecodeArgs& a, cudaStream_t s) {
-  const int bytes = Geo<D, KV8>::smem(a.grp);
+  const int bytes = Geo<D, KV8, BIG>::smem(a.grp);
   // the kernels are set up while the one before them runs, and wait for its results themselves
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -787,7 +789,7 @@ cudaError_t launch_paged_t(const PagedDecodeArgs& a, cudaStream_t s) {
   cfg.numAttrs = 1;
   cudaError_t e;
   if (a.cluster > 0) {
-    auto kern = paged_split_kernel<D, KV8, true>;
+    auto kern = paged_split_kernel<D, KV8, true, BIG>;
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
     if (a.cluster > 8 &&
         (e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
@@ -799,7 +801,7 @@ cudaError_t launch_paged_t(const PagedDecodeArgs& a, cudaStream_t s) {
     cfg.gridDim = dim3((unsigned)(a.B * a.Hkv * a.cluster));
     return cudaLaunchKernelEx(&cfg, kern, a);
   }
-  auto kern = paged_split_kernel<D, KV8, false>;
+  auto kern = paged_split_kernel<D, KV8, false, BIG>;
   if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
   cfg.gridDim = dim3(a.grid);
   if ((e = cudaLaunchKernelEx(&cfg, kern, a)) != cudaSuccess) return e;
@@ -820,7 +822,9 @@ cudaError_t launch_paged_t(const PagedDecodeArgs& a, cudaStream_t s) {
 // faster (296 pairs of up to 680 keys in the cluster form: 21.6 us full, 18.8 ragged; 22.4 and 13.6 as a list).
 PagedPlan paged_decode_plan(const Pat& p, int B, int Hq, int Hkv, int d, bool kv8, int max_pages, int page_size) {
   const int grp = Hq / Hkv;
-  const int most = 148 * (kv8 ? Geo<128, true>::ctas(grp) : (d == 128 ? Geo<128, false>::ctas(grp) : Geo<64, false>::ctas(grp)));
+  const int most = 148 * (kv8       ? (grp > 5 ? Geo<128, true, true>::ctas(grp) : Geo<128, true, false>::ctas(grp))
+                          : d == 128 ? Geo<128, false, false>::ctas(grp)
+                                     : Geo<64, false, false>::ctas(grp));
   const int64_t cap = (int64_t)max_pages * page_size, R = (int64_t)p.T - p.S, pairs = (int64_t)B * Hkv;
   const int64_t wide = R > 0 ? (R + p.H - 1) / p.H : 0;
   auto tiles = [&](int64_t n) { return n > 0 ? ((n < cap ? n : cap) + kTok - 1) / kTok + 1 : 0; };
@@ -841,9 +845,9 @@ size_t paged_decode_bytes(int grid, int grp, int d) {
 }
 
 cudaError_t launch_paged_decode(const PagedDecodeArgs& a, int d, bool kv8, cudaStream_t s) {
-  if (kv8) return d == 128 ? launch_paged_t<128, true>(a, s) : cudaErrorInvalidValue;
-  if (d == 64) return launch_paged_t<64, false>(a, s);
-  if (d == 128) return launch_paged_t<128, false>(a, s);
+  if (kv8 && d == 128) return a.grp > 5 ? launch_paged_t<128, true, true>(a, s) : launch_paged_t<128, true, false>(a, s);
+  if (!kv8 && d == 64) return launch_paged_t<64, false, false>(a, s);
+  if (!kv8 && d == 128) return launch_paged_t<128, false, false>(a, s);
   return cudaErrorInvalidValue;
 }
 
