@@ -627,8 +627,11 @@ def _native():
     if _binding_of is not L:
         import torch  # noqa: F401  (the extension needs its libraries)
 
-        from . import _binding as b
-
+        try:
+            from . import _binding as b
+        except ImportError as e:
+            raise RuntimeError("_binding.so is missing or was built against another torch; build it with "
+                               "`python -m structured_sparse_attention_cowa_b200.build`") from e
         b.use(L._handle)
         _binding, _binding_of = b, L
     return _binding

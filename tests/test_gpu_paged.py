@@ -811,3 +811,42 @@ def test_debug_build_gives_the_same_bits(cuda_device):
         cw._lib, cw.LIB_PATH = saved
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+def test_chained_calls_without_waits(cuda_device, wide):
+    """Each call reads what the one before it in the stream wrote, with nothing in between (the kernels are
+    set up while the one before runs): the same bits as with the GPU waited for after every call."""
+    B, Hq, Hkv, d, ps, n = 6, 4, 2, 128, 32, 20
+    pat, rope = cw.Pattern(16, 100, 640, 2), cw.Rope(cw.rope_frequencies(d, device=cuda_device))
+    tabh = np.random.default_rng(101).permutation(B * n).astype(np.int32).reshape(B, n)
+    if wide:
+        pat, tabh = widened(pat, tabh, ps)
+    tab = torch.from_numpy(tabh).to(cuda_device)
+    pools = [synth.cuda_normal_bf16((B * n, ps, Hkv, d), synth.seed_of(x, 101), cuda_device) for x in ("k_cache", "v_cache")]
+    first = synth.cuda_normal_bf16((B, Hq, d), synth.seed_of("q", 101), cuda_device)
+    steps = [torch.tensor([(37 * i + 101 * b) % 600 for b in range(B)], dtype=torch.int32, device=cuda_device)
+             for i in range(40)]
+    cu = torch.arange(B + 1, dtype=torch.int32, device=cuda_device)
+
+    def run(wait):
+        kp, vp = (p.clone() for p in pools)
+        ws = torch.zeros(1 << 23, dtype=torch.uint8, device=cuda_device)
+        x, qo, o = first.clone(), torch.empty_like(first), torch.empty_like(first)
+        lse, lse2 = torch.empty((B, Hq), device=cuda_device), torch.empty((Hq, B), device=cuda_device)
+        calls = (lambda p: cw.paged_append(x, x[:, :Hkv], x[:, Hkv:], p, kp, vp, tab, rope=rope, q_out=qo),
+                 lambda p: cw.cowa_decode_paged(qo, kp, vp, tab, p, pat, out=o, lse=lse, workspace=ws),
+                 lambda p: cw.cowa_fwd_paged(o, kp, vp, tab, cu, p, pat, out=qo, lse=lse2, workspace=ws),
+                 lambda p: cw.cowa_rope(qo[None], None, rope, p[None], q_out=x[None]))
+        torch.cuda.synchronize()
+        for p in steps:
+            for call in calls:
+                call(p)
+                if wait:
+                    torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        assert cw.workspace_status(ws) == 0
+        return x, o, lse, kp, vp
+
+    for a, b in zip(run(True), run(False)):
+        assert torch.isfinite(a.float()).all() and torch.equal(a, b)

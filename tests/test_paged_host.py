@@ -160,3 +160,16 @@ def test_binding_refuses_cpu_tensors_and_wrong_types():
         cw.cowa_decode_paged(q[:, 0], q, q, pos, pos, cw.Pattern(1, 1, 1, 1))
     with pytest.raises(TypeError):
         cw.cowa_decode_paged_fp8(q[:, 0], q, q, pos, pos, cw.Pattern(1, 1, 1, 1), 1.0, 1.0)
+
+
+def test_missing_compiled_binding_raises(monkeypatch):
+    import sys
+
+    import structured_sparse_attention_cowa_b200 as pkg
+
+    monkeypatch.setattr(cw, "_binding_of", None)
+    monkeypatch.delattr(pkg, "_binding", raising=False)
+    monkeypatch.setitem(sys.modules, pkg.__name__ + "._binding", None)
+    q = torch.zeros((2, 4, 64), dtype=torch.bfloat16)
+    with pytest.raises(RuntimeError, match="_binding.so"):
+        cw.paged_append(None, q, q, q, q, q, q)
