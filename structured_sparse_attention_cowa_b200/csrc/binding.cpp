@@ -50,11 +50,6 @@ const at::Tensor& tensor(PyObject* o, const char* name) {
   if (!t) bad_type(std::string(name) + " must be a tensor");
   return *t;
 }
-long integer(PyObject* o) {
-  const long v = PyLong_AsLong(o);
-  if (v == -1 && PyErr_Occurred()) throw Refused{nullptr, ""};
-  return v;
-}
 double number(PyObject* o) {
   const double v = PyFloat_AsDouble(o);
   if (v == -1.0 && PyErr_Occurred()) throw Refused{nullptr, ""};
@@ -332,6 +327,11 @@ void check_lse(const at::Tensor* lse, at::IntArrayRef shape) {
     bad_value("lse must be a contiguous float32 tensor of the shape of the rows");
 }
 
+// The caller's workspace, or none: one piece of memory, so that its size is what the kernels may use
+void check_workspace(const at::Tensor* ws) {
+  if (ws && !ws->is_contiguous()) bad_value("workspace must be a contiguous tensor");
+}
+
 // decode(q_t, k_pages, v_pages, page_table, pos, pattern, scales, layout, out, lse, workspace, want_lse)
 // -> (status, out, lse)
 PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -353,6 +353,7 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (out->sizes() != q.sizes() || !out->is_contiguous()) bad_value("out must be contiguous [B, H_q, d]");
     }
     check_lse(lse, {B, Hq});
+    check_workspace(ws);
     same_device(q, {&kp, &vp, &tab, &pos, out, lse, ws});
     const c10::cuda::CUDAGuard guard(q.device());
     at::Tensor mo, ml, mw;
@@ -393,6 +394,7 @@ PyObject* fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
                      *ws = tensor_or_none(a[10], "workspace");
     if (out) { bf16(*out, "out"); of_shape(*out, "out", q.sizes()); }
     check_lse(lse, {Hq, total});
+    check_workspace(ws);
     same_device(q, {&kp, &vp, &tab, &cu, &start, out, lse, ws});
     const c10::cuda::CUDAGuard guard(q.device());
     at::Tensor mo, ml, mw;

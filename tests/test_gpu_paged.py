@@ -850,3 +850,20 @@ def test_chained_calls_without_waits(cuda_device, wide):
 
     for a, b in zip(run(True), run(False)):
         assert torch.isfinite(a.float()).all() and torch.equal(a, b)
+
+
+def test_workspace_in_pieces_is_refused(cuda_device):
+    """A workspace whose elements are not one piece of memory would be smaller, or in other places, than its
+    element count says."""
+    q = torch.zeros((2, 4, 64), dtype=torch.bfloat16, device=cuda_device)
+    pool = torch.zeros((6, 16, 2, 64), dtype=torch.bfloat16, device=cuda_device)
+    tab = torch.zeros((2, 3), dtype=torch.int32, device=cuda_device)
+    pos = torch.zeros(2, dtype=torch.int32, device=cuda_device)
+    cu = torch.tensor([0, 1, 2], dtype=torch.int32, device=cuda_device)
+    pat = cw.Pattern(4, 8, 48, 2)
+    one = torch.zeros(1, dtype=torch.uint8, device=cuda_device)
+    for ws in (one.expand(1 << 24), torch.zeros(1 << 24, dtype=torch.uint8, device=cuda_device)[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            cw.cowa_decode_paged(q, pool, pool, tab, pos, pat, workspace=ws)
+        with pytest.raises(ValueError, match="workspace"):
+            cw.cowa_fwd_paged(q, pool, pool, tab, cu, pos, pat, workspace=ws)
