@@ -658,7 +658,8 @@ class Rope:
     """Rotary positions of a layer (cowa_rotary in include/cowa.h): inv_freq, a CUDA float32 tensor of
     rotary_dim / 2 frequencies; `sections`, how many pairs turn with each position axis (1 to 4 axes,
     adding up to rotary_dim / 2; default one axis); `interleaved`, pairs (2i, 2i+1) instead of
-    (i, i + rotary_dim/2); `scale`, a factor of cos and sin (0 means 1)."""
+    (i, i + rotary_dim/2); `scale`, a factor of cos and sin (0 means 1).  Attributes cannot be set again:
+    the structure that the calls read holds the address of inv_freq."""
 
     def __init__(self, inv_freq, sections=(), interleaved: bool = False, scale: float = 1.0):
         import torch
@@ -674,6 +675,11 @@ class Rope:
         self._c = c_rotary(inv_freq.data_ptr(), 2 * inv_freq.numel(), len(sections),
                            (ctypes.c_int32 * 4)(*sections), int(self.interleaved), self.scale)
         self._address = ctypes.addressof(self._c)
+
+    def __setattr__(self, name, value):
+        if name in self.__dict__:
+            raise AttributeError("a Rope cannot be changed; make another one")
+        super().__setattr__(name, value)
 
     def c(self) -> c_rotary:
         return self._c

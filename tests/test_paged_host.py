@@ -173,3 +173,11 @@ def test_missing_compiled_binding_raises(monkeypatch):
     q = torch.zeros((2, 4, 64), dtype=torch.bfloat16)
     with pytest.raises(RuntimeError, match="_binding.so"):
         cw.paged_append(None, q, q, q, q, q, q)
+
+
+def test_rope_cannot_be_changed():
+    """A call reads the address that the Rope was made with: other frequencies need another Rope."""
+    rope = object.__new__(cw.Rope)
+    rope.inv_freq = torch.ones(32)
+    with pytest.raises(AttributeError, match="Rope"):
+        rope.inv_freq = torch.ones(32)
