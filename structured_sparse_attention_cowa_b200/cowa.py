@@ -651,6 +651,8 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, device="cuda"):
     """inv_freq[i] = base^(-2 i / rotary_dim), i < rotary_dim / 2, float32 on `device`."""
     import torch
 
+    if rotary_dim < 2 or rotary_dim % 2 or not base > 0:
+        raise ValueError("rotary_dim must be even and at least 2, base positive")
     return (float(base) ** (-torch.arange(0, rotary_dim, 2, dtype=torch.float64) / rotary_dim)).float().to(device)
 
 

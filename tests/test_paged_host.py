@@ -181,3 +181,15 @@ def test_rope_cannot_be_changed():
     rope.inv_freq = torch.ones(32)
     with pytest.raises(AttributeError, match="Rope"):
         rope.inv_freq = torch.ones(32)
+
+
+@pytest.mark.parametrize("rotary_dim,base", [(0, 1e4), (-2, 1e4), (7, 1e4), (64, 0.0), (64, -1e4)])
+def test_rope_frequencies_refusals(rotary_dim, base):
+    with pytest.raises(ValueError):
+        cw.rope_frequencies(rotary_dim, base, device="cpu")
+
+
+def test_rope_frequencies_match_their_formula():
+    got = cw.rope_frequencies(96, 5e5, device="cpu")
+    want = np.array([5e5 ** (-2 * i / 96) for i in range(48)])
+    assert got.dtype == torch.float32 and (np.abs(got.double().numpy() - want) <= 2.0 ** -23 * want).all()
