@@ -204,3 +204,11 @@ def test_refusals_of_the_binding(cuda_device):
         cw.cowa_rope(q, None, cw.Rope(torch.ones(40, device=cuda_device)))
     with pytest.raises(cw.CowaError):  # a broadcast head
         cw.cowa_rope(q[:, :, :1].expand(2, 8, 4, 64), None, rope)
+
+
+def test_no_memory_for_an_output(cuda_device):
+    """An output that does not fit raises what torch raises for it (2^30 tokens of 64 heads of 128: 16 TiB)."""
+    f, _ = freq_of(128, cuda_device)
+    q = torch.zeros((1, 1, 1, 128), dtype=torch.bfloat16, device=cuda_device).expand(1, 1 << 30, 64, 128)
+    with pytest.raises(torch.OutOfMemoryError):
+        cw.cowa_rope(q, None, cw.Rope(f))
