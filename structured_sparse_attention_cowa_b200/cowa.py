@@ -691,8 +691,9 @@ class Rope:
 
 
 def _rope(bwd, q, k, rope, positions, q_out, k_out, stream):
-    if stream is not None:
-        with _on(q if q is not None else k, stream):
+    x = q if q is not None else k
+    if stream is not None and x is not None:
+        with _on(x, stream):
             return _rope(bwd, q, k, rope, positions, q_out, k_out, None)
     status, q_out, k_out = _native().rope(bwd, q, k, rope._address, rope.inv_freq, positions, q_out, k_out)
     if status:

@@ -193,3 +193,11 @@ def test_rope_frequencies_match_their_formula():
     got = cw.rope_frequencies(96, 5e5, device="cpu")
     want = np.array([5e5 ** (-2 * i / 96) for i in range(48)])
     assert got.dtype == torch.float32 and (np.abs(got.double().numpy() - want) <= 2.0 ** -23 * want).all()
+
+
+def test_rope_of_nothing_on_a_stream_is_refused():
+    fake = object.__new__(cw.Rope)
+    fake.inv_freq, fake._c = torch.ones(32), rotary(r=64)
+    fake._address = ctypes.addressof(fake._c)
+    with pytest.raises(ValueError, match="q or k"):
+        cw.cowa_rope(None, None, fake, stream=object())
