@@ -13,7 +13,6 @@
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <dlfcn.h>
-#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <string>
@@ -186,7 +185,12 @@ PyObject* guarded(Py_ssize_t n, Py_ssize_t want, F f) {
   } catch (const Refused& r) {
     if (r.type) PyErr_SetString(r.type, r.text.c_str());
   } catch (const c10::OutOfMemoryError& e) {
-    PyErr_SetString(THPException_OutOfMemoryError, e.what_without_backtrace());
+    // torch.OutOfMemoryError, whose C++ symbol libtorch_python does not export
+    PyObject* torch = PyImport_ImportModule("torch");
+    PyObject* type = torch ? PyObject_GetAttrString(torch, "OutOfMemoryError") : nullptr;
+    if (type) PyErr_SetString(type, e.what_without_backtrace());
+    Py_XDECREF(type);
+    Py_XDECREF(torch);
   } catch (const c10::Error& e) {
     PyErr_SetString(PyExc_RuntimeError, e.what_without_backtrace());
   } catch (const std::exception& e) {
