@@ -42,9 +42,10 @@
  *     it (COWA_ERR_TIMEOUT).
  *   - The library keeps no mutable global state on the call path; calls on
  *     different streams with different workspaces may run concurrently.
- *   - cowa_fwd, cowa_bwd and cowa_decode never synchronise the host and allocate
- *     nothing, so a step made of them can be captured in a CUDA graph on a
- *     capturing stream and replayed (same bits as the calls made directly).
+ *   - cowa_fwd, cowa_bwd and cowa_decode, the rotary and the paged calls never
+ *     synchronise the host and allocate nothing, so a step made of them can be
+ *     captured in a CUDA graph on a capturing stream and replayed (same bits as
+ *     the calls made directly).
  *     cowa_workspace_status synchronises and is not capturable.
  */
 #ifndef COWA_H
@@ -409,7 +410,7 @@ size_t cowa_decode_paged_workspace_size(const cowa_pattern* pat, int B, int H_q,
 cowa_status cowa_decode_paged(const cowa_pattern* pat, int B, int H_q, int H_kv, int d, const void* q_t,
                               cowa_tensor k_pages, cowa_tensor v_pages, cowa_page_table table, const int32_t* pos,
                               void* o, float* lse_or_null, void* ws, size_t ws_bytes, void* stream);
-/* Over pages of E4M3 codes (d = 128; scales as for cowa_decode_fp8). */
+/* Over pages of E4M3 codes (d = 128; scales, and q_t used in f16, as for cowa_decode_fp8). */
 size_t cowa_decode_paged_fp8_workspace_size(const cowa_pattern* pat, int B, int H_q, int H_kv, int d, int max_pages,
                                             int page_size);
 cowa_status cowa_decode_paged_fp8(const cowa_pattern* pat, int B, int H_q, int H_kv, int d, const void* q_t,
@@ -421,13 +422,15 @@ cowa_status cowa_decode_paged_fp8(const cowa_pattern* pat, int B, int H_q, int H
  * cu_seqlens[s] .. cu_seqlens[s+1]-1 of q [total, H_q, d], the first at position q_start[s], against its
  * keys at positions 0 .. q_start[s] + len_s - 1, the chunk's own among them (cowa_paged_append first).
  * Outputs o [total, H_q, d] and lse fp32 [H_q, total] as cowa_fwd_varlen, whose rules hold for
- * cu_seqlens (device int32 [n_seq + 1]) and strides; rows behind the last sequence are left as they are.  q_start: device int32 [n_seq], clamped into [0, capacity - len_s] (rows of a sequence
- * longer than the capacity see the keys there are); a row that sees nothing has o 0 and lse -inf.
+ * cu_seqlens (device int32 [n_seq + 1]) and strides; rows behind the last sequence are left as they
+ * are.  q_start: device int32 [n_seq], clamped into [0, capacity - len_s] (rows of a sequence longer than
+ * the capacity see the keys there are); a row that sees nothing has o 0 and lse -inf.
  * Where an entry of a page with a key that some row of a query tile (128 rows of a sequence) sees lies
  * outside [0, n_pages), the tile's rows of that KV head's group are left empty (o 0, lse -inf) and
  * COWA_ERR_PAGE is reported as for cowa_decode_paged; other entries may hold anything.  Keys and values
  * below q_start[s] + len_s on mapped pages must be finite where they share a tile of 128 positions with
- * visible ones; what stands behind them is never used.  bf16 pages only.  The workspace's first 256 bytes must be zero before its first call. */
+ * visible ones; what stands behind them is never used.  bf16 pages only.  The workspace's first 256
+ * bytes must be zero before its first call. */
 size_t cowa_fwd_paged_workspace_size(const cowa_pattern* pat, int n_seq, int total, int H_q, int H_kv, int d,
                                      int max_pages, int page_size);
 cowa_status cowa_fwd_paged(const cowa_pattern* pat, int n_seq, int total, int H_q, int H_kv, int d,

@@ -154,7 +154,7 @@ cowa_status cowa_workspace_status(void* ws, void* stream) {
   uint32_t word[4] = {0, 0, 0, 0};
   if (cudaMemcpyAsync(word, ws, sizeof(word), cudaMemcpyDeviceToHost, s) != cudaSuccess) return COWA_ERR_CUDA;
   if (cudaStreamSynchronize(s) != cudaSuccess) return COWA_ERR_CUDA;
-  if (word[0] != 0 || word[3] != 0) {
+  if (word[0] != 0 || word[3] == kPageFlag) {
     // clear the status word, the self-check record (words 1 and 2) and the bad-page flag (word 3)
     // for the next call
     if (cudaMemsetAsync(ws, 0, sizeof(word), s) != cudaSuccess) return COWA_ERR_CUDA;

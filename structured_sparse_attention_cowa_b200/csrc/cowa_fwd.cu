@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cowa_fwd_kernel(const __grid_c
           const bool want = p < e && (p < a.pat.S || e > t0 - a.pat.L + 1 || (p < iv.hi && e > iv.lo));
           const bool good = want && page >= 0 && page < a.tab.n_pages;
           if (want && !good) {
-            a.status[3] = 1u;
+            a.status[3] = kPageFlag;
             *reinterpret_cast<volatile int*>(&bad_page) = 1;
           }
           const int slot = p % a.tab.page_size;

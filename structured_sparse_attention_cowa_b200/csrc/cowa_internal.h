@@ -15,6 +15,9 @@ namespace cowa {
 // Every workspace starts with a 256-byte header whose first word is the device
 // status (0 = ok, bit 0 = a bounded wait ran out).  Kernel data follows.
 constexpr size_t kWsHeader = 256;
+// What the paged calls write to word 3 of the workspace for a bad page.  (A value of its own: the other
+// calls never needed that word cleared, and it may hold anything in their workspaces.)
+constexpr uint32_t kPageFlag = 0x50414745u;
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 

@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV8, BIG>::kCtas)
           const uint64_t rows = a.box_rows == kTok ? ~0ull : (1ull << a.box_rows) - 1;
           for (int x = 0; x < nbox; ++x)
             if ((bad >> x) & 1) vis &= ~(rows << (x * a.box_rows));
-          if (lane == 0) a.status[3] = 1u;
+          if (lane == 0) a.status[3] = kPageFlag;
         }
         if (st >= kStages && !ptx::mbar_wait_warp(&empty_bar[sl], ((st / kStages) & 1) ^ 1, &abort_flag, a.status))
           return false;

@@ -867,3 +867,13 @@ def test_workspace_in_pieces_is_refused(cuda_device):
             cw.cowa_decode_paged(q, pool, pool, tab, pos, pat, workspace=ws)
         with pytest.raises(ValueError, match="workspace"):
             cw.cowa_fwd_paged(q, pool, pool, tab, cu, pos, pat, workspace=ws)
+
+
+def test_status_of_workspaces_of_other_calls(cuda_device):
+    """Only the status word had to be cleared before there were paged calls: whatever else the header of such
+    a workspace holds is not a bad page."""
+    ws = torch.full((256,), 0x5A, dtype=torch.uint8, device=cuda_device)
+    ws[:4] = 0
+    assert cw.workspace_status(ws) == 0
+    ws[12:16] = torch.tensor([1, 0, 0, 0], dtype=torch.uint8, device=cuda_device)
+    assert cw.workspace_status(ws) == 0
