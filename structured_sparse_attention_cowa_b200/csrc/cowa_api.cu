@@ -871,6 +871,7 @@ cowa_status cowa_fwd_paged(const cowa_pattern* pat, int n_seq, int total, int Hq
   a.Nq = total; a.Nk = total;
   a.varlen = 1; a.n_seq = n_seq; a.total = total; a.cu_seqlens = cu_seqlens;
   a.paged = 1;
+  for (int g = 0; g < Hkv && g < kPagedIv; ++g) a.iv[g] = interval_of(p, g);
   a.q_start = q_start;
   a.box_rows = page_box_rows(table.page_size, 128);
   a.o = o.ptr; a.o_st = o.stride_t; a.o_sh = o.stride_h;

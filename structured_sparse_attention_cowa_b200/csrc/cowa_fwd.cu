@@ -78,16 +78,31 @@ struct FwdGeom {
   static constexpr int kColO = 256;
 };
 
-// PAGED: query tile `rank` of the packed chunks; one warp.  Up to 64 sequences: the tiles in descending
-// order of the position they begin at (in steps of a tile), which is about that of their work, found
-// by a binary search over that position with the sequences in the lanes' registers.  More: sequence by
-// sequence.  The offsets are clamped as in the sequence table of kernel_common.cuh.
+// PAGED: what CTA `rank` (of all parts of a tile) works on; one warp.  Pairs of heads come before the single
+// heads of odd groups, which are half as much work.
+//   * Where all CTAs run at once (148 of them or fewer), or with more than 64 sequences: tile by tile of one
+//     sequence after the other.
+//   * Up to 64 (KV head, sequence)s: the (head, query tile)s in descending order of their keys, counted in
+//     tiles.  A tile that begins at position t has about min(t, L) + clamp(t - L - lo, 0, hi - lo) of them
+//     besides the sinks, so those of one head and sequence with x tiles or more are the ones that begin at
+//     tile x (x up to the band's width) or x + lo (beyond it).  The x of a rank is found by a binary search,
+//     with up to two (head, sequence)s in a lane's registers.  Against the next form: six ragged chunks (40/8
+//     heads, L = 2048, interval 4080) 303 -> 264 us, two behind 7K keys (56/8 heads, 1150 rows) 151 -> 121, 4K
+//     rows behind 28K keys 503 -> 473; three behind 6K with L = 4096, where positions say as much, 439 -> 444.
+//   * Up to 64 sequences: the tiles in descending order of their positions, all heads of a tile together (the
+//     same search, with sequences instead).
+// The offsets are clamped as in the sequence table of kernel_common.cuh.
 struct Chunk {
-  int seq, tile, row0, len, start;  // seq -1: there are no more tiles
+  int seq, tile, row0, len, start;  // seq -1: there is no work left
+  int g, pair;
 };
+constexpr int kSorted = 64;
+static_assert(kSorted <= kPagedIv, "the search takes the intervals from the arguments");
 __device__ __forceinline__ Chunk find_chunk(const FwdArgs& a, int rank) {
   constexpr unsigned kAll = 0xffffffffu;
+  const Chunk none{-1, 0, 0, 0, 0, 0, 0};
   const int lane = threadIdx.x & 31, cap = a.tab.max_pages * a.tab.page_size;
+  const int grp = a.Hq / a.Hkv, whole = grp >> 1;
   struct Seq {
     int row0, len, start, tiles;
   };
@@ -110,44 +125,92 @@ __device__ __forceinline__ Chunk find_chunk(const FwdArgs& a, int rank) {
     end = __shfl_sync(kAll, e, 31);
     return q;
   };
-  auto hand = [&](const Seq& q, int src, int first, int tile) {
-    return Chunk{first + src, __shfl_sync(kAll, tile, src), __shfl_sync(kAll, q.row0, src), __shfl_sync(kAll, q.len, src),
-                 __shfl_sync(kAll, q.start, src)};
-  };
-  if (a.n_seq <= 64) {
-    const Seq q0 = load(0);
-    Seq q1 = {0, 0, 0, 0};
-    if (a.n_seq > 32) q1 = load(32);
-    const int k0 = q0.start / kBM, k1 = q1.start / kBM;  // place of a sequence's first tile
-    auto from = [&](int x) {  // tiles at place x or later
-      return (int)__reduce_add_sync(kAll, (unsigned)(imax(0, imin(q0.tiles, k0 + q0.tiles - x)) +
-                                                     imax(0, imin(q1.tiles, k1 + q1.tiles - x))));
-    };
-    if (from(0) <= rank) return Chunk{-1, 0, 0, 0, 0};
-    int lo = 0, hi = (int)__reduce_max_sync(kAll, (unsigned)imax(k0 + q0.tiles, k1 + q1.tiles));
-    while (lo < hi) {  // the last place with more than `rank` tiles at it or later
-      const int mid = (lo + hi + 1) >> 1;
-      if (from(mid) > rank) lo = mid; else hi = mid - 1;
+  int pair = whole, g;
+  auto take_pair = [&](int n) -> bool {  // n: (head, tile)s; false: past the last work
+    if (rank < n * whole) {
+      pair = rank % whole;
+      rank /= whole;
+      return true;
     }
-    const int nth = rank - from(lo + 1);
-    const unsigned in0 = __ballot_sync(kAll, k0 <= lo && lo < k0 + q0.tiles), in1 = __ballot_sync(kAll, k1 <= lo && lo < k1 + q1.tiles);
-    const int n0 = __popc(in0);
-    return nth < n0 ? hand(q0, __fns(in0, 0, nth + 1), 0, lo - k0) : hand(q1, __fns(in1, 0, nth - n0 + 1), 32, lo - k1);
-  }
-  for (int first = 0, done = 0; first < a.n_seq; first += 32) {
-    const Seq q = load(first);
-    int incl = q.tiles;
+    rank -= n * whole;
+    return grp % 2 != 0 && rank < n;
+  };
+  auto sum = [&](int x) { return (int)__reduce_add_sync(kAll, (unsigned)x); };
+  // the lane of x's running sum over the lanes that holds place n (n < the sum), n then counting from its own
+  auto lane_of = [&](int x, int& n) {
+    int incl = x;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(kAll, incl, o);
       if (lane >= o) incl += y;
     }
-    const int before = done + incl - q.tiles;
-    const unsigned in = __ballot_sync(kAll, rank >= before && rank < before + q.tiles);
-    if (in) return hand(q, __ffs(in) - 1, first, q.tiles - 1 - (rank - before));
-    done += __shfl_sync(kAll, incl, 31);
+    const int l = __ffs(__ballot_sync(kAll, incl > n)) - 1;
+    n -= __shfl_sync(kAll, incl - x, l);
+    return l;
+  };
+  auto hand = [&](const Seq& q, int l, int first, int tile) {
+    return Chunk{first + l, tile, __shfl_sync(kAll, q.row0, l), __shfl_sync(kAll, q.len, l), __shfl_sync(kAll, q.start, l), g,
+                 pair};
+  };
+  if (gridDim.x > 148 && a.n_seq <= kSorted) {
+    const Seq q0 = load(0);
+    Seq q1 = {0, 0, 0, 0};
+    if (a.n_seq > 32) q1 = load(32);
+    if (!take_pair(a.Hkv * (sum(q0.tiles) + sum(q1.tiles)))) return none;
+    const bool by_head = a.n_seq * (int64_t)a.Hkv <= kSorted;
+    int band = 1 << 29, wide = 0;  // (all tiles in the band: their positions decide)
+    if (by_head) {
+      const Range iv = a.iv[0];
+      band = (a.pat.L - 1) / kBM + 1;
+      wide = (iv.hi - iv.lo) / kBM + 1;
+    } else {
+      g = rank % a.Hkv;
+      rank /= a.Hkv;
+    }
+    // item i = 32 j + lane: head i / n_seq (by_head) and sequence i % n_seq; its tiles [k, k + n), and the
+    // tile its interval begins in
+    int k[2], n[2], lo[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int i = 32 * j + lane, h = i / a.n_seq, s = i - h * a.n_seq;
+      const int s0 = __shfl_sync(kAll, q0.start, s & 31), t0 = __shfl_sync(kAll, q0.tiles, s & 31);
+      const int s1 = __shfl_sync(kAll, q1.start, s & 31), t1 = __shfl_sync(kAll, q1.tiles, s & 31);
+      k[j] = (s < 32 ? s0 : s1) / kBM;
+      n[j] = h < (by_head ? a.Hkv : 1) ? (s < 32 ? t0 : t1) : 0;
+      lo[j] = by_head && h < a.Hkv ? a.iv[h].lo / kBM : 0;
+    }
+    // tiles of an item with x tiles of keys or more
+    auto with = [&](int j, int x) {
+      return x - band > wide ? 0 : imax(0, imin(n[j], k[j] + n[j] - x - (x > band ? lo[j] : 0)));
+    };
+    auto all_with = [&](int x) { return sum(with(0, x) + with(1, x)); };
+    int x = 0, hi = imin(band + wide, (int)__reduce_max_sync(kAll, (unsigned)imax(k[0] + n[0], k[1] + n[1])));
+    while (x < hi) {  // the last x with more than `rank` tiles
+      const int mid = (x + hi + 1) >> 1;
+      if (all_with(mid) > rank) x = mid; else hi = mid - 1;
+    }
+    int nth = rank - all_with(x + 1);
+    const int more0 = with(0, x + 1), more1 = with(1, x + 1), m0 = with(0, x) - more0, m1 = with(1, x) - more1, in0 = sum(m0);
+    const bool second = nth >= in0;
+    if (second) nth -= in0;
+    const int l = lane_of(second ? m1 : m0, nth), i = (second ? 32 : 0) + l, h = i / a.n_seq, s = i - h * a.n_seq;
+    if (by_head) g = h;
+    const int tile = __shfl_sync(kAll, second ? n[1] - more1 : n[0] - more0, l) - 1 - nth;
+    return s < 32 ? hand(q0, s, 0, tile) : hand(q1, s - 32, 32, tile);
   }
-  return Chunk{-1, 0, 0, 0, 0};
+  if (!take_pair((int)packed_tiles_bound(a.total, a.n_seq) * a.Hkv)) return none;
+  g = rank % a.Hkv;
+  rank /= a.Hkv;
+  for (int first = 0; first < a.n_seq; first += 32) {
+    const Seq q = load(first);
+    const int in = sum(q.tiles);
+    if (rank < in) {
+      const int l = lane_of(q.tiles, rank);
+      return hand(q, l, first, __shfl_sync(kAll, q.tiles, l) - 1 - rank);
+    }
+    rank -= in;
+  }
+  return none;
 }
 
 // Part `part` of `parts` of a tile list, in order (parts differ by at most one tile; some may be empty).
@@ -204,27 +267,20 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cowa_fwd_kernel(const __grid_c
   int i, row0 = 0, Nq = a.Nq, Nk = a.Nk, q_off = a.q_off;  // row0: first row of the sequence
   int pg_seq = 0, part = 0;
   int pair, g, b = 0;
+  __shared__ Chunk chunk;
   if constexpr (PAGED) {
     // (set up while the kernel before it in the stream ran; waits for that one's results here)
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    __shared__ Chunk chunk;
-    const int whole = grp >> 1, bound = (int)packed_tiles_bound(a.total, a.n_seq), n_whole = bound * a.Hkv * whole;
-    int rank = blockIdx.x / a.parts;
     part = blockIdx.x % a.parts;
-    if (rank < n_whole) {
-      pair = rank % whole; rank /= whole;
-    } else {  // the odd heads, half as much work each
-      rank -= n_whole;
-      pair = whole;
-    }
-    g = rank % a.Hkv; rank /= a.Hkv;
     if (warp == 0) {
-      const Chunk c = find_chunk(a, rank);
+      const Chunk c = find_chunk(a, blockIdx.x / a.parts);
       if (lane == 0) chunk = c;
     }
     __syncthreads();
     if (chunk.seq < 0) return;  // whole CTA, before any barrier or TMEM use
     pg_seq = chunk.seq;
+    g = chunk.g;
+    pair = chunk.pair;
     i = chunk.tile;
     row0 = chunk.row0;
     Nq = chunk.len;
@@ -249,11 +305,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cowa_fwd_kernel(const __grid_c
     g = rem % a.Hkv;
     b = rem / a.Hkv;
   }
-  const int h0 = g * grp + 2 * pair;
+  int h0 = g * grp + 2 * pair;
   const bool has1 = (2 * pair + 1) < grp;
   // query rows of the tile: local q rows [i*BM, ...), absolute positions [t0, t1)
   const int t0 = q_off + i * kBM, t1 = imin(q_off + Nq, t0 + kBM);
-  const Range iv = interval_of(a.pat, g);
+  const Range iv = PAGED && a.Hkv <= kPagedIv ? a.iv[g] : interval_of(a.pat, g);
   // (a paged sequence longer than its cache: its last rows see the keys that there are)
   const Tiles T = PAGED ? part_of(plan_tiles(a.pat, iv, t0, imin(t1, Nk)), part, a.parts) : plan_tiles(a.pat, iv, t0, t1);
 
@@ -664,6 +720,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cowa_fwd_kernel(const __grid_c
       const float l = la + lb;
       // ---- epilogue
       if constexpr (PAGED) {
+        // (read again, so that they need no registers in the loop)
+        row0 = chunk.row0;
+        q_off = chunk.start;
+        h0 = chunk.g * grp + 2 * chunk.pair;
         if (ntiles == 0 && t < t1 && k < (has1 ? 2 : 1)) {  // no keys: an empty part, or past the cache and its band
           const size_t row = (size_t)(h0 + k) * a.total + row0 + t - q_off;
           if (a.parts > 1) {

@@ -153,6 +153,7 @@ struct FwdArgs {
   float2* part_ml;
   float* part_o;
   PageTab tab;
+  Range iv[kPagedIv];  // interval_of each KV head (more than kPagedIv heads: worked out on the device)
   const int32_t* q_start;
   void* o;
   int64_t o_sb, o_st, o_sh;

@@ -877,3 +877,40 @@ def test_status_of_workspaces_of_other_calls(cuda_device):
     assert cw.workspace_status(ws) == 0
     ws[12:16] = torch.tensor([1, 0, 0, 0], dtype=torch.uint8, device=cuda_device)
     assert cw.workspace_status(ws) == 0
+
+
+@pytest.mark.parametrize("Hq,Hkv,pat,chunks", [
+    # up to 64 (head, sequence)s, odd groups, intervals that some rows see in part
+    (24, 8, cw.Pattern(40, 200, 2500, 8), [(1900, 700), (0, 1), (130, 513), (2700, 90)]),
+    # .. repeated intervals of other ranks' heads, one sequence
+    (30, 6, cw.Pattern(0, 64, 2000, 4, kv_head_base=3, h_kv_global=12), [(700, 1300)]),
+    # .. 64 of them, most empty; a band longer than the cache, no long-range region
+    (24, 8, cw.Pattern(100, 2**31 - 1, 100, 1), [(0, 900), (1500, 0), (0, 0), (77, 300), (5, 2), (1, 0), (0, 0), (2000, 200)]),
+    # more: sequences by their positions
+    (24, 8, cw.Pattern(40, 200, 2500, 8), [(1200, 300), (0, 1), (130, 129), (2700, 90)] + [(3, 20)] * 5),
+])
+def test_chunks_of_more_work_than_the_gpu_holds(cuda_device, Hq, Hkv, pat, chunks):
+    """Calls of more than 148 (query tile, pair of heads)s, which are dealt out by their weight: each is
+    computed, once."""
+    d, ps, n = 64, 64, 44
+    lens, B = [r for _, r in chunks], len(chunks)
+    rng = np.random.default_rng(98)
+    (k64, kp), (v64, vp) = (host_and_device((120, ps, Hkv, d), x, cuda_device, 98) for x in ("k", "v"))
+    tabh = rng.integers(0, 120, (B, n)).astype(np.int32)
+    total = sum(lens)
+    assert (total // 128 + B) * Hkv * ((Hq // Hkv + 1) // 2) > 148
+    q64, q = host_and_device((total, Hq, d), "q", cuda_device, 98)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=cuda_device)
+    cu = np.cumsum([0] + lens)
+    ws = torch.zeros(1 << 24, dtype=torch.uint8, device=cuda_device)
+    out = torch.full((total, Hq, d), float("nan"), dtype=torch.bfloat16, device=cuda_device)
+    o, lse = cw.cowa_fwd_paged(q, kp, vp, torch.from_numpy(tabh).to(cuda_device), i32(cu.tolist()),
+                               i32([s for s, _ in chunks]), pat, out=out, workspace=ws)
+    assert cw.workspace_status(ws) == 0
+    for s, (start, rows) in enumerate(chunks):
+        if rows == 0:
+            continue
+        r = slice(cu[s], cu[s + 1])
+        k, _ = orp.gather_pages(k64, tabh[s:s + 1], start + rows)
+        v, _ = orp.gather_pages(v64, tabh[s:s + 1], start + rows)
+        assert_chunk(o[r], lse[:, r], q64[r], k[0], v[0], start, pat)
