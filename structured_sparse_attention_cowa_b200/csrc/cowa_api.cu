@@ -843,7 +843,7 @@ size_t cowa_fwd_paged_workspace_size(const cowa_pattern* pat, int n_seq, int tot
   if (n_seq < 1 || check_pattern(pat, H_kv, &p) != COWA_OK || check_heads(1, total, H_q, H_kv, d) != COWA_OK ||
       max_pages < 1 || page_size < 8 || page_size % 8 != 0 || (int64_t)max_pages * page_size > (1 << 30))
     return 0;
-  return kWsHeader + fwd_paged_bytes(fwd_paged_parts(p, n_seq, total, H_q, H_kv, d, max_pages, page_size), total, H_q, d);
+  return kWsHeader + fwd_paged_bytes(fwd_paged_cut(p, n_seq, total, H_q, H_kv, d, max_pages, page_size).parts, total, H_q, d);
 }
 
 cowa_status cowa_fwd_paged(const cowa_pattern* pat, int n_seq, int total, int Hq, int Hkv, int d,
@@ -860,7 +860,8 @@ cowa_status cowa_fwd_paged(const cowa_pattern* pat, int n_seq, int total, int Hq
   FwdArgs a;
   memset(&a, 0, sizeof(a));
   COWA_TRY(check_page_table(table, n_seq, &a.tab));
-  a.parts = fwd_paged_parts(p, n_seq, total, Hq, Hkv, d, table.max_pages, table.page_size);
+  const FwdCut cut = fwd_paged_cut(p, n_seq, total, Hq, Hkv, d, table.max_pages, table.page_size);
+  a.parts = cut.parts; a.solo = cut.solo;
   COWA_TRY(check_ws(ws, ws_bytes, kWsHeader + fwd_paged_bytes(a.parts, total, Hq, d)));
   if (a.parts > 1) {
     a.part_ml = reinterpret_cast<float2*>(reinterpret_cast<char*>(ws) + kWsHeader);

@@ -19,8 +19,9 @@
 // 128 rows, and fetches the boxes that some row of the query tile sees.  V rows that are not fetched,
 // or lie past the last key, are zeroed (their P is 0, but 0 times what memory holds may be NaN).  The
 // CTAs come heaviest first over all sequences (see find_chunk), and those with a single head, of an
-// odd group, last.  Where there are too few CTAs for the GPU (a short chunk behind a long prefix),
-// several share the key tiles of one (a.parts) and leave fp32 results that a second kernel joins.
+// odd group, last.  Where there are too few CTAs for the GPU (a short chunk behind a long prefix), a CTA
+// takes one head instead of two (a.solo), or several share the key tiles of one (a.parts) and leave fp32
+// results that a second kernel joins.
 // Registers: the kernel is compiled for 168 per thread (384 * 168 = 64512 at launch); the two
 // softmax warpgroups then raise theirs to 216 and the third lowers to 72
 // (2*128*216 + 128*72 = 64512), so a whole 128-column score row stays in registers.  The
@@ -79,7 +80,7 @@ struct FwdGeom {
 };
 
 // PAGED: what CTA `rank` (of all parts of a tile) works on; one warp.  Pairs of heads come before the single
-// heads of odd groups, which are half as much work.
+// heads of odd groups, which are half as much work (a.solo: there are single heads only).
 //   * Where all CTAs run at once (148 of them or fewer), or with more than 64 sequences: tile by tile of one
 //     sequence after the other.
 //   * Up to 64 (KV head, sequence)s: the (head, query tile)s in descending order of their keys, counted in
@@ -94,15 +95,15 @@ struct FwdGeom {
 // The offsets are clamped as in the sequence table of kernel_common.cuh.
 struct Chunk {
   int seq, tile, row0, len, start;  // seq -1: there is no work left
-  int g, pair;
+  int g, head, two;                 // the first query head within the group, and whether there is a second
 };
 constexpr int kSorted = 64;
 static_assert(kSorted <= kPagedIv, "the search takes the intervals from the arguments");
 __device__ __forceinline__ Chunk find_chunk(const FwdArgs& a, int rank) {
   constexpr unsigned kAll = 0xffffffffu;
-  const Chunk none{-1, 0, 0, 0, 0, 0, 0};
+  const Chunk none{-1, 0, 0, 0, 0, 0, 0, 0};
   const int lane = threadIdx.x & 31, cap = a.tab.max_pages * a.tab.page_size;
-  const int grp = a.Hq / a.Hkv, whole = grp >> 1;
+  const int grp = a.Hq / a.Hkv, pairs = a.solo ? 0 : grp >> 1, singles = grp - 2 * pairs;
   struct Seq {
     int row0, len, start, tiles;
   };
@@ -125,15 +126,20 @@ __device__ __forceinline__ Chunk find_chunk(const FwdArgs& a, int rank) {
     end = __shfl_sync(kAll, e, 31);
     return q;
   };
-  int pair = whole, g;
-  auto take_pair = [&](int n) -> bool {  // n: (head, tile)s; false: past the last work
-    if (rank < n * whole) {
-      pair = rank % whole;
-      rank /= whole;
+  int g, head;
+  bool two;
+  auto take_heads = [&](int n) -> bool {  // n: (KV head, tile)s; false: past the last work
+    two = rank < n * pairs;
+    if (two) {
+      head = 2 * (rank % pairs);
+      rank /= pairs;
       return true;
     }
-    rank -= n * whole;
-    return grp % 2 != 0 && rank < n;
+    rank -= n * pairs;
+    if (rank >= n * singles) return false;
+    head = 2 * pairs + rank % singles;
+    rank /= singles;
+    return true;
   };
   auto sum = [&](int x) { return (int)__reduce_add_sync(kAll, (unsigned)x); };
   // the lane of x's running sum over the lanes that holds place n (n < the sum), n then counting from its own
@@ -150,13 +156,13 @@ __device__ __forceinline__ Chunk find_chunk(const FwdArgs& a, int rank) {
   };
   auto hand = [&](const Seq& q, int l, int first, int tile) {
     return Chunk{first + l, tile, __shfl_sync(kAll, q.row0, l), __shfl_sync(kAll, q.len, l), __shfl_sync(kAll, q.start, l), g,
-                 pair};
+                 head, two};
   };
   if (gridDim.x > 148 && a.n_seq <= kSorted) {
     const Seq q0 = load(0);
     Seq q1 = {0, 0, 0, 0};
     if (a.n_seq > 32) q1 = load(32);
-    if (!take_pair(a.Hkv * (sum(q0.tiles) + sum(q1.tiles)))) return none;
+    if (!take_heads(a.Hkv * (sum(q0.tiles) + sum(q1.tiles)))) return none;
     const bool by_head = a.n_seq * (int64_t)a.Hkv <= kSorted;
     int band = 1 << 29, wide = 0;  // (all tiles in the band: their positions decide)
     if (by_head) {
@@ -198,7 +204,7 @@ __device__ __forceinline__ Chunk find_chunk(const FwdArgs& a, int rank) {
     const int tile = __shfl_sync(kAll, second ? n[1] - more1 : n[0] - more0, l) - 1 - nth;
     return s < 32 ? hand(q0, s, 0, tile) : hand(q1, s - 32, 32, tile);
   }
-  if (!take_pair((int)packed_tiles_bound(a.total, a.n_seq) * a.Hkv)) return none;
+  if (!take_heads((int)packed_tiles_bound(a.total, a.n_seq) * a.Hkv)) return none;
   g = rank % a.Hkv;
   rank /= a.Hkv;
   for (int first = 0; first < a.n_seq; first += 32) {
@@ -266,7 +272,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cowa_fwd_kernel(const __grid_c
   const int per_i = a.B * a.Hkv * npair;
   int i, row0 = 0, Nq = a.Nq, Nk = a.Nk, q_off = a.q_off;  // row0: first row of the sequence
   int pg_seq = 0, part = 0;
-  int pair, g, b = 0;
+  int head, g, b = 0;  // head: the first of the pair within the group
+  bool has1;
   __shared__ Chunk chunk;
   if constexpr (PAGED) {
     // (set up while the kernel before it in the stream ran; waits for that one's results here)
@@ -280,7 +287,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cowa_fwd_kernel(const __grid_c
     if (chunk.seq < 0) return;  // whole CTA, before any barrier or TMEM use
     pg_seq = chunk.seq;
     g = chunk.g;
-    pair = chunk.pair;
+    head = chunk.head;
+    has1 = chunk.two;
     i = chunk.tile;
     row0 = chunk.row0;
     Nq = chunk.len;
@@ -301,12 +309,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cowa_fwd_kernel(const __grid_c
       q_off = 0;
     }
     int rem = blockIdx.x % per_i;
-    pair = rem % npair; rem /= npair;
+    head = 2 * (rem % npair); rem /= npair;
+    has1 = head + 1 < grp;
     g = rem % a.Hkv;
     b = rem / a.Hkv;
   }
-  int h0 = g * grp + 2 * pair;
-  const bool has1 = (2 * pair + 1) < grp;
+  int h0 = g * grp + head;
   // query rows of the tile: local q rows [i*BM, ...), absolute positions [t0, t1)
   const int t0 = q_off + i * kBM, t1 = imin(q_off + Nq, t0 + kBM);
   const Range iv = PAGED && a.Hkv <= kPagedIv ? a.iv[g] : interval_of(a.pat, g);
@@ -723,7 +731,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cowa_fwd_kernel(const __grid_c
         // (read again, so that they need no registers in the loop)
         row0 = chunk.row0;
         q_off = chunk.start;
-        h0 = chunk.g * grp + 2 * chunk.pair;
+        h0 = chunk.g * grp + chunk.head;
         if (ntiles == 0 && t < t1 && k < (has1 ? 2 : 1)) {  // no keys: an empty part, or past the cache and its band
           const size_t row = (size_t)(h0 + k) * a.total + row0 + t - q_off;
           if (a.parts > 1) {
@@ -935,7 +943,7 @@ cudaError_t launch_fwd_d(const FwdArgs& a, cudaStream_t s) {
   // packed batch: an upper bound on the q-tiles (sum of ceil(len/BM) <= total/BM + n_seq); the
   // sequence table is computed on the device first
   const long long nq = a.varlen ? packed_tiles_bound(a.total, a.n_seq) : (a.Nq + kBM - 1) / kBM;
-  const long long nblk = nq * a.B * a.Hkv * ((grp + 1) / 2);
+  const long long nblk = nq * a.B * a.Hkv * (PAGED && a.solo ? grp : (grp + 1) / 2) * (PAGED ? a.parts : 1);
   if (nblk > 0x7fffffffLL) return cudaErrorInvalidValue;
   // the in-kernel register split assumes the compiled count equals the launch allocation
   static int regs_ok = -1;
@@ -950,7 +958,7 @@ cudaError_t launch_fwd_d(const FwdArgs& a, cudaStream_t s) {
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(nblk * a.parts));
+    cfg.gridDim = dim3((unsigned)nblk);
     cfg.blockDim = dim3(kFwdThreads);
     cfg.dynamicSmemBytes = Geo::kSmem;
     cfg.stream = s;
@@ -976,25 +984,41 @@ cudaError_t launch_seq_table(const int32_t* cu_seqlens, int n_seq, int total, in
   return cudaGetLastError();
 }
 
-// Parts that the key tiles of a paged call's CTAs are cut into: as many as leave every CTA a tile and an SM
-// of its own, with at most kPartBytes of partial results (which cost their writing and reading).  1: no cut.
-// 16 rows behind 32K keys (40/8 heads) 110 -> 32 us, 300 rows behind 4K (4/1 heads) 69 -> 24, 60 behind 1K
-// (2/2 heads, d = 64) 17.8 -> 12.4 (15.0 with three tiles a part at least).
-int fwd_paged_parts(const Pat& p, int n_seq, int total, int Hq, int Hkv, int d, int max_pages, int page_size) {
-  constexpr int64_t kPartBytes = 12 << 20;
+// How the work of a paged call is cut: the parts of its CTAs' key tiles (1: no cut; at most kPartBytes of
+// partial results), and whether a CTA takes one query head instead of two.  A pair of heads is the better use
+// of a key tile (4K rows behind 28K keys: 468 us in pairs, 547 with single heads), but fewer CTAs of longer
+// work.  The form with the least estimated time is taken, from what the host knows: bounds of the query tiles
+// and of the longest list of key tiles.  In us, d = 128 (3/4 of it a tile at d = 64):
+//   key tiles of a part x (1.65 a pair of heads, 1.2 a single one)
+//   + where the CTAs take turns, 4 + a turn beyond the first x (8 + 1/5 of that: the longest come first)
+//   + where parts are joined, 3 + their bytes at 3.5 TB/s
+// Measured against pairs in as many parts as all run at once: 50 calls 10% less time in the mean (3% more than
+// the best of all forms), 52 others 9% less, the worst of them 22 -> 26 us, the most 204 -> 119 (357 rows of 6
+// sequences, 32/4 heads: two parts) and 35 -> 23 (339 rows of 5, 20/4 heads: single heads); 16 rows behind 32K
+// keys (40/8 heads) 110 -> 32 (parts).
+FwdCut fwd_paged_cut(const Pat& p, int n_seq, int total, int Hq, int Hkv, int d, int max_pages, int page_size) {
+  constexpr int64_t kPartBytes = 15 << 20;
+  constexpr int kMaxParts = 32;  // (a lane each when they are joined)
   const int64_t cap = (int64_t)max_pages * page_size, R = (int64_t)p.T - p.S;
   const int64_t wide = R > 0 ? (R + p.H - 1) / p.H : 0;
   auto tiles = [&](int64_t n) { return n > 0 ? ((n < cap ? n : cap) + kBN - 1) / kBN + 1 : 0; };
   int64_t n = tiles(p.S) + tiles(wide) + tiles((int64_t)p.L + kBM);
   const int64_t all = (cap + kBN - 1) / kBN;
   n = n < all ? n : all;
-  const int64_t ctas = packed_tiles_bound(total, n_seq) * Hkv * ((Hq / Hkv + 1) / 2);
-  int64_t parts = 148 / ctas;
-  if (parts > n) parts = n;
-  const int64_t bytes = (int64_t)Hq * total * (d + 2) * sizeof(float);
-  if (parts > kPartBytes / bytes) parts = kPartBytes / bytes;
-  if (parts > 32) parts = 32;  // (a lane each when they are joined)
-  return parts < 1 ? 1 : (int)parts;
+  const int grp = Hq / Hkv;
+  const double work = (double)packed_tiles_bound(total, n_seq) * Hkv, bytes = (double)Hq * total * (d + 2) * sizeof(float);
+  FwdCut best{1, 0};
+  double least = 1e30;
+  for (int solo = 0; solo < (grp > 1 ? 2 : 1); ++solo)
+    for (int parts = 1; parts <= kMaxParts && parts <= n && (parts == 1 || parts * bytes <= kPartBytes); ++parts) {
+      const double longest = (double)((n + parts - 1) / parts) * (solo ? 1.2 : 1.65) * (d == 128 ? 1.0 : 0.75);
+      const double turns = work * (solo ? grp : (grp + 1) / 2) * parts / 148;
+      double us = longest;
+      if (turns > 1) us += 4 + (turns - 1) * (8 + 0.2 * longest);
+      if (parts > 1) us += 3 + parts * bytes / 3.5e6;
+      if (us < least) { least = us; best = FwdCut{parts, solo}; }
+    }
+  return best;
 }
 
 size_t fwd_paged_bytes(int parts, int total, int Hq, int d) {

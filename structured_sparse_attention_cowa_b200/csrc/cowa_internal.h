@@ -150,6 +150,7 @@ struct FwdArgs {
   // parts > 1: each CTA's key tiles are cut into so many parts, whose results go to part_ml (running max
   // in log2 units and sum, [parts][Hq][total]) and part_o ([parts][Hq][total][d])
   int parts;
+  int solo;  // != 0: a CTA takes one query head, not two
   float2* part_ml;
   float* part_o;
   PageTab tab;
@@ -163,7 +164,10 @@ struct FwdArgs {
   CUtensorMap tm_q, tm_k, tm_v;
 };
 cudaError_t launch_fwd(const FwdArgs& a, cudaStream_t s);
-int fwd_paged_parts(const Pat& p, int n_seq, int total, int Hq, int Hkv, int d, int max_pages, int page_size);
+struct FwdCut {
+  int parts, solo;
+};
+FwdCut fwd_paged_cut(const Pat& p, int n_seq, int total, int Hq, int Hkv, int d, int max_pages, int page_size);
 size_t fwd_paged_bytes(int parts, int total, int Hq, int d);
 
 // ---- packed variable-length batches ----

@@ -914,3 +914,44 @@ def test_chunks_of_more_work_than_the_gpu_holds(cuda_device, Hq, Hkv, pat, chunk
         k, _ = orp.gather_pages(k64, tabh[s:s + 1], start + rows)
         v, _ = orp.gather_pages(v64, tabh[s:s + 1], start + rows)
         assert_chunk(o[r], lse[:, r], q64[r], k[0], v[0], start, pat)
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,T,parts,chunks", [
+    (20, 4, 64, 1000, 1, [(1200, 500), (1900, 380)]),                             # single heads, taking turns
+    (3, 1, 64, 1000, 6, [(2000, 200), (0, 1), (700, 0), (300, 140), (2600, 5)]),  # single heads, cut
+    (8, 1, 128, 1000, 2, [(1500, 1279)]),                                         # single heads, cut, taking turns
+    (20, 4, 64, 1000, 2, [(2600, 100), (0, 50), (9, 0), (9, 1), (1000, 27), (2222, 60), (40, 40)]),  # pairs, the same
+])
+def test_chunks_in_other_cuts(cuda_device, Hq, Hkv, d, T, parts, chunks):
+    """Calls whose CTAs take single heads, or parts of the key tiles, or both, and where these take turns on the
+    GPU; then with a bad page under the first sequence's sinks, which empties that sequence alone."""
+    ps, n, pat = 64, 44, cw.Pattern(100, 2000, T, 1)
+    lens, B = [r for _, r in chunks], len(chunks)
+    rng = np.random.default_rng(99)
+    (k64, kp), (v64, vp) = (host_and_device((120, ps, Hkv, d), x, cuda_device, 99) for x in ("k", "v"))
+    tabh = rng.integers(0, 120, (B, n)).astype(np.int32)
+    total = sum(lens)
+    size = cw.lib().cowa_fwd_paged_workspace_size(ctypes.byref(pat.c()), B, total, Hq, Hkv, d, n, ps)
+    per_part = Hq * total * (d + 2) * 4  # (and the alignment of what each part keeps)
+    assert 0 <= size - 256 - (parts > 1) * parts * per_part < 256
+    q64, q = host_and_device((total, Hq, d), "q", cuda_device, 99)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=cuda_device)
+    cu = np.cumsum([0] + lens)
+    ws = torch.zeros(size, dtype=torch.uint8, device=cuda_device)
+    run = lambda tab: cw.cowa_fwd_paged(q, kp, vp, torch.from_numpy(tab).to(cuda_device), i32(cu.tolist()),
+                                        i32([s for s, _ in chunks]), pat, workspace=ws)
+    o, lse = run(tabh)
+    assert cw.workspace_status(ws) == 0
+    for s, (start, rows) in enumerate(chunks):
+        if rows == 0:
+            continue
+        r = slice(cu[s], cu[s + 1])
+        k, _ = orp.gather_pages(k64, tabh[s:s + 1], start + rows)
+        v, _ = orp.gather_pages(v64, tabh[s:s + 1], start + rows)
+        assert_chunk(o[r], lse[:, r], q64[r], k[0], v[0], start, pat)
+    bad = tabh.copy()
+    bad[0, 0] = 120
+    ob, lb = run(bad)
+    assert cw.workspace_status(ws) == 8
+    assert (ob[:cu[1]] == 0).all() and (lb[:, :cu[1]] == -float("inf")).all()
+    assert torch.equal(ob[cu[1]:], o[cu[1]:]) and torch.equal(lb[:, cu[1]:], lse[:, cu[1]:])
