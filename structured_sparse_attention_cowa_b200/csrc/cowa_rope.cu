@@ -345,11 +345,22 @@ cudaError_t launch_turn(const RopeArgs& a, cudaStream_t s) {
   const int units = cut == kSplit ? a.half / 8 + (a.d - rd) / 8 : (cut == kInter ? a.d / 16 : a.d / 8);
   const int heads = a.Hq + (MODE == kTurn ? 1 : 2) * a.Hk;
   const int lanes = kThreadsOf<MODE> / units;
-  // tokens per block: enough rows to fill its threads, but no fewer blocks than the SMs can hold
+  // Tokens per block: what takes the fewest passes over rows, in the turns that the blocks take on the SMs; a
+  // block's start costs about half a pass, an angle a thread 0.2 (in 64 bits 0.6), one more block on an SM
+  // 0.1.  (Against powers of two as large as leave eight blocks an SM: 4K tokens of 32/8 heads 18.3 -> 16.6 us
+  // with 7, 2K of 40/8 13.0 -> 11.1 with 4, 8K appended as E4M3 codes 41.2 -> 39.9 with 7, 7.5K of 8/1
+  // appended in bf16 15.7 -> 12.3; 32K the same.)
   int tok = 1;
-  while (tok < kMaxTok && (tok * heads < lanes || (a.M + 2 * tok - 1) / (2 * tok) >= 148 * 8) &&
-         smem_bytes(MODE, 2 * tok, a.half, a.Hk) <= 32 * 1024)
-    tok *= 2;
+  double least = 1e30;
+  for (int n = 1; n <= kMaxTok && (n == 1 || smem_bytes(MODE, n, a.half, a.Hk) <= 32 * 1024); ++n) {
+    const int at_once = 148 * imin(1024 / kThreadsOf<MODE>, (int)(228 * 1024 / (smem_bytes(MODE, n, a.half, a.Hk) + 1024)));
+    const long long blocks = (a.M + n - 1) / n, turns = (blocks + at_once - 1) / at_once;
+    const long long rows = (long long)lanes * (cut == kAny ? 2 : 1), passes = ((long long)n * heads + rows - 1) / rows;
+    const int angles = (n * a.half + kThreadsOf<MODE> - 1) / kThreadsOf<MODE>;  // a thread's
+    const double cost = (double)turns * (passes + 0.5 + (MODE == kPagesE4m3 ? 0.6 : 0.2) * angles) +
+                        0.1 * ((blocks + 147) / 148);
+    if (cost < least || (cost == least && turns > 1)) { least = cost; tok = n; }
+  }
   const long long blocks = (a.M + tok - 1) / tok;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   const size_t smem = smem_bytes(MODE, tok, a.half, a.Hk);

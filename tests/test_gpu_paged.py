@@ -955,3 +955,25 @@ def test_chunks_in_other_cuts(cuda_device, Hq, Hkv, d, T, parts, chunks):
     assert cw.workspace_status(ws) == 8
     assert (ob[:cu[1]] == 0).all() and (lb[:, :cu[1]] == -float("inf")).all()
     assert torch.equal(ob[cu[1]:], o[cu[1]:]) and torch.equal(lb[:, cu[1]:], lse[:, cu[1]:])
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("total,Hq,Hkv", [(2400, 40, 8), (1822, 8, 1), (4003, 0, 2)])
+def test_tokens_are_appended_alike_however_many(cuda_device, total, Hq, Hkv, e4m3):
+    """How many tokens a block owns depends on the call's size: the same queries and pages as from calls of 100
+    tokens."""
+    d, ps = 128, 16
+    n = (total + ps - 1) // ps
+    rope = cw.Rope(cw.rope_frequencies(96, device=cuda_device))
+    _, qkv = host_and_device((total, Hq + 2 * Hkv, d), "q", cuda_device, 83)
+    q, k, v = qkv.split([Hq, Hkv, Hkv], dim=1)
+    i32 = lambda x: torch.from_numpy(x.astype(np.int32)).to(cuda_device)
+    rng = np.random.default_rng(84)
+    tab, pos, seq = i32(rng.permutation(n)[None]), i32(rng.permutation(total)), i32(np.zeros(total))
+    pools = [torch.zeros((n, ps, Hkv, d), dtype=torch.uint8 if e4m3 else torch.bfloat16, device=cuda_device) for _ in range(4)]
+    fn, scales = (cw.paged_append_fp8, (0.02, 0.03)) if e4m3 else (cw.paged_append, ())
+    put = lambda s, kp, vp: fn(q[s] if Hq else None, k[s], v[s], pos[s], kp, vp, tab, *scales, rope=rope, seq=seq[s])
+    got = put(slice(0, total), *pools[:2])
+    parts = [put(slice(i, i + 100), *pools[2:]) for i in range(0, total, 100)]
+    assert got is None if Hq == 0 else torch.equal(got, torch.cat(parts))
+    assert torch.equal(pools[0], pools[2]) and torch.equal(pools[1], pools[3]) and pools[0].any()

@@ -212,3 +212,22 @@ def test_no_memory_for_an_output(cuda_device):
     q = torch.zeros((1, 1, 1, 128), dtype=torch.bfloat16, device=cuda_device).expand(1, 1 << 30, 64, 128)
     with pytest.raises(torch.OutOfMemoryError):
         cw.cowa_rope(q, None, cw.Rope(f))
+
+
+@pytest.mark.parametrize("B,N,Hq,Hkv,d,r,inter", [
+    (4, 1025, 32, 8, 128, 128, False), (2, 1000, 40, 8, 128, 96, True), (3, 500, 5, 1, 64, 30, False), (1, 868, 1, 1, 128, 64, True),
+])
+def test_tokens_are_rotated_alike_however_many(cuda_device, B, N, Hq, Hkv, d, r, inter):
+    """How many tokens a block owns depends on the call's size, what a token becomes does not: the same bits as
+    from calls of 100 tokens."""
+    f, _ = freq_of(r, cuda_device)
+    rope = cw.Rope(f, (r // 2 - 3, 3), interleaved=inter)
+    _, q = host_and_device((B, N, Hq, d), "q", cuda_device, 67)
+    _, k = host_and_device((B, N, Hkv, d), "k", cuda_device, 67)
+    pos = torch.from_numpy(np.random.default_rng(N).integers(-9, 99999, (2, B, N)).astype(np.int32)).to(cuda_device)
+    gq, gk = cw.cowa_rope(q, k, rope, pos)
+    for b in range(B):
+        for t in range(0, N, 100):
+            s = slice(t, t + 100)
+            wq, wk = cw.cowa_rope(q[b:b + 1, s], k[b:b + 1, s], rope, pos[:, b:b + 1, s])
+            assert torch.equal(gq[b:b + 1, s], wq) and torch.equal(gk[b:b + 1, s], wk)
