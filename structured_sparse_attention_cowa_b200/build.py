@@ -64,7 +64,7 @@ def build_binding(verbose: bool = False) -> str:
     inc = [*ext.include_paths(), os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            *("-isystem" + i for i in inc), src, "-o", BINDING, *("-L" + p for p in ext.library_paths()), "-lc10",
-           "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_python"]
+           "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)

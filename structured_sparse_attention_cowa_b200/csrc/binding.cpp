@@ -10,6 +10,7 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <dlfcn.h>
@@ -166,6 +167,12 @@ Rotary rotary(PyObject* address, PyObject* freq) {
   return r;
 }
 
+// A contiguous tensor on x's device, past the dispatcher (0.7 us less than at::empty_like)
+at::Tensor fresh(const at::Tensor& x, at::IntArrayRef shape, at::ScalarType type) {
+  return at::Tensor(at::detail::empty_cuda(shape, type, x.device(), std::nullopt));
+}
+at::Tensor fresh_like(const at::Tensor& x) { return fresh(x, x.sizes(), x.scalar_type()); }
+
 void* stream_of(const at::Tensor& x) { return c10::cuda::getCurrentCUDAStream(x.get_device()).stream(); }
 
 // (status, object, ...): the object given, or the tensor made in its place
@@ -258,8 +265,8 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     same_device(x, {k, pos, qo, ko, r.freq});
     const c10::cuda::CUDAGuard guard(x.device());
     at::Tensor mq, mk;
-    if (q && !qo) qo = &(mq = at::empty_like(*q, at::MemoryFormat::Contiguous));
-    if (k && !ko) ko = &(mk = at::empty_like(*k, at::MemoryFormat::Contiguous));
+    if (q && !qo) qo = &(mq = fresh_like(*q));
+    if (k && !ko) ko = &(mk = fresh_like(*k));
     const cowa_tensor none{nullptr, 0, 0, 0};
     const int status = (PyObject_IsTrue(a[0]) ? lib.rope_bwd : lib.rope)(
         r.c, to_int(B), to_int(N), q ? to_int(q->size(2)) : 0, k ? to_int(k->size(2)) : 0, to_int(x.size(3)),
@@ -312,7 +319,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     same_device(k, {q, &v, &pos, seq, rp, qo, &kp, &vp, &tab, r.freq});
     const c10::cuda::CUDAGuard guard(k.device());
     at::Tensor made;
-    if (q && !qo) qo = &(made = at::empty_like(*q, at::MemoryFormat::Contiguous));
+    if (q && !qo) qo = &(made = fresh_like(*q));
     const cowa_tensor none{nullptr, 0, 0, 0}, qt = q ? rows(*q, "q") : none, qot = qo ? rows(*qo, "q_out") : none;
     const int Hq = q ? to_int(q->size(1)) : 0;
     int status;
@@ -364,8 +371,8 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     same_device(q, {&kp, &vp, &tab, &pos, out, lse, ws});
     const c10::cuda::CUDAGuard guard(q.device());
     at::Tensor mo, ml, mw;
-    if (!out) out = &(mo = at::empty_like(q));
-    if (!lse && PyObject_IsTrue(a[11])) lse = &(ml = at::empty({B, Hq}, q.options().dtype(at::kFloat)));
+    if (!out) out = &(mo = fresh_like(q));
+    if (!lse && PyObject_IsTrue(a[11])) lse = &(ml = fresh(q, {B, Hq}, at::kFloat));
     const int b = to_int(B), hq = to_int(Hq), di = to_int(d);
     if (!ws) {
       const size_t bytes = (codes ? lib.decode_fp8_size : lib.decode_size)(&pat, b, hq, p.Hkv, di, p.table.max_pages,
@@ -405,8 +412,8 @@ PyObject* fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     same_device(q, {&kp, &vp, &tab, &cu, &start, out, lse, ws});
     const c10::cuda::CUDAGuard guard(q.device());
     at::Tensor mo, ml, mw;
-    if (!out) out = &(mo = at::empty_like(q, at::MemoryFormat::Contiguous));
-    if (!lse) lse = &(ml = at::empty({Hq, total}, q.options().dtype(at::kFloat)));
+    if (!out) out = &(mo = fresh_like(q));
+    if (!lse) lse = &(ml = fresh(q, {Hq, total}, at::kFloat));
     const int t = to_int(total), hq = to_int(Hq), di = to_int(d);
     if (!ws) {
       const size_t bytes = lib.fwd_size(&pat, p.n_seq, t, hq, p.Hkv, di, p.table.max_pages, p.table.page_size);
