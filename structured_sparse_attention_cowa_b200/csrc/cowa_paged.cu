@@ -251,6 +251,14 @@ __device__ __forceinline__ float cluster_ld(const float* own, int rank) {  // th
   return v;
 }
 
+// Element d of a row's result, from its maximum, sum and unscaled O.  The sum is 0 only if the row saw nothing
+// (o 0, lse -inf); where all scores were NaN the maximum is still -inf, but the sum is NaN, and so is the row.
+template <int D>
+__device__ __forceinline__ void put_row(const PagedDecodeArgs& a, size_t h, int d, float m, float l, float o) {
+  reinterpret_cast<__nv_bfloat16*>(a.o)[h * D + d] = __float2bfloat16_rn(l == 0.f ? 0.f : o / l);
+  if (a.lse && d == 0) a.lse[h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
+}
+
 // CL: CTAs c, c + 1, .. of a cluster of a.cluster share one pair; else every CTA has its share of the list.
 template <int D, bool KV8, bool CL, bool BIG>
 __global__ void __launch_bounds__(kThreads, Geo<D, KV8, BIG>::kCtas)
@@ -671,8 +679,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV8, BIG>::kCtas)
           }
           if (KV8) o *= a.v_scale;
           if (!CL && begins && ends) {  // the pair is finished here
-            reinterpret_cast<__nv_bfloat16*>(a.o)[(size_t)(h0 + hd) * D + d] = __float2bfloat16_rn(m == -INFINITY ? 0.f : o / l);
-            if (a.lse && d == 0) a.lse[h0 + hd] = m == -INFINITY ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
+            put_row<D>(a, (size_t)(h0 + hd), d, m, l, o);
           } else {
             part[hd * (D + 2) + 2 + d] = o;
             if (d == 0) { part[hd * (D + 2)] = m; part[hd * (D + 2) + 1] = l; }
@@ -704,6 +711,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV8, BIG>::kCtas)
 #pragma unroll
       for (int r = 0; r < kMaxCluster; ++r) {
         mr[r] = -INFINITY;
+        lr[r] = 0.f;
         if (r < k) mr[r] = cluster_ld(p, r);
       }
 #pragma unroll
@@ -716,14 +724,12 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV8, BIG>::kCtas)
       for (int r = 0; r < kMaxCluster; ++r) m = fmaxf(m, mr[r]);
 #pragma unroll
       for (int r = 0; r < kMaxCluster; ++r) {
-        if (mr[r] == -INFINITY) continue;  // (no such CTA, or its outputs were not written)
-        const float f = ptx::ex2(mr[r] - m);
-        l += f * lr[r];
-        o += f * om[r];
+        const float f = mr[r] == -INFINITY ? 0.f : ptx::ex2(mr[r] - m);
+        l += f * lr[r];  // (0 times NaN is NaN: a CTA that saw nothing else still counts)
+        if (mr[r] != -INFINITY) o += f * om[r];  // (no such CTA, or its outputs were not written)
       }
       const size_t h = (size_t)first_item * grp + hd;
-      reinterpret_cast<__nv_bfloat16*>(a.o)[h * D + d] = __float2bfloat16_rn(m == -INFINITY ? 0.f : o / l);
-      if (a.lse && d == 0) a.lse[h] = m == -INFINITY ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
+      put_row<D>(a, h, d, m, l, o);
     }
     __syncwarp();
     cluster_sync();  // no CTA leaves while another still reads from it
@@ -771,8 +777,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const __gri
   float o = so[0][d];
   for (int w = 1; w < warps; ++w) { l += sl[w]; o += so[w][d]; }
   const size_t h = (size_t)rec.x * a.grp + hd;
-  reinterpret_cast<__nv_bfloat16*>(a.o)[h * D + d] = __float2bfloat16_rn(m == -INFINITY ? 0.f : o / l);
-  if (a.lse && d == 0) a.lse[h] = m == -INFINITY ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
+  put_row<D>(a, h, d, m, l, o);
 }
 
 template <int D, bool KV8, bool BIG>
