@@ -761,9 +761,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cowa_fwd_kernel(const __grid_c
       if (!split) {
         if (ok && ntiles > 0 && ptx::mbar_wait_warp(&o_done[k], 0, &abort_flag, a.status)) {
           ptx::tc_fence_after();
-          // (a paged row may see nothing, or its query tile a bad page)
+          // (a paged row may see nothing, or its query tile a bad page.  The sum tells the first: it is 0 then,
+          // and NaN where all scores were, which leave the maximum at -inf too)
           const bool bad = PAGED && *reinterpret_cast<volatile int*>(&bad_page);
-          const bool none = PAGED && (m_used == -INFINITY || bad);
+          const bool none = PAGED && (l == 0.f || bad);
           const float inv = 1.f / l;
           const bool partial = PAGED && a.parts > 1;
           if (t < t1) {
@@ -810,7 +811,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cowa_fwd_kernel(const __grid_c
         const float f1 = m1 == -INFINITY ? 0.f : ptx::ex2(m1 - m);
         const float lt = l * f0 + l1 * f1;
         const bool bad = PAGED && *reinterpret_cast<volatile int*>(&bad_page);
-        const bool none = PAGED && (m == -INFINITY || bad), partial = PAGED && a.parts > 1;
+        const bool none = PAGED && (lt == 0.f || bad), partial = PAGED && a.parts > 1;
         const float inv = partial ? 1.f : 1.f / lt, g0 = f0 * inv, g1 = f1 * inv;
         const bool two = ntiles > 1;  // slot 1 has tiles (uniform over the CTA)
         if (t < t1 && partial) a.part_ml[part_row(h0)] = make_float2(m, bad ? -1.f : lt);
@@ -923,7 +924,7 @@ __global__ void __launch_bounds__(256) fwd_join_kernel(const __grid_constant__ F
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] += w * x[e];
   }
-  const bool none = bad || m == -INFINITY;
+  const bool none = bad || l == 0.f;  // (a part of NaN scores only has the maximum -inf, but the sum NaN)
   uint32_t w[E / 2];
 #pragma unroll
   for (int e = 0; e < E / 2; ++e) w[e] = none ? 0u : ptx::pack_bf16(acc[2 * e] / l, acc[2 * e + 1] / l);

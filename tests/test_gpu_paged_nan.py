@@ -3,6 +3,8 @@ exact softmax attention does (and the contiguous forward's and decode's o), howe
 sees NaN only must not pass for one that sees nothing (o 0, lse -inf), and a piece of the work that holds
 nothing but NaN must not be dropped when the pieces are joined.  Rows that do not see it keep their bits."""
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -89,3 +91,56 @@ def test_decode_of_a_nan_value(cuda_device, e4m3, wide):
     hit = torch.zeros_like(o, dtype=torch.bool)
     hit[0, :5, 5] = True
     assert o[hit].isnan().all() and torch.equal(o[~hit], wo[~hit]) and torch.equal(lse, wl)
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,rows,parts", [
+    (40, 8, 128, 1000, False),   # pairs of heads and single ones, not cut
+    (24, 24, 64, 1000, False),   # single heads
+    (3, 1, 64, 300, True),       # key tiles cut into parts
+    (2, 1, 128, 300, True),
+])
+def test_chunk_of_nan_queries_and_keys(cuda_device, Hq, Hkv, d, rows, parts):
+    """Query rows that are NaN, and a key that is NaN: the rows that see it, in the heads it belongs to.  Not cut:
+    key 0 is a sink, which all rows see (alone in its tile for the far ones), the others are seen through a band
+    of 50.  Cut: every key up to the row."""
+    ps, n, start, total = 16, 128, 900, rows + 10
+    pat = cw.Pattern(1, 50, 2000 if parts else 1, 1)
+    tab = torch.from_numpy(make_table(np.random.default_rng(121), 1, n)[0]).to(cuda_device)
+    kp, vp = (host_and_device((n + 2, ps, Hkv, d), x, cuda_device, 121)[1] for x in ("k", "v"))
+    q = host_and_device((total, Hq, d), "q", cuda_device, 121)[1]
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=cuda_device)
+    size = cw.lib().cowa_fwd_paged_workspace_size(ctypes.byref(pat.c()), 1, total, Hq, Hkv, d, n, ps)
+    assert (size > 256) == parts
+    ws = torch.zeros(size, dtype=torch.uint8, device=cuda_device)
+
+    def run(q, kp):
+        out, lse = torch.zeros_like(q), torch.zeros((Hq, total), device=cuda_device)
+        cw.cowa_fwd_paged(q, kp, vp, tab, i32([0, rows]), i32([start]), pat, out=out, lse=lse, workspace=ws)
+        assert cw.workspace_status(ws) == 0
+        return out, lse.t()
+
+    def check(got, want, hit):
+        (o, lse), (wo, wl) = got, want
+        assert o[hit].isnan().all() and lse[hit].isnan().all()
+        assert torch.equal(o[~hit], wo[~hit]) and torch.equal(lse[~hit], wl[~hit])
+
+    want = run(q, kp)
+    assert not any(x.isnan().any() for x in want)
+    bad = q.clone()
+    bad[17, 1, 3] = bad[128, 0, 0] = bad[rows - 1, Hq - 1, 1] = NAN
+    hit = torch.zeros((total, Hq), dtype=torch.bool, device=cuda_device)
+    hit[17, 1] = hit[128, 0] = hit[rows - 1, Hq - 1] = True
+    check(run(bad, kp), want, hit)
+    for key, seen in ((0, slice(0, rows)), (1000, slice(100, 150) if not parts else slice(100, rows))):
+        bad = kp.clone()
+        bad[int(tab[0, key // ps]), key % ps, 0, 2] = NAN
+        hit = torch.zeros((total, Hq), dtype=torch.bool, device=cuda_device)
+        hit[seen, :Hq // Hkv] = True
+        check(run(q, bad), want, hit)
+    # nothing but NaN in a tile of keys that some rows see in part: all keys of the last 64 positions
+    bad = kp.clone()
+    for key in range(start + rows - 64, start + rows):
+        bad[int(tab[0, key // ps]), key % ps, 0] = NAN
+    hit = torch.zeros((total, Hq), dtype=torch.bool, device=cuda_device)
+    hit[rows - 64:rows, :Hq // Hkv] = True
+    check(run(q, bad), want, hit)
