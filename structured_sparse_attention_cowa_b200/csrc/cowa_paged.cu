@@ -70,7 +70,8 @@ struct Geo {
   static constexpr int kOffBar = kStages * 2 * kTileBytes;
   static_assert(3 * kStages <= 16, "the block's own words start at word 16");
   static constexpr int kOffRed = kOffBar + kBarBytes;
-  static int smem(int grp) { return kOffRed + kWarps * grp * (D + 2) * 4; }
+  static constexpr int smem(int grp) { return kOffRed + kWarps * grp * (D + 2) * 4; }
+  static constexpr int kMostSmem = smem(KV8 && !BIG ? 5 : 8);  // of the largest group
   // of an SM's 228 KB a block takes its shared memory and 1 KB more
   static int ctas(int grp) { return imin(kCtas, (228 * 1024) / (smem(grp) + 1024)); }
 };
@@ -794,9 +795,12 @@ cudaError_t launch_paged_t(const PagedDecodeArgs& a, cudaStream_t s) {
   cfg.attrs = at;
   cfg.numAttrs = 1;
   cudaError_t e;
+  // (what a kernel may ask for is set to the same value by every call: calls of other groups may be between
+  // this and their launch in other threads)
+  constexpr int most = Geo<D, KV8, BIG>::kMostSmem;
   if (a.cluster > 0) {
     auto kern = paged_split_kernel<D, KV8, true, BIG>;
-    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most)) != cudaSuccess) return e;
     if (a.cluster > 8 &&
         (e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
       return e;
@@ -808,7 +812,7 @@ cudaError_t launch_paged_t(const PagedDecodeArgs& a, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, kern, a);
   }
   auto kern = paged_split_kernel<D, KV8, false, BIG>;
-  if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
+  if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most)) != cudaSuccess) return e;
   cfg.gridDim = dim3(a.grid);
   if ((e = cudaLaunchKernelEx(&cfg, kern, a)) != cudaSuccess) return e;
   // a pair in many pieces is one of few: more warps for it
