@@ -7,7 +7,8 @@ structured_sparse_attention_cowa_b200/libcowa.so (static CUDA runtime; the
 driver API is reached through cudaGetDriverEntryPoint, so no -lcuda).
 csrc/binding.cpp, the part of the Python binding that is compiled, becomes
 _binding.so beside it (against the installed torch; it finds either library's
-entry points at run time).  Objects are rebuilt only when a source or header is newer.
+entry points at run time; without torch it is left out).  Objects are rebuilt only when a source or
+header is newer.
 
 --debug builds libcowa_debug.so with COWA_DEBUG=1: the kernels check every planned tile and
 cache row against the call's tensors before loading it, and a failed check is reported as
@@ -19,6 +20,7 @@ from __future__ import annotations
 
 import argparse
 import glob
+import importlib.util
 import os
 import subprocess
 import sys
@@ -109,7 +111,6 @@ def build(debug: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             sys.stderr.write(r.stdout + r.stderr)
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed on {os.path.basename(src)}")
-    build_binding(verbose)
     out = LIB_DEBUG if debug else LIB
     lib_t = os.path.getmtime(out) if os.path.exists(out) else -1
     if lib_t < max(os.path.getmtime(o) for o in objs):
@@ -120,6 +121,11 @@ def build(debug: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         if r.returncode != 0:
             sys.stderr.write(r.stdout + r.stderr)
             raise RuntimeError(f"link of {os.path.basename(out)} failed")
+    # after the library, which needs neither torch nor g++
+    if importlib.util.find_spec("torch") is None:
+        sys.stderr.write("torch is not installed: _binding.so, which only a program with torch can use, is not built\n")
+    else:
+        build_binding(verbose)
     return out
 
 
