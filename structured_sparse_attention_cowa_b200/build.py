@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import argparse
 import glob
+import hashlib
 import importlib.util
 import os
 import subprocess
@@ -51,28 +52,49 @@ def _newest_header() -> float:
     return max((os.path.getmtime(h) for h in hdrs), default=0.0)
 
 
+def _digest(path: str) -> str:
+    with open(path, "rb") as f:
+        return hashlib.sha256(f.read()).hexdigest()
+
+
 def build_binding(verbose: bool = False) -> str:
-    """Compile csrc/binding.cpp against the installed torch into _binding.so, if it is out of date."""
-    src = os.path.join(CSRC, "binding.cpp")
-    hdr = os.path.join(ROOT, "include", "cowa.h")
-    if os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(os.path.getmtime(src), os.path.getmtime(hdr)):
-        return BINDING
+    """Compile csrc/binding.cpp against the installed torch into _binding.so, if it is out of date: older than
+    its sources, or not the file that was last built, or built by another command or against another torch or
+    Python (the stamp in _build/ names all of these)."""
     import sysconfig
 
     import torch
     from torch.utils import cpp_extension as ext
 
+    src = os.path.join(CSRC, "binding.cpp")
+    hdr = os.path.join(ROOT, "include", "cowa.h")
+    stamp = os.path.join(BUILD, "binding.stamp")
+    new = BINDING + f".{os.getpid()}.tmp"
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))) if os.path.isabs(_nvcc()) else "/usr/local/cuda"
     inc = [*ext.include_paths(), os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-           *("-isystem" + i for i in inc), src, "-o", BINDING, *("-L" + p for p in ext.library_paths()), "-lc10",
+           *("-isystem" + i for i in inc), src, *("-L" + p for p in ext.library_paths()), "-lc10",
            "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
+    made_by = "\n".join([torch.__version__, sys.version, *cmd]).replace(ROOT, ".")  # (the tree may be moved)
+    if os.path.exists(BINDING) and os.path.exists(stamp) and \
+            os.path.getmtime(BINDING) >= max(os.path.getmtime(src), os.path.getmtime(hdr)):
+        with open(stamp) as f:
+            if f.read() == f"{_digest(BINDING)}\n{made_by}":
+                return BINDING
+    cmd += ["-o", new]
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)
+        if os.path.exists(new):
+            os.remove(new)
         raise RuntimeError("g++ failed on binding.cpp")
+    digest = _digest(new)
+    os.replace(new, BINDING)  # (a program that has the old one loaded keeps it)
+    os.makedirs(BUILD, exist_ok=True)
+    with open(stamp, "w") as f:
+        f.write(f"{digest}\n{made_by}")
     return BINDING
 
 
