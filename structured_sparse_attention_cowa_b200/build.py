@@ -10,10 +10,11 @@ _binding.so beside it (against the installed torch; it finds either library's
 entry points at run time; without torch it is left out).  Objects are rebuilt only when a source or
 header is newer.
 
---debug builds libcowa_debug.so with COWA_DEBUG=1: the kernels check every planned tile and
-cache row against the call's tensors before loading it, and a failed check is reported as
+--debug builds libcowa_debug.so with COWA_DEBUG=1: the attention kernels check every planned tile
+and cache row against the call's tensors before loading it, and a failed check is reported as
 COWA_ERR_CHECK through the workspace status (the binding loads this library when the
-environment has COWA_DEBUG=1).
+environment has COWA_DEBUG=1).  The rotary and append kernels have no workspace to report through,
+and no checks.
 """
 
 from __future__ import annotations

@@ -360,7 +360,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cowa_fwd_kernel(const __grid_c
   if (warp == kProducerWarp) {
     // ------------------------------------------------------------------ TMA producer
     if constexpr (PAGED) {
-      if (lane == 0) {
+      // (debug builds) the work item addresses rows and heads of the call, and a sequence of the table
+      const bool q_ok = ptx::dbg_check(i >= 0 && i * kBM < Nq && row0 >= 0 && Nq <= a.total - row0 && q_off >= 0 &&
+                                           h0 + (has1 ? 1 : 0) < a.Hq && pg_seq < a.n_seq && part < a.parts,
+                                       a.status, &abort_flag, 0x103, i);
+      if (q_ok && lane == 0) {
         ptx::tma_prefetch_desc(&a.tm_q);
         ptx::tma_prefetch_desc(&a.tm_k);
         ptx::tma_prefetch_desc(&a.tm_v);
@@ -379,7 +383,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cowa_fwd_kernel(const __grid_c
       const int tl = imin(t1, Nk), gp = a.tab.sh ? 0 : g;
       const int box_bytes = rows * 128 * (D / 64);
       int issued = 0;
-      if (lane < nbox && ntiles > 0) {
+      if (q_ok && lane < nbox && ntiles > 0) {
         TileCursor cur;
         cur.init(T);
         // (the load is unconditional, at a clamped place: nothing waits for it before its tile's turn)
@@ -392,12 +396,16 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cowa_fwd_kernel(const __grid_c
           if (n + 1 < ntiles) next_page = look(cur.j);
           // some row of the query tile sees a key of the box
           const bool want = p < e && (p < a.pat.S || e > t0 - a.pat.L + 1 || (p < iv.hi && e > iv.lo));
-          const bool good = want && page >= 0 && page < a.tab.n_pages;
+          const int slot = p % a.tab.page_size;
+          // (debug builds) the box lies in the cache and in its page
+          const bool fits = ptx::dbg_check(!want || (p >= 0 && p / a.tab.page_size < a.tab.max_pages &&
+                                                     slot + rows <= a.tab.page_size),
+                                           a.status, nullptr, 0x104, p);
+          const bool good = want && fits && page >= 0 && page < a.tab.n_pages;
           if (want && !good) {
             a.status[3] = kPageFlag;
             *reinterpret_cast<volatile int*>(&bad_page) = 1;
           }
-          const int slot = p % a.tab.page_size;
           bool ok = true;
 #pragma unroll
           for (int is_v = 0; is_v < 2; ++is_v) {
@@ -430,7 +438,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cowa_fwd_kernel(const __grid_c
       }
       __syncwarp();
       // drain: no copy may still be landing in shared memory when the CTA exits
-      ptx::mbar_wait(&q_full, 0, nullptr, a.status);
+      if (q_ok) ptx::mbar_wait(&q_full, 0, nullptr, a.status);
       for (int idx = (issued > Geo::kRing ? issued - Geo::kRing : 0); idx < issued; ++idx)
         ptx::mbar_wait(&kv_full[idx % Geo::kRing], (idx / Geo::kRing) & 1, nullptr, a.status);
     } else if (lane == 0) {

@@ -404,6 +404,12 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV8, BIG>::kCtas)
         const int i = a.page_shift >= 0 ? p >> a.page_shift : p / a.tab.page_size;
         k.slot = p - i * a.tab.page_size;
         k.page = a.tab.ptr[s.b * a.tab.sb + k.g * a.tab.sh + imin(i, a.tab.max_pages - 1)];
+        // (debug builds) the tile's keys lie in the cache and in the tile, the box in its page
+        if (!ptx::dbg_check(!k.want || (item < n_items && k.base >= 0 && k.lo >= k.base && k.hi <= k.base + kTok &&
+                                        k.hi <= a.tab.max_pages * a.tab.page_size && k.slot >= 0 &&
+                                        k.slot + a.box_rows <= a.tab.page_size),
+                            a.status, nullptr, 0x402, k.base))
+          k.page = -1;  // (not fetched, its keys left out)
         return true;
       };
       int issued = 0;
@@ -508,6 +514,8 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV8, BIG>::kCtas)
     } while (off >= lim);
     return true;
   };
+  // (debug builds) the pair is one of the call's: its query rows, record and outputs lie in their arrays
+  auto listed = [&]() { return ptx::dbg_check(item < n_items, a.status, &abort_flag, 0x403, item); };
   bool more = false;
   if (w0 < w1) {
     item = first_item;
@@ -520,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV8, BIG>::kCtas)
     }
     off = imax(0, w0 - place - kSegment);
     lim = imin(n, w1 - place - kSegment);
-    more = off < lim || (!CL && step());
+    more = (off < lim || (!CL && step())) && listed();
     if (more) load_q(item);
   }
   while (more) {
@@ -631,14 +639,17 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV8, BIG>::kCtas)
       // ---- the next segment's pair and query rows, while the warps are joined
       const bool begins = off == 0, ends = lim == n;
       if (!CL && begins) {  // whether the pair goes on, and to which CTA
-        const int4 r = make_int4(ends ? -1 : item, c, sh.of(place + kSegment + n - 1), 0);
+        const int last = sh.of(place + kSegment + n - 1);
+        // (debug builds) the pieces that the join will read are those of CTAs of this launch
+        const bool joins = !ends && ptx::dbg_check(last >= c && last < (int)gridDim.x, a.status, &abort_flag, 0x404, last);
+        const int4 r = make_int4(joins ? item : -1, c, last, 0);
         if (a.by_pair) {
           if (threadIdx.x == 0) a.rec[item] = r;
         } else if (!ends) {
           rec = r;
         }
       }
-      more = !CL && step();
+      more = !CL && step() && listed();
       if (more) load_q(item);
       // ---- join the warps
 #pragma unroll
