@@ -1,0 +1,192 @@
+"""GPU parity of the paged calls where a call takes another way through the code than the cases of
+test_gpu_paged: rotary dimensions that are no whole units of 8 pairs (written as bf16 and as E4M3 codes), more KV
+heads than travel with a kernel's arguments, more (sequence, head) pairs than the threads of a block keep at
+hand; and the contiguous calls and whole serving steps held to the derived bounds of test_gpu_paged."""
+
+import numpy as np
+import pytest
+import torch
+
+import tests.test_gpu_paged as tp
+from oracle import fp8_kv as f8
+from oracle import rope as orp
+from structured_sparse_attention_cowa_b200 import cowa as cw
+from tests.gpu_helpers import host_and_device, to64
+from tests.test_gpu_rope import assert_rotated
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("Hq,Hkv,r,sec,inter,ps,n,per_head,layout", [
+    (8, 2, 22, (11,), False, 16, 6, False, "bthd"),      # halves of 11 pairs: pieces through shared memory
+    (5, 1, 26, (6, 7), False, 24, 5, True, "bhtd"),
+    (6, 2, 20, (7, 3), True, 8, 12, False, "bhtd"),      # neighbours, r = 4 mod 8
+    (4, 4, 126, (63,), False, 16, 6, False, "bthd"),
+    (8, 2, 40, (20,), True, 16, 6, False, "bthd"),       # neighbours, the last unit half rotated
+    (3, 3, 72, (12, 12, 12), True, 32, 4, True, "bthd"),
+    (0, 2, 8, (4,), True, 16, 6, False, "bhtd"),         # half a unit, no queries
+    (2, 1, 2, (1,), False, 16, 6, False, "bthd"),        # one pair
+])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("chunks", [False, True])
+def test_append_of_odd_rotary_dimensions(cuda_device, Hq, Hkv, r, sec, inter, ps, n, per_head, layout, e4m3, chunks):
+    tp.test_append_matches_oracle(cuda_device, Hq, Hkv, 128, r, sec, inter, ps, n, per_head, layout, e4m3, chunks)
+
+
+MANY_HEADS = [
+    # Hq, Hkv, d, pattern, page, pages, per head, layout
+    (66, 66, 64, cw.Pattern(20, 50, 700, 6), 16, 48, False, "bthd"),
+    (130, 65, 128, cw.Pattern(0, 9, 768, 65), 24, 32, True, "bhtd"),
+    (140, 70, 128, cw.Pattern(33, 100, 500, 7, kv_head_base=10, h_kv_global=140), 32, 24, False, "bhtd"),
+]
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,pat,ps,n,per_head,layout", MANY_HEADS)
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("wide", [False, True])
+def test_decode_of_many_heads(cuda_device, Hq, Hkv, d, pat, ps, n, per_head, layout, e4m3, wide):
+    """More than 64 KV heads, whose intervals are worked out on the device."""
+    if e4m3 and d != 128:
+        pytest.skip("E4M3 pages need d = 128")
+    tp.test_decode_matches_oracle(cuda_device, Hq, Hkv, d, pat, ps, n, per_head, layout, [767, 300, -1], e4m3, wide)
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,pat,ps,n,per_head,layout", MANY_HEADS)
+def test_chunks_of_many_heads(cuda_device, Hq, Hkv, d, pat, ps, n, per_head, layout):
+    tp.test_chunks_match_oracle(cuda_device, Hq, Hkv, d, pat, ps, n, per_head, layout, [(500, 200), (0, 3), (766, 2)])
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,d,e4m3", [
+    (100, 16, 8, 64, False),    # 800 pairs: five a thread
+    (90, 24, 8, 128, True),     # groups of 3
+    (128, 48, 8, 128, True),    # groups of 6
+    (401, 2, 2, 128, False),    # 802
+    (2000, 1, 1, 64, False),    # 13 a thread
+    (81, 8, 8, 128, False),     # 648
+])
+def test_decode_of_many_pairs(cuda_device, B, Hq, Hkv, d, e4m3):
+    """More than 640 (sequence, KV head)s: lengths from none to some hundreds, runs of empty slots at the start, in
+    the middle and at the end, one long sequence that many blocks share; every row against the oracle, and the
+    same bits again."""
+    ps, n, n_pages = 16, 600, 700
+    pat = cw.Pattern(10, 60, 9600, Hkv)
+    rng = np.random.default_rng(B)
+    pos = [int(x) for x in np.where(rng.random(B) < 0.2, -1, rng.integers(0, 300, B))]
+    for i in (0, 1, 2, *range(B // 2, B // 2 + 7), B - 2, B - 1):
+        pos[i] = -1
+    pos[B // 3] = n * ps - 1
+    pos[B // 3 + 1] = 0
+    tab = rng.integers(0, n_pages, (B, n)).astype(np.int32)
+    shape = (n_pages, ps, Hkv, d)
+    if e4m3:
+        kc, vc = (f8.f64_to_e4m3(rng.standard_normal(shape) * 3) for _ in range(2))
+        kd, vd = torch.from_numpy(kc).to(cuda_device), torch.from_numpy(vc).to(cuda_device)
+        k64, v64 = 0.4 * f8.e4m3_to_f64(kc), 0.25 * f8.e4m3_to_f64(vc)
+    else:
+        (k64, kd), (v64, vd) = (host_and_device(shape, x, cuda_device, 141) for x in ("k", "v"))
+    q64, q = host_and_device((B, Hq, d), "q", cuda_device, 141)
+    fn = "cowa_decode_paged_fp8" if e4m3 else "cowa_decode_paged"
+    ws = tp.ws_for(fn, pat, B, Hq, Hkv, d, n, ps, cuda_device)
+    run = lambda: getattr(cw, fn)(q, kd, vd, torch.from_numpy(tab).to(cuda_device),
+                                  torch.tensor(pos, dtype=torch.int32, device=cuda_device), pat,
+                                  *((0.4, 0.25) if e4m3 else ()), workspace=ws)
+    assert B * Hkv > 640
+    o, lse = run()
+    o2, lse2 = run()
+    assert cw.workspace_status(ws) == 0
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    for b in range(B):
+        t = max(pos[b], 0) + 1
+        k, v = (orp.gather_pages(x, tab[b:b + 1], t)[0] for x in (k64, v64))
+        tp.assert_decoded(o[b:b + 1], lse[b:b + 1], q64[b:b + 1], k, v, [pos[b]], pat, 2.0 ** -11 if e4m3 else 2.0 ** -8)
+
+
+def test_decode_and_the_contiguous_decode_within_the_derived_bound(cuda_device):
+    """The same keys in pages and in one array per sequence: each within the bound of its roundings."""
+    B, Hq, Hkv, d, Tc, ps = 3, 10, 2, 128, 2048, 64
+    pat, pos = cw.Pattern(64, 300, 2048, 2), [2047, 1000, 3]
+    (k64, kc), (v64, vc) = (host_and_device((B, Hkv, Tc, d), x, cuda_device, 142) for x in ("k", "v"))
+    q64, q = host_and_device((B, Hq, d), "q", cuda_device, 142)
+    posd = torch.tensor(pos, dtype=torch.int32, device=cuda_device)
+    pages = lambda x: x.view(B, Hkv, Tc // ps, ps, d).permute(0, 2, 1, 3, 4).reshape(-1, Hkv, ps, d).contiguous()
+    tab = torch.arange(B * Tc // ps, dtype=torch.int32, device=cuda_device).view(B, -1)
+    for o, lse in (cw.cowa_decode_paged(q, pages(kc), pages(vc), tab, posd, pat, layout="bhtd"),
+                   cw.cowa_decode(q, kc, vc, posd, pat)):
+        tp.assert_decoded(o, lse, q64, k64, v64, pos, pat)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("per_head,layout,ps", [(False, "bhtd", 32), (True, "bthd", 16), (True, "bhtd", 24)])
+def test_serving_steps_within_the_derived_bounds(cuda_device, per_head, layout, ps, e4m3):
+    """A prompt written to pages in two chunks (bf16: the second's rows attend to both), then steps of append and
+    decode, heads giving pages back to another sequence that overwrites them.  What the pages hold is the rotated
+    keys and the values; what the attention gives is right for exactly what the pages and the queries hold."""
+    B, Hq, Hkv, d, N0, steps = 2, 8, 2, 128, 200, 40
+    pat = cw.Pattern(20, 40, 300, 2)
+    f = cw.rope_frequencies(d, device=cuda_device)
+    rope, fr = cw.Rope(f), f.cpu().numpy()
+    N = N0 + steps
+    (q64, q), (k64, k), (v64, v) = (host_and_device((B, N, h, d), x, cuda_device, 143)
+                                    for x, h in (("q", Hq), ("k", Hkv), ("v", Hkv)))
+    n = -(-N // ps)
+    tab, n_pages = tp.make_table(np.random.default_rng(143), B, n, heads=Hkv if per_head else None)
+    shape = (n_pages, ps, 1 if per_head else Hkv, d) if layout == "bthd" else (n_pages, 1 if per_head else Hkv, ps, d)
+    ks, vs = 0.02, 0.03
+    kp, vp = (torch.full(shape, 0x7f if e4m3 else float("nan"), dtype=torch.uint8 if e4m3 else torch.bfloat16,
+                         device=cuda_device) for _ in range(2))
+    tabd = torch.from_numpy(tab).to(cuda_device)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=cuda_device)
+
+    def append(q, k, v, pos, seq=None):
+        rest = dict(rope=rope, seq=None if seq is None else i32(seq), layout=layout)
+        if e4m3:
+            return cw.paged_append_fp8(q, k, v, i32(pos), kp, vp, tabd, ks, vs, **rest)
+        return cw.paged_append(q, k, v, i32(pos), kp, vp, tabd, **rest)
+
+    def held(t):  # keys, values 0 .. t as the pages hold them, and which have a page
+        out = []
+        for pool, scale in ((kp, ks), (vp, vs)):
+            x = pool.transpose(1, 2) if layout == "bhtd" else pool
+            x = scale * f8.e4m3_to_f64(x.cpu().numpy()) if e4m3 else to64(x)
+            out.append(orp.gather_pages(x, tabd.cpu().numpy(), t + 1)[0])
+        return out
+
+    turned = lambda x, p: np.stack([orp.rope(x[b], np.asarray(p)[None], fr) for b in range(B)])
+    first, last = 130, N0
+    for lo, hi in ((0, first), (first, last)):
+        flat = lambda x: x[:, lo:hi].reshape(B * (hi - lo), -1, d)
+        qr = append(flat(q), flat(k), flat(v), list(range(lo, hi)) * B, [b for b in range(B) for _ in range(lo, hi)])
+        assert_rotated(to64(qr).reshape(B * (hi - lo), Hq, d), q64[:, lo:hi].reshape(-1, Hq, d),
+                       turned(q64[:, lo:hi], np.arange(lo, hi)).reshape(-1, Hq, d), d, False)
+    hk, hv = held(N0 - 1)
+    want_k = turned(k64[:, :N0], np.arange(N0)).transpose(0, 2, 1, 3)
+    want_v = v64[:, :N0].transpose(0, 2, 1, 3)
+    if e4m3:
+        code = lambda x, s: s * f8.e4m3_to_f64(f8.quantize_e4m3_f32(x.astype(np.float32), s))
+        np.testing.assert_array_equal(hk, code(want_k, ks))
+        np.testing.assert_array_equal(hv, code(want_v, vs))
+    else:
+        flat = lambda x: x.reshape(-1, 1, d)
+        assert_rotated(flat(hk), flat(k64[:, :N0].transpose(0, 2, 1, 3)), flat(want_k), d, False)
+        np.testing.assert_array_equal(hv, want_v)
+        o, lse = cw.cowa_fwd_paged(qr, kp, vp, tabd, i32([0, last - first, 2 * (last - first)]), i32([first] * B), pat,
+                                   layout=layout)
+        for b in range(B):
+            r = slice(b * (last - first), (b + 1) * (last - first))
+            tp.assert_chunk(o[r], lse[:, r], to64(qr[r]), hk[b], hv[b], first, pat)
+    fn = "cowa_decode_paged_fp8" if e4m3 else "cowa_decode_paged"
+    ws = tp.ws_for(fn, pat, B, Hq, Hkv, d, n, ps, cuda_device)
+    for t in range(N0, N):
+        qt = append(q[:, t], k[:, t], v[:, t], [t] * B)
+        o, lse = getattr(cw, fn)(qt, kp, vp, tabd, i32([t] * B), pat, *((ks, vs) if e4m3 else ()), layout=layout,
+                                 workspace=ws)
+        tp.assert_decoded(o, lse, to64(qt), *held(t), [t] * B, pat, 2.0 ** -11 if e4m3 else 2.0 ** -8)
+        if per_head and t % 5 == 0:  # pages go back, and somebody else writes to them
+            for g, keep in enumerate(cw.pages_needed(pat, Hkv, ps, n, t + 1)):
+                gone = tabd[:, g, torch.from_numpy(~keep).to(cuda_device)].long().reshape(-1)
+                gone = gone[gone >= 0]
+                kp[gone], vp[gone] = (0x7f, 0xff) if e4m3 else (float("nan"), float("inf"))
+                tabd[:, g, torch.from_numpy(~keep).to(cuda_device)] = -1
+    assert cw.workspace_status(ws) == 0
+    if per_head:
+        assert (tabd < 0).any()
