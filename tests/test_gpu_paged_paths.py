@@ -11,6 +11,7 @@ import tests.test_gpu_paged as tp
 from oracle import fp8_kv as f8
 from oracle import rope as orp
 from structured_sparse_attention_cowa_b200 import cowa as cw
+from structured_sparse_attention_cowa_b200 import synth
 from tests.gpu_helpers import host_and_device, to64
 from tests.test_gpu_rope import assert_rotated
 
@@ -190,3 +191,128 @@ def test_serving_steps_within_the_derived_bounds(cuda_device, per_head, layout, 
     assert cw.workspace_status(ws) == 0
     if per_head:
         assert (tabd < 0).any()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("layout", ["bthd", "bhtd"])
+def test_decode_of_strided_pools_and_tables(cuda_device, e4m3, wide, layout):
+    """Keys and values of a page side by side in one pool, which holds more heads than the call's; a table that is a
+    slice of a larger one; no lse; a scale of the scores."""
+    B, Hq, Hkv, d, ps, n = 5, 6, 3, 128, 24, 30
+    pat, pos = cw.Pattern(9, 70, 600, 3, softmax_scale=0.05), [719, 0, -1, 23, 400]
+    rng = np.random.default_rng(144)
+    tab, n_pages = tp.make_table(rng, B, n)
+    if wide:
+        pat, tab = tp.widened(pat, tab, ps)
+    shape = (n_pages, 2, ps, Hkv + 2, d) if layout == "bthd" else (n_pages, 2, Hkv + 2, ps, d)
+    if e4m3:
+        codes = f8.f64_to_e4m3(rng.standard_normal(shape) * 3)
+        pool, p64 = torch.from_numpy(codes).to(cuda_device), 0.25 * f8.e4m3_to_f64(codes)
+    else:
+        p64, pool = host_and_device(shape, "k", cuda_device, 144)
+    cut = (lambda x: (x[:, 0, :, 1:1 + Hkv], x[:, 1, :, 2:])) if layout == "bthd" else \
+        (lambda x: (x[:, 0, 1:1 + Hkv], x[:, 1, 2:]))
+    large = torch.full((2 * B, tab.shape[1] + 9), -7, dtype=torch.int32, device=cuda_device)
+    large[::2, 5:5 + tab.shape[1]] = torch.from_numpy(tab).to(cuda_device)
+    q64, q = host_and_device((B, Hq, d), "q", cuda_device, 144)
+    fn = cw.cowa_decode_paged_fp8 if e4m3 else cw.cowa_decode_paged
+    run = lambda **c: fn(q, *cut(pool), large[::2, 5:5 + tab.shape[1]], torch.tensor(pos, dtype=torch.int32, device=cuda_device),
+                         pat, *((0.25, 0.25) if e4m3 else ()), layout=layout, **c)
+    o, lse = run()
+    k, v = (orp.gather_pages(x.transpose(0, 2, 1, 3) if layout == "bhtd" else x, tab, n * ps)[0] for x in cut(p64))
+    tp.assert_decoded(o, lse, q64, k, v, pos, pat, 2.0 ** -11 if e4m3 else 2.0 ** -8)
+    o2, none = run(want_lse=False)
+    assert none is None and torch.equal(o, o2)
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,ps,n,pat,chunks", [
+    (6, 3, 128, 24, 30, cw.Pattern(9, 70, 600, 3, softmax_scale=0.05), [(300, 200), (0, 7)]),
+    (10, 2, 64, 16, 64, cw.Pattern(0, 2**31 - 1, 2**31 - 1, 2), [(1000, 24), (0, 130)]),           # all in the band
+    (10, 2, 64, 1024, 1, cw.Pattern(2**31 - 1, 1, 2**31 - 1, 2), [(1023, 1), (100, 300)]),         # all sinks, one page
+    (4, 4, 64, 512, 2, cw.Pattern(5, 3, 2**31 - 1, 4), [(0, 1024)]),                               # intervals far away
+    (16, 2, 128, 40, 25, cw.Pattern(1, 1, 1000, 1, softmax_scale=0.3), [(999, 1), (0, 1), (500, 129)]),
+])
+def test_chunks_of_strided_tensors_and_extreme_patterns(cuda_device, Hq, Hkv, d, ps, n, pat, chunks):
+    """Queries that are a slice of a packed projection, outputs that are a slice of a wider array, keys and values
+    side by side in one pool; windows up to INT_MAX, pages of many tiles."""
+    B, rng = len(chunks), np.random.default_rng(ps * n)
+    tab, n_pages = tp.make_table(rng, B, n)
+    p64, pool = host_and_device((n_pages, ps, 2 * Hkv, d), "k", cuda_device, 145)
+    lens = [r for _, r in chunks]
+    total, cu = sum(lens), np.cumsum([0] + lens)
+    x64, x = host_and_device((total, Hq + 3, d), "q", cuda_device, 145)
+    wide = torch.full((total, 2, Hq, d), 3.0, dtype=torch.bfloat16, device=cuda_device)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=cuda_device)
+    o, lse = cw.cowa_fwd_paged(x[:, 2:2 + Hq], pool[:, :, :Hkv], pool[:, :, Hkv:], torch.from_numpy(tab).to(cuda_device),
+                               i32(cu.tolist()), i32([s for s, _ in chunks]), pat, out=wide[:, 1])
+    assert (wide[:, 0] == 3.0).all()
+    k, v = (orp.gather_pages(y, tab, n * ps)[0] for y in (p64[:, :, :Hkv], p64[:, :, Hkv:]))
+    for b, (start, rows) in enumerate(chunks):
+        r, e = slice(cu[b], cu[b + 1]), start + rows
+        tp.assert_chunk(wide[r, 1], lse[:, r], x64[r, 2:2 + Hq], k[b, :, :e], v[b, :, :e], start, pat)
+
+
+@pytest.mark.parametrize("pat", [
+    cw.Pattern(0, 2**31 - 1, 2**31 - 1, 2), cw.Pattern(2**31 - 1, 1, 2**31 - 1, 2), cw.Pattern(5, 3, 2**31 - 1, 1),
+    cw.Pattern(0, 1, 0, 1), cw.Pattern(2**31 - 1, 2**31 - 1, 2**31 - 1, 1),
+])
+@pytest.mark.parametrize("ps,n", [(8, 1), (1024, 2), (4096, 5)])
+def test_decode_of_extreme_patterns(cuda_device, pat, ps, n):
+    Hq, Hkv, d, B = 6, 2, 64, 4
+    cap = ps * n
+    pos = [cap - 1, 0, cap // 2, 2**31 - 1]
+    tab, n_pages = tp.make_table(np.random.default_rng(ps), B, n)
+    (k64, kd), (v64, vd) = (host_and_device((n_pages, ps, Hkv, d), x, cuda_device, 146) for x in ("k", "v"))
+    q64, q = host_and_device((B, Hq, d), "q", cuda_device, 146)
+    o, lse = cw.cowa_decode_paged(q, kd, vd, torch.from_numpy(tab).to(cuda_device),
+                                  torch.tensor(pos, dtype=torch.int32, device=cuda_device), pat)
+    k, v = (orp.gather_pages(x, tab, cap)[0] for x in (k64, v64))
+    tp.assert_decoded(o, lse, q64, k, v, pos, pat)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_paged_calls_side_by_side(cuda_device, e4m3):
+    """Appends, chunks and decodes of four caches on four streams at once, each with a workspace of its own, over
+    and over: the bits of the calls made one after the other."""
+    Hq, Hkv, d, ps, n, rows = 8, 2, 128, 32, 40, 300
+    pat, rope = cw.Pattern(16, 200, 1280, 2), cw.Rope(cw.rope_frequencies(d, device=cuda_device))
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=cuda_device)
+    r = lambda s, nm, x: synth.cuda_normal_bf16(s, synth.seed_of(nm, 147 + x), cuda_device)
+    sets = []
+    for x in range(4):
+        pools = [r((2 * n, ps, Hkv, d), nm, x) for nm in ("k", "v")]
+        if e4m3:
+            pools = [cw.quantize_e4m3(p, 1 / 64) for p in pools]
+        sets.append(dict(qkv=r((rows, Hq + 2 * Hkv, d), "q", x), pools=pools, first=[p.clone() for p in pools],
+                         tab=torch.randperm(2 * n, device=cuda_device).int().view(2, n),
+                         ws=torch.zeros(1 << 24, dtype=torch.uint8, device=cuda_device), stream=torch.cuda.Stream()))
+    pos = i32([900 + i for i in range(200)] + [17 + i for i in range(rows - 200)])
+    seq, cu, start, last = i32([0] * 200 + [1] * (rows - 200)), i32([0, 200, rows]), i32([900, 17]), i32([1099, 16 + rows - 200])
+
+    def step(s, stream):
+        q, k, v = s["qkv"].split([Hq, Hkv, Hkv], dim=1)
+        kp, vp = s["pools"]
+        rest = dict(rope=rope, seq=seq, stream=stream)
+        if e4m3:
+            qr = cw.paged_append_fp8(q, k, v, pos, kp, vp, s["tab"], 1 / 64, 1 / 64, **rest)
+            return qr, *cw.cowa_decode_paged_fp8(qr[:2], kp, vp, s["tab"], last, pat, 1 / 64, 1 / 64, workspace=s["ws"],
+                                                 stream=stream)
+        qr = cw.paged_append(q, k, v, pos, kp, vp, s["tab"], **rest)
+        return qr, *cw.cowa_fwd_paged(qr, kp, vp, s["tab"], cu, start, pat, workspace=s["ws"], stream=stream), \
+            *cw.cowa_decode_paged(qr[:2], kp, vp, s["tab"], last, pat, workspace=s["ws"], stream=stream)
+
+    want = []
+    for s in sets:
+        want.append([x.clone() for x in (*step(s, None), *s["pools"])])
+        torch.cuda.synchronize()
+        for p, f in zip(s["pools"], s["first"]):
+            p.copy_(f)
+    torch.cuda.synchronize()
+    for _ in range(10):
+        got = [step(s, s["stream"]) for s in sets]
+    torch.cuda.synchronize()
+    for s, g, w in zip(sets, got, want):
+        assert cw.workspace_status(s["ws"]) == 0
+        for a, b in zip((*g, *s["pools"]), w):
+            assert torch.equal(a, b)
