@@ -70,7 +70,8 @@ typedef enum {
   COWA_ERR_TIMEOUT = 6,     /* a device-side bounded wait ran out */
   COWA_ERR_CHECK = 7,       /* a device-side self-check of a COWA_DEBUG build failed (a planned
                                tile or cache row outside the call's tensors); the access was
-                               skipped.  Release builds never report it. */
+                               skipped.  Release builds report it only if a block's shared memory
+                               were not aligned as its swizzle needs, which does not occur. */
   COWA_ERR_PAGE = 8         /* the page table entry of a page that holds visible keys lies outside
                                the pool; those keys were left out */
 } cowa_status;

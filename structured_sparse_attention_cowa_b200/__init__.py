@@ -1,7 +1,9 @@
 """CoWindow Attention (CoWA) for NVIDIA B200 (sm_100a).
 
 The compute lives in libcowa.so (hand-written CUDA: TMA + tcgen05 forward and
-backward kernels, a split-KV decode kernel); `cowa` is its ctypes binding.
+backward kernels, split-KV decode kernels over contiguous, compacted and paged
+caches, rotary positions); `cowa` is its Python binding (ctypes, and _binding.so
+for the calls of a serving step).
 """
 
 from .cowa import (CowaError, Pattern, Rope, compact_append, compact_cache, compact_rows, cowa_bwd,  # noqa: F401

@@ -1,4 +1,5 @@
-"""Python binding of libcowa.so: argument marshalling only.
+"""Python binding of libcowa.so: argument marshalling only (ctypes; the calls of a serving step
+through compiled code, csrc/binding.cpp).
 
 Every step of the computation runs in the library's CUDA kernels; this module
 turns torch tensors into the C ABI's pointers and strides, allocates the
@@ -10,7 +11,10 @@ Calls are asynchronous on the stream, as in the C ABI.  A kernel whose bounded w
 runs out records COWA_ERR_TIMEOUT in its workspace's status word instead of hanging;
 reading that word needs a stream synchronisation, so no call reads it on its own:
 pass `workspace=` and call `workspace_status(workspace)` at a point where a sync is
-acceptable (a workspace the binding allocates itself is not checked).
+acceptable (a workspace the binding allocates itself is not checked).  The first 256 bytes of a
+workspace must be zero before its first call (torch.zeros); a nonzero status word left there
+makes a kernel's waits give up at once and its outputs stay unwritten.  Its size is what the
+C function of the call's name with `_workspace_size` returns (lib().cowa_fwd_workspace_size ...).
 
 Function names follow the C ABI (include/cowa.h): cowa_fwd, cowa_fwd_chunk,
 cowa_fwd_varlen, cowa_bwd, cowa_bwd_varlen, cowa_decode, cowa_decode_compact (with compact_cache /
@@ -770,7 +774,11 @@ def _decode_paged(q_t, k_pages, v_pages, page_table, pos, pattern, scales, layou
 def cowa_decode_paged(q_t, k_pages, v_pages, page_table, pos, pattern: Pattern, layout: str = "bthd", out=None,
                       lse=None, workspace=None, stream=None, want_lse: bool = True):
     """o [B, H_q, d] bf16 (and lse [B, H_q] fp32) for one new token per sequence at pos[b] over a paged
-    cache (pools and page_table as for paged_append).  pos[b] < 0: no sequence, o = 0 and lse = -inf."""
+    cache (pools and page_table as for paged_append).  pos[b] < 0: no sequence, o = 0 and lse = -inf.
+
+    workspace: a CUDA tensor of at least lib().cowa_decode_paged_workspace_size(pattern.c(), B, H_q, H_kv, d,
+    max_pages, page_size) bytes, its first 256 bytes zero before its first call.  Without one the call
+    allocates and clears one, which a step of one token notices (8 K tokens: 13.7 us instead of 8.3)."""
     return _decode_paged(q_t, k_pages, v_pages, page_table, pos, pattern, None, layout, out, lse, workspace, stream,
                          want_lse)
 
@@ -779,7 +787,7 @@ def cowa_decode_paged_fp8(q_t, k_pages, v_pages, page_table, pos, pattern: Patte
                           layout: str = "bthd", out=None, lse=None, workspace=None, stream=None,
                           want_lse: bool = True):
     """cowa_decode_paged over pages of E4M3 codes (uint8, d = 128): keys k_scale * e4m3(code), values
-    v_scale * e4m3(code)."""
+    v_scale * e4m3(code).  (Its workspace: lib().cowa_decode_paged_fp8_workspace_size.)"""
     return _decode_paged(q_t, k_pages, v_pages, page_table, pos, pattern, (float(k_scale), float(v_scale)), layout,
                          out, lse, workspace, stream, want_lse)
 
@@ -788,8 +796,13 @@ def cowa_fwd_paged(q, k_pages, v_pages, page_table, cu_seqlens, q_start, pattern
                    out=None, lse=None, workspace=None, stream=None):
     """Packed query chunks over a paged cache that already holds their keys: q [total, H_q, d],
     cu_seqlens CUDA int32 [n_seq + 1], q_start CUDA int32 [n_seq] the position of each chunk's first row;
-    pools and page_table as for paged_append (bf16).  Returns o [total, H_q, d] bf16 and lse [H_q, total]
-    fp32."""
+    pools and page_table as for paged_append, in bf16 (pages of E4M3 codes are read by cowa_decode_paged_fp8
+    only: no call attends to them with a chunk of queries).  Returns o [total, H_q, d] bf16 and lse
+    [H_q, total] fp32.
+
+    workspace: at least lib().cowa_fwd_paged_workspace_size(pattern.c(), n_seq, total, H_q, H_kv, d, max_pages,
+    page_size) bytes, up to 15 MB, the first 256 zero before its first call; allocated and cleared by the call
+    if not given."""
     if stream is not None:
         with _on(q, stream):
             return cowa_fwd_paged(q, k_pages, v_pages, page_table, cu_seqlens, q_start, pattern, layout, out, lse,
