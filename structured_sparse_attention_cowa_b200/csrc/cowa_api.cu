@@ -39,7 +39,7 @@ CUresult with_context(F encode) {
   CUresult r = encode();
   if (r == CUDA_ERROR_INVALID_CONTEXT || r == CUDA_ERROR_NOT_INITIALIZED) {
     int device;
-    if (cudaGetDevice(&device) == cudaSuccess && cudaSetDevice(device) == cudaSuccess) r = encode();
+    if (status_of(cudaGetDevice(&device)) == COWA_OK && status_of(cudaSetDevice(device)) == COWA_OK) r = encode();
   }
   return r;
 }
@@ -141,10 +141,8 @@ int cowa_version(void) { return 1; }
 cowa_status cowa_debug_wait_timeout(void* ws, size_t ws_bytes, int64_t limit_ns, void* stream) {
   COWA_TRY(check_ws(ws, ws_bytes, kWsHeader));
   if (limit_ns < 1000 || limit_ns > 10000000000LL) return COWA_ERR_INVALID_ARG;
-  return launch_wait_timeout_probe(reinterpret_cast<uint32_t*>(ws), (unsigned long long)limit_ns,
-                                   reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
-             ? COWA_OK
-             : COWA_ERR_CUDA;
+  return status_of(launch_wait_timeout_probe(reinterpret_cast<uint32_t*>(ws), (unsigned long long)limit_ns,
+                                   reinterpret_cast<cudaStream_t>(stream)));
 }
 
 const char* cowa_status_string(cowa_status s) {
@@ -166,13 +164,13 @@ cowa_status cowa_workspace_status(void* ws, void* stream) {
   if (!ws) return COWA_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   uint32_t word[4] = {0, 0, 0, 0};
-  if (cudaMemcpyAsync(word, ws, sizeof(word), cudaMemcpyDeviceToHost, s) != cudaSuccess) return COWA_ERR_CUDA;
-  if (cudaStreamSynchronize(s) != cudaSuccess) return COWA_ERR_CUDA;
+  COWA_TRY(status_of(cudaMemcpyAsync(word, ws, sizeof(word), cudaMemcpyDeviceToHost, s)));
+  COWA_TRY(status_of(cudaStreamSynchronize(s)));
   if (word[0] != 0 || word[3] == kPageFlag) {
     // clear the status word, the self-check record (words 1 and 2) and the bad-page flag (word 3)
     // for the next call
-    if (cudaMemsetAsync(ws, 0, sizeof(word), s) != cudaSuccess) return COWA_ERR_CUDA;
-    if (cudaStreamSynchronize(s) != cudaSuccess) return COWA_ERR_CUDA;
+    COWA_TRY(status_of(cudaMemsetAsync(ws, 0, sizeof(word), s)));
+    COWA_TRY(status_of(cudaStreamSynchronize(s)));
     if (word[0] == 0) return COWA_ERR_PAGE;
     return (word[0] & 2u) ? COWA_ERR_CHECK : COWA_ERR_TIMEOUT;
   }
@@ -201,11 +199,9 @@ cowa_status cowa_compact_build(const cowa_pattern* pat, int B, int N, int Hkv, i
   COWA_TRY(check_tensor(v));
   if (!k_compact || !v_compact) return COWA_ERR_INVALID_ARG;
   if (!aligned16(k_compact) || !aligned16(v_compact)) return COWA_ERR_ALIGNMENT;
-  return launch_compact_build(p, B, N, Hkv, d, k.ptr, k.stride_b, k.stride_t, k.stride_h, v.ptr, v.stride_b,
+  return status_of(launch_compact_build(p, B, N, Hkv, d, k.ptr, k.stride_b, k.stride_t, k.stride_h, v.ptr, v.stride_b,
                               v.stride_t, v.stride_h, k_compact, v_compact,
-                              reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
-             ? COWA_OK
-             : COWA_ERR_CUDA;
+                              reinterpret_cast<cudaStream_t>(stream)));
 }
 
 cowa_status cowa_compact_append(const cowa_pattern* pat, int B, int Hkv, int d, const void* k_new, const void* v_new,
@@ -217,10 +213,8 @@ cowa_status cowa_compact_append(const cowa_pattern* pat, int B, int Hkv, int d, 
   if (!k_new || !v_new || !pos || !k_compact || !v_compact) return COWA_ERR_INVALID_ARG;
   if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(k_compact) || !aligned16(v_compact))
     return COWA_ERR_ALIGNMENT;
-  return launch_compact_append(p, B, Hkv, d, k_new, v_new, pos, k_compact, v_compact,
-                               reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
-             ? COWA_OK
-             : COWA_ERR_CUDA;
+  return status_of(launch_compact_append(p, B, Hkv, d, k_new, v_new, pos, k_compact, v_compact,
+                               reinterpret_cast<cudaStream_t>(stream)));
 }
 
 size_t cowa_decode_compact_workspace_size(const cowa_pattern* pat, int B, int Hq, int Hkv, int d) {
@@ -261,7 +255,7 @@ cowa_status cowa_decode_compact(const cowa_pattern* pat, int B, int Hq, int Hkv,
       !make_tmap_bf16(&a.tm_v, v_compact, d, (int)rows, Hkv, B, d, rows * d, (int64_t)Hkv * rows * d,
                       64))
     return COWA_ERR_CUDA;
-  return launch_decode(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? COWA_OK : COWA_ERR_CUDA;
+  return status_of(launch_decode(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 size_t cowa_decode_workspace_size(const cowa_pattern* pat, int B, int Hq, int Hkv, int d, int T_cap) {
@@ -299,7 +293,7 @@ cowa_status cowa_decode(const cowa_pattern* pat, int B, int Hq, int Hkv, int d, 
       !make_tmap_bf16(&a.tm_v, v_cache.ptr, d, T_cap, Hkv, B, v_cache.stride_t, v_cache.stride_h,
                       v_cache.stride_b, 64))
     return COWA_ERR_CUDA;
-  return launch_decode(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? COWA_OK : COWA_ERR_CUDA;
+  return status_of(launch_decode(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 // ------------------------------------------------------------------------------ E4M3 cache
@@ -340,7 +334,7 @@ cowa_status cowa_decode_fp8(const cowa_pattern* pat, int B, int Hq, int Hkv, int
       !make_tmap_u8(&a.tm_v, v_cache.ptr, d, T_cap, Hkv, B, v_cache.stride_t, v_cache.stride_h, v_cache.stride_b,
                     64))
     return COWA_ERR_CUDA;
-  return launch_decode(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? COWA_OK : COWA_ERR_CUDA;
+  return status_of(launch_decode(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 // compacted E4M3 cache: rows of d = 128 codes (128 bytes, the row size of a d = 64 bf16 cache, so
@@ -356,11 +350,9 @@ cowa_status cowa_compact_build_fp8(const cowa_pattern* pat, int B, int N, int Hk
   COWA_TRY(check_tensor8(v));
   if (!k_compact || !v_compact) return COWA_ERR_INVALID_ARG;
   if (!aligned16(k_compact) || !aligned16(v_compact)) return COWA_ERR_ALIGNMENT;
-  return launch_compact_build(p, B, N, Hkv, 64, k.ptr, k.stride_b / 2, k.stride_t / 2, k.stride_h / 2, v.ptr,
+  return status_of(launch_compact_build(p, B, N, Hkv, 64, k.ptr, k.stride_b / 2, k.stride_t / 2, k.stride_h / 2, v.ptr,
                               v.stride_b / 2, v.stride_t / 2, v.stride_h / 2, k_compact, v_compact,
-                              reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
-             ? COWA_OK
-             : COWA_ERR_CUDA;
+                              reinterpret_cast<cudaStream_t>(stream)));
 }
 
 cowa_status cowa_compact_append_fp8(const cowa_pattern* pat, int B, int Hkv, int d, const void* k_new,
@@ -374,10 +366,8 @@ cowa_status cowa_compact_append_fp8(const cowa_pattern* pat, int B, int Hkv, int
   if (!k_new || !v_new || !pos || !k_compact || !v_compact) return COWA_ERR_INVALID_ARG;
   if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(k_compact) || !aligned16(v_compact))
     return COWA_ERR_ALIGNMENT;
-  return launch_compact_append(p, B, Hkv, 64, k_new, v_new, pos, k_compact, v_compact,
-                               reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
-             ? COWA_OK
-             : COWA_ERR_CUDA;
+  return status_of(launch_compact_append(p, B, Hkv, 64, k_new, v_new, pos, k_compact, v_compact,
+                               reinterpret_cast<cudaStream_t>(stream)));
 }
 
 size_t cowa_decode_fp8_compact_workspace_size(const cowa_pattern* pat, int B, int Hq, int Hkv, int d) {
@@ -418,16 +408,14 @@ cowa_status cowa_decode_fp8_compact(const cowa_pattern* pat, int B, int Hq, int 
   if (!make_tmap_u8(&a.tm_k, k_compact, d, (int)rows, Hkv, B, d, rows * d, (int64_t)Hkv * rows * d, 64) ||
       !make_tmap_u8(&a.tm_v, v_compact, d, (int)rows, Hkv, B, d, rows * d, (int64_t)Hkv * rows * d, 64))
     return COWA_ERR_CUDA;
-  return launch_decode(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? COWA_OK : COWA_ERR_CUDA;
+  return status_of(launch_decode(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 cowa_status cowa_quantize_e4m3(const void* x, void* codes, int64_t n, float scale, void* stream) {
   if (!x || !codes || n < 0 || n % 8 != 0 || !(scale > 0.f) || !isfinite(scale)) return COWA_ERR_INVALID_ARG;
   if (!aligned16(x) || (reinterpret_cast<uintptr_t>(codes) & 7u)) return COWA_ERR_ALIGNMENT;
   const float inv = 1.0f / scale;
-  return launch_quantize_e4m3(x, codes, n, inv, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
-             ? COWA_OK
-             : COWA_ERR_CUDA;
+  return status_of(launch_quantize_e4m3(x, codes, n, inv, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 // ------------------------------------------------------------------------------ forward
@@ -469,7 +457,7 @@ cowa_status cowa_fwd_chunk(const cowa_pattern* pat, int B, int N_q, int N_k, int
       !make_tmap_bf16(&a.tm_k, k.ptr, d, N_k, Hkv, B, k.stride_t, k.stride_h, k.stride_b, 128) ||
       !make_tmap_bf16(&a.tm_v, v.ptr, d, N_k, Hkv, B, v.stride_t, v.stride_h, v.stride_b, 128))
     return COWA_ERR_CUDA;
-  return launch_fwd(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? COWA_OK : COWA_ERR_CUDA;
+  return status_of(launch_fwd(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 size_t cowa_fwd_varlen_workspace_size(const cowa_pattern* pat, int n_seq, int total, int Hq, int Hkv, int d) {
@@ -506,7 +494,7 @@ cowa_status cowa_fwd_varlen(const cowa_pattern* pat, int n_seq, int total, int H
       !make_tmap_bf16(&a.tm_k, k.ptr, d, total, Hkv, 1, k.stride_t, k.stride_h, k.stride_b, 128) ||
       !make_tmap_bf16(&a.tm_v, v.ptr, d, total, Hkv, 1, v.stride_t, v.stride_h, v.stride_b, 128))
     return COWA_ERR_CUDA;
-  return launch_fwd(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? COWA_OK : COWA_ERR_CUDA;
+  return status_of(launch_fwd(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 // ------------------------------------------------------------------------------ backward
@@ -570,7 +558,7 @@ cowa_status cowa_bwd_stages(const cowa_pattern* pat, int B, int N, int Hq, int H
       !make_tmap_bf16(&a.tm_v, v.ptr, d, N, Hkv, B, v.stride_t, v.stride_h, v.stride_b, 128) ||
       !make_tmap_bf16(&a.tm_do, dO.ptr, d, N, Hq, B, dO.stride_t, dO.stride_h, dO.stride_b, 128))
     return COWA_ERR_CUDA;
-  return launch_bwd(a, stages, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? COWA_OK : COWA_ERR_CUDA;
+  return status_of(launch_bwd(a, stages, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 // ------------------------------------------------------------------------------ packed backward
@@ -663,9 +651,8 @@ cowa_status cowa_bwd_varlen(const cowa_pattern* pat, int n_seq, int total, int H
       !make_tmap_bf16(&a.tm_do, dO.ptr, d, total, Hq, 1, dO.stride_t, dO.stride_h, dO.stride_b, 128))
     return COWA_ERR_CUDA;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (launch_seq_table(cu_seqlens, n_seq, total, a.seq_tab, st) != cudaSuccess) return COWA_ERR_CUDA;
-  return launch_bwd(a, COWA_BWD_PREPROCESS | COWA_BWD_DKDV | COWA_BWD_DQ, st) == cudaSuccess ? COWA_OK
-                                                                                            : COWA_ERR_CUDA;
+  COWA_TRY(status_of(launch_seq_table(cu_seqlens, n_seq, total, a.seq_tab, st)));
+  return status_of(launch_bwd(a, COWA_BWD_PREPROCESS | COWA_BWD_DKDV | COWA_BWD_DQ, st));
 }
 
 // ------------------------------------------------------------------------------ rotary positions
@@ -724,7 +711,7 @@ cowa_status rope(const cowa_rotary* rot, bool transpose, int B, int N, int Hq, i
   a.k = in_ptr(k); a.k_sb = k.stride_b; a.k_st = k.stride_t; a.k_sh = k.stride_h;
   a.qo = out_ptr(qo); a.qo_sb = qo.stride_b; a.qo_st = qo.stride_t; a.qo_sh = qo.stride_h;
   a.ko = out_ptr(ko); a.ko_sb = ko.stride_b; a.ko_st = ko.stride_t; a.ko_sh = ko.stride_h;
-  return launch_rope(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? COWA_OK : COWA_ERR_CUDA;
+  return status_of(launch_rope(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 }  // namespace
 
@@ -794,7 +781,7 @@ cowa_status paged_append(const cowa_rotary* rot, int total, int n_seq, int Hq, i
   a.kp = kp.ptr; a.kp_sp = kp.stride_b; a.kp_st = kp.stride_t; a.kp_sh = kp.stride_h;
   a.vp = vp.ptr; a.vp_sp = vp.stride_b; a.vp_st = vp.stride_t; a.vp_sh = vp.stride_h;
   if (e4m3) { a.inv_k = 1.0f / k_scale; a.inv_v = 1.0f / v_scale; }
-  return launch_paged_append(a, e4m3, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? COWA_OK : COWA_ERR_CUDA;
+  return status_of(launch_paged_append(a, e4m3, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 size_t paged_workspace(const cowa_pattern* pat, int B, int Hq, int Hkv, int d, bool e4m3, int max_pages,
@@ -846,8 +833,7 @@ cowa_status decode_paged(const cowa_pattern* pat, int B, int Hq, int Hkv, int d,
   if (!map(&a.tm_k, kp.ptr, d, table.page_size, h, table.n_pages, kp.stride_t, kp.stride_h, kp.stride_b, a.box_rows) ||
       !map(&a.tm_v, vp.ptr, d, table.page_size, h, table.n_pages, vp.stride_t, vp.stride_h, vp.stride_b, a.box_rows))
     return COWA_ERR_CUDA;
-  return launch_paged_decode(a, d, e4m3, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? COWA_OK
-                                                                                                : COWA_ERR_CUDA;
+  return status_of(launch_paged_decode(a, d, e4m3, reinterpret_cast<cudaStream_t>(stream)));
 }
 }  // namespace
 
@@ -900,7 +886,7 @@ cowa_status cowa_fwd_paged(const cowa_pattern* pat, int n_seq, int total, int Hq
       !make_tmap_bf16(&a.tm_v, v_pages.ptr, d, table.page_size, h, table.n_pages, v_pages.stride_t, v_pages.stride_h,
                       v_pages.stride_b, a.box_rows))
     return COWA_ERR_CUDA;
-  return launch_fwd(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? COWA_OK : COWA_ERR_CUDA;
+  return status_of(launch_fwd(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 cowa_status cowa_pages_needed(const cowa_pattern* pat, int Hkv, int page_size, int n, int pos, uint8_t* out) {
@@ -1017,15 +1003,15 @@ cowa_status cowa_plan_debug(const cowa_pattern* pat, int Hkv, int N, int BM, int
     if (!dev_scratch) return COWA_ERR_INVALID_ARG;
     unsigned long long* dcount = reinterpret_cast<unsigned long long*>(dev_scratch);
     int32_t* drec = reinterpret_cast<int32_t*>(reinterpret_cast<char*>(dev_scratch) + 256);
-    if (cudaMemset(dcount, 0, sizeof(unsigned long long)) != cudaSuccess) return COWA_ERR_CUDA;
+    COWA_TRY(status_of(cudaMemset(dcount, 0, sizeof(unsigned long long))));
     const size_t dcap = cap;  // the first 256 bytes of dev_scratch hold the counter
-    if (launch_plan_debug(p, Hkv, N, BM, BN, drec, dcap, dcount, 0) != cudaSuccess) return COWA_ERR_CUDA;
-    if (cudaDeviceSynchronize() != cudaSuccess) return COWA_ERR_CUDA;
+    COWA_TRY(status_of(launch_plan_debug(p, Hkv, N, BM, BN, drec, dcap, dcount, 0)));
+    COWA_TRY(status_of(cudaDeviceSynchronize()));
     unsigned long long cnt = 0;
-    if (cudaMemcpy(&cnt, dcount, sizeof(cnt), cudaMemcpyDeviceToHost) != cudaSuccess) return COWA_ERR_CUDA;
+    COWA_TRY(status_of(cudaMemcpy(&cnt, dcount, sizeof(cnt), cudaMemcpyDeviceToHost)));
     n = (size_t)cnt;
     const size_t ncopy = n < dcap ? n : dcap;
-    if (ncopy && cudaMemcpy(out, drec, ncopy * 16, cudaMemcpyDeviceToHost) != cudaSuccess) return COWA_ERR_CUDA;
+    if (ncopy) COWA_TRY(status_of(cudaMemcpy(out, drec, ncopy * 16, cudaMemcpyDeviceToHost)));
     *n_written = n;
     return n > dcap ? COWA_ERR_WORKSPACE : COWA_OK;
   }

@@ -64,13 +64,13 @@ unsigned long long current_ctx_id() {
 // again only if that device's context has changed since).
 cowa_status scratch_on_current_device(void** out) {
   int dev = -1;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return COWA_ERR_CUDA;
+  if (status_of(cudaGetDevice(&dev)) != COWA_OK || dev < 0 || dev >= kMaxDevices) return COWA_ERR_CUDA;
   std::lock_guard<std::mutex> lock(g_scratch_mu);
   ScratchAddr& e = g_scratch_addr[dev];
   unsigned long long id = current_ctx_id();
   if (e.ptr == nullptr || id == 0 || id != e.ctx_id) {
     void* p = nullptr;
-    if (cudaGetSymbolAddress(&p, g_decode_scratch) != cudaSuccess || p == nullptr) return COWA_ERR_CUDA;
+    if (status_of(cudaGetSymbolAddress(&p, g_decode_scratch)) != COWA_OK || p == nullptr) return COWA_ERR_CUDA;
     if (id == 0) id = current_ctx_id();  // the lookup made the device's primary context current
     e.ptr = p;
     e.ctx_id = id;
@@ -97,7 +97,7 @@ extern "C" cowa_status cowa_decode_noalloc(const cowa_pattern* pat, int B, int H
   const cowa_status st = cowa::scratch_on_current_device(&scratch);
   if (st != COWA_OK) return st;
   // the status word must start at zero; the split partials are fully rewritten by every call
-  if (cudaMemsetAsync(scratch, 0, cowa::kWsHeader, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+  if (cowa::status_of(cudaMemsetAsync(scratch, 0, cowa::kWsHeader, reinterpret_cast<cudaStream_t>(stream))) != COWA_OK)
     return COWA_ERR_CUDA;
   return cowa_decode(pat, B, H_q, H_kv, d, T_cap, q_t, k_cache, v_cache, pos, o, lse_or_null, scratch,
                      COWA_DECODE_NOALLOC_SCRATCH_BYTES, stream);

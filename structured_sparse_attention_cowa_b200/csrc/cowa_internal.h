@@ -19,6 +19,14 @@ constexpr size_t kWsHeader = 256;
 // calls never needed that word cleared, and it may hold anything in their workspaces.)
 constexpr uint32_t kPageFlag = 0x50414745u;
 
+// A runtime call's result as a status.  A failed call is also kept as the thread's last error, which the check
+// after the next launch would take for its own: it is cleared.
+inline cowa_status status_of(cudaError_t e) {
+  if (e == cudaSuccess) return COWA_OK;
+  cudaGetLastError();
+  return COWA_ERR_CUDA;
+}
+
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // Encode a 4-D bf16 tensor map over (d, t, h, b) with a box of (64, box_rows, 1, 1)
