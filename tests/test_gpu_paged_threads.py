@@ -5,6 +5,7 @@ of a C program (tests/c_abi/concurrent_decodes.c): Python's take turns at the in
 
 import ctypes
 import os
+import shutil
 import subprocess
 
 import pytest
@@ -25,6 +26,8 @@ class Job(ctypes.Structure):
 
 @pytest.fixture(scope="module")
 def run_jobs(tmp_path_factory):
+    if shutil.which("gcc") is None:
+        pytest.skip("gcc not available")
     so = str(tmp_path_factory.mktemp("threads") / "concurrent_decodes.so")
     subprocess.run(["gcc", "-std=c99", "-Wall", "-Wextra", "-Werror", "-pthread", "-shared", "-fPIC", "-I",
                     os.path.join(ROOT, "include"), os.path.join(ROOT, "tests", "c_abi", "concurrent_decodes.c"), "-o", so],
