@@ -316,3 +316,56 @@ def test_paged_calls_side_by_side(cuda_device, e4m3):
         assert cw.workspace_status(s["ws"]) == 0
         for a, b in zip((*g, *s["pools"]), w):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("per_head", [False, True])
+@pytest.mark.parametrize("Hkv,T", [(1, 0), (2, 2**30)])
+def test_the_last_positions_of_the_largest_capacity(cuda_device, per_head, Hkv, T):
+    """2^30 positions in pages of 8: append, decode and a chunk at the end, the sinks and the band mapped (and, with
+    an interval of 2^29 positions for each head, nothing of it: left out and reported)."""
+    ps, n, d, Hq, S, L = 8, 1 << 27, 64, 4, 10, 100
+    cap, pat = ps * n, cw.Pattern(S, L, max(S, T), Hkv)
+    last = cap - 1
+    near = np.arange(last - L - 60, cap)  # positions that the rows see through the band, and some
+    pages_at = np.unique(np.r_[np.arange(S), near] // ps)
+    shape = (1, Hkv, n) if per_head else (1, n)
+    tab = torch.full(shape, -1, dtype=torch.int32, device=cuda_device)
+    heads = Hkv if per_head else 1
+    ids = np.random.default_rng(160).permutation(len(pages_at) * heads + 3)[:len(pages_at) * heads].reshape(heads, -1)
+    where = torch.from_numpy(pages_at).to(cuda_device)
+    for g in range(heads):
+        (tab[0, g] if per_head else tab[0])[where] = torch.from_numpy(ids[g].astype(np.int32)).to(cuda_device)
+    kp, vp = (torch.full((len(pages_at) * heads + 3, ps, 1 if per_head else Hkv, d), float("nan"), dtype=torch.bfloat16,
+                         device=cuda_device) for _ in range(2))
+    rows = (pages_at[:, None] * ps + np.arange(ps)).reshape(-1)  # every position of the mapped pages
+    edge = [S + i * (max(S, T) - S) // Hkv for i in range(Hkv + 1)]
+    (k64, k), (v64, v) = (host_and_device((len(rows), Hkv, d), x, cuda_device, 160) for x in ("k", "v"))
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=cuda_device)
+    cw.paged_append(None, k, v, i32(rows.tolist()), kp, vp, tab, seq=i32([0] * len(rows)))
+    q64, q = host_and_device((50, Hq, d), "q", cuda_device, 160)
+    ws = torch.zeros(1 << 24, dtype=torch.uint8, device=cuda_device)
+
+    def want(t, row):
+        out = []
+        for h in range(Hq):
+            g = h * Hkv // Hq
+            see = (rows <= t) & ((rows < S) | (rows > t - L) | ((rows >= edge[g]) & (rows < edge[g + 1])))
+            s = k64[see, g] @ q64[row, h] / np.sqrt(d)
+            p = np.exp(s - s.max())
+            out.append((p @ v64[see, g] / p.sum(), p @ np.abs(v64[see, g]) / p.sum(), s.max() + np.log(p.sum())))
+        return [np.array(x) for x in zip(*out)]
+
+    def check(o, lse, t, row):
+        w, A, wl = want(t, row)
+        assert (np.abs(to64(o) - w) <= 2.0 ** -8 * (A + np.abs(w)) + 2.0 ** -12 * A).all()
+        assert np.abs(lse.double().cpu().numpy() - wl).max() <= tp.LSE_TOL
+
+    for pos in (last, last - 3, 2**31 - 1):
+        o, lse = cw.cowa_decode_paged(q[:1], kp, vp, tab, i32([pos]), pat, workspace=ws)
+        assert cw.workspace_status(ws) == (8 if T else 0)
+        check(o[0], lse[0], min(pos, last), 0)
+    if T == 0:
+        o, lse = cw.cowa_fwd_paged(q, kp, vp, tab, i32([0, 50]), i32([cap - 50]), pat, workspace=ws)
+        assert cw.workspace_status(ws) == 0
+        for row in range(50):
+            check(o[row], lse[:, row], cap - 50 + row, row)
