@@ -83,12 +83,14 @@ void same_device(const at::Tensor& x, std::initializer_list<const at::Tensor*> o
     if (y && y->device() != x.device())
       bad_value("tensors are on different devices: " + x.device().str() + " and " + y->device().str());
 }
+// The stride of dimension i; that of a dimension of one element, which may be anything, as d: the library wants
+// every stride to be a positive multiple of 16 bytes
+int64_t stride(const at::Tensor& t, int i) { return t.size(i) > 1 ? t.stride(i) : t.size(-1); }
 // [B, N, H, d] or packed [total, H, d] (d contiguous) as a cowa_tensor
 cowa_tensor rows(const at::Tensor& t, const char* name) {
-  const auto s = t.strides();
-  if (s.back() != 1) bad_value(std::string("the last dimension of ") + name + " must be contiguous");
-  if (t.dim() == 3) return {t.data_ptr(), s[0] * std::max<int64_t>(1, t.size(0)), s[0], s[1]};
-  return {t.data_ptr(), s[0], s[1], s[2]};
+  if (t.stride(-1) != 1) bad_value(std::string("the last dimension of ") + name + " must be contiguous");
+  if (t.dim() == 3) return {t.data_ptr(), stride(t, 0) * std::max<int64_t>(1, t.size(0)), stride(t, 0), stride(t, 1)};
+  return {t.data_ptr(), stride(t, 0), stride(t, 1), stride(t, 2)};
 }
 int to_int(int64_t v) {
   if (v > 0x7fffffff) bad_value("a dimension is larger than 2^31 - 1");
@@ -119,11 +121,11 @@ Pages pages(const at::Tensor& k, const at::Tensor& v, const at::Tensor& table, P
   if (dims == 3 && k.size(h) != 1) bad_value("with a page table per KV head a page holds one head");
   if (k.stride(3) != 1 || v.stride(3) != 1) bad_value("the last dimension of the pools must be contiguous");
   Pages p;
-  p.k = {k.data_ptr(), k.stride(0), k.stride(t), k.stride(h)};
-  p.v = {v.data_ptr(), v.stride(0), v.stride(t), v.stride(h)};
+  p.k = {k.data_ptr(), stride(k, 0), stride(k, t), stride(k, h)};
+  p.v = {v.data_ptr(), stride(v, 0), stride(v, t), stride(v, h)};
   p.Hkv = to_int(dims == 3 ? table.size(1) : k.size(h));
   p.n_seq = to_int(table.size(0));
-  p.table = {static_cast<const int32_t*>(table.data_ptr()), table.stride(0), dims == 3 ? table.stride(1) : 0,
+  p.table = {static_cast<const int32_t*>(table.data_ptr()), stride(table, 0), dims == 3 ? stride(table, 1) : 0,
              to_int(table.size(-1)), to_int(k.size(t)), to_int(k.size(0)), dims == 3};
   return p;
 }

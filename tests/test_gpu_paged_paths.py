@@ -369,3 +369,33 @@ def test_the_last_positions_of_the_largest_capacity(cuda_device, per_head, Hkv, 
         assert cw.workspace_status(ws) == 0
         for row in range(50):
             check(o[row], lse[:, row], cap - 50 + row, row)
+
+
+@pytest.mark.parametrize("odd", [0, 1, 7])
+def test_strides_of_dimensions_of_one_element(cuda_device, odd):
+    """What a tensor says of the stride of a dimension with a single element means nothing (another framework's
+    tensor, or a view, may say anything): the same bits as with the usual strides."""
+    def as_odd(x):
+        return x.as_strided(x.shape, [s if n > 1 else odd for s, n in zip(x.stride(), x.shape[:-1])] + [1])
+
+    d, ps, n = 64, 16, 1
+    rand = lambda s, nm: synth.cuda_normal_bf16(s, synth.seed_of(nm, 161), cuda_device)
+    rope, pat = cw.Rope(cw.rope_frequencies(d, device=cuda_device)), cw.Pattern(2, 9, 16, 1)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=cuda_device)
+    one, cu, start = i32([5]), i32([0, 1]), i32([5])
+    for layout, per_head in (("bthd", False), ("bhtd", True)):
+        x4, q, k = rand((1, 1, 1, d), "q"), rand((1, 1, d), "q"), rand((1, 1, d), "k")
+        pool = rand((1, ps, 1, d) if layout == "bthd" else (1, 1, ps, d), "v")
+        tab = torch.zeros((1, 1, n) if per_head else (1, n), dtype=torch.int32, device=cuda_device)
+
+        def run(f):
+            kp, vp = pool.clone(), pool.clone()
+            fk, fv, ft = f(kp), f(vp), tab if f is not as_odd else tab.as_strided(tab.shape, [odd] * (tab.dim() - 1) + [1])
+            out = [*cw.cowa_rope(f(x4), f(x4), rope, i32([[3]])), *cw.cowa_rope_bwd(f(x4), None, rope, i32([[3]]))[:1]]
+            out.append(cw.paged_append(f(q), f(k), f(k), one, fk, fv, ft, rope=rope, layout=layout))
+            out += cw.cowa_decode_paged(q, fk, fv, ft, one, pat, layout=layout)
+            out += cw.cowa_fwd_paged(f(q), fk, fv, ft, cu, start, pat, layout=layout, out=f(torch.zeros_like(q)))
+            return [*out, kp, vp]
+
+        for a, b in zip(run(as_odd), run(lambda x: x)):
+            assert torch.equal(a, b)
